@@ -229,6 +229,10 @@ def prepare(case, seed):
         rows = torch.randn((tokens, q + 2 * heads * d), generator=g, device="cuda").to(dtype)
         s["new_k"] = rows[:, q:q + heads * d].unflatten(1, (heads, d))
         s["new_v"] = rows[:, q + heads * d:].unflatten(1, (heads, d))
+        if own:  # the cache's handle, which a program keeps as long as the cache
+            import shape_driven_tile_gb300 as sdt
+
+            s["handle"] = sdt.PagedCache(s["k"], s["v"], s.get("ks"), s.get("vs"))
         return s
     lens = _attn_lens(case)
     s["lens"] = torch.tensor(lens, dtype=torch.int32, device="cuda")[_order(len(lens), g)]
@@ -239,9 +243,10 @@ def prepare(case, seed):
     s["table"][torch.arange(wide, device="cuda")[None] < held[:, None]] = ids[:total]
     s.update(_cache(case, total + 5, g))
     s["q"] = torch.randn((case["batch"], case["q_heads"], d), generator=g, device="cuda").to(dtype)
-    if own:  # the workspace that a program keeps for all its steps
+    if own:  # the cache's handle and the workspace that a program keeps for all its steps
         import shape_driven_tile_gb300 as sdt
 
+        s["handle"] = sdt.PagedCache(s["k"], s["v"], s.get("ks"), s.get("vs"))
         s["workspace"] = sdt.paged_attn_workspace(case["q_heads"], heads, d)
     return s
 
@@ -257,10 +262,10 @@ def _run_own(s):
                                                         slots=s["slots"])
         return dict(table=s["table"], kv_lens=kv_lens, starts=starts, slots=slots, used=used)
     if s["op"] == "append":
-        sdt.paged_append(s["new_k"], s["new_v"], s["slots"], s["k"], s["v"], k_scales=s.get("ks"), v_scales=s.get("vs"))
+        sdt.paged_append(s["new_k"], s["new_v"], s["slots"], s["handle"])
         return _held(s)
-    return sdt.paged_attn_m1(s["q"], s["k"], s["v"], s["table"], s["lens"], k_scales=s.get("ks"), v_scales=s.get("vs"),
-                             window=s["case"]["window"], workspace=s["workspace"])
+    return sdt.paged_attn_m1(s["q"], s["handle"], s["table"], s["lens"], window=s["case"]["window"],
+                             workspace=s["workspace"])
 
 
 def _held(s):
