@@ -1,12 +1,15 @@
 /*
  * sdt.h -- C ABI of the shape-driven-tile library (libsdt.so) for GB300 (sm_103a).
  *
- * Two compute calls and the tile-selection calls around them:
+ * Two products with the tile-selection calls around them, and the attention of a decode
+ * step between them:
  *
  *   gemm_f16   C = A . B, fp16 in, fp32 accumulate, fp16 out, with the CTA tile
  *              chosen from the problem shape.
  *   gemv_m1    y = W . x for a single activation row (M = 1 decode), streaming a
  *              K-major weight matrix, bf16 or q8 (int8 + one fp16 scale per 32).
+ *   paged_attn_m1  attention of one new token per request over a paged key-value
+ *              cache (paged_tables, paged_append around it).
  *
  * Conventions for every call in this header:
  *  - Pointers named A, B, C, x, W, scales, y are DEVICE pointers owned by the
@@ -448,6 +451,93 @@ int sdt_tune_table_size(void);
 int sdt_tune_table_lookup(int64_t M, int64_t N, int64_t K);
 
 /* ------------------------------------------------------------------------ */
+/* Paged key-value cache: one decode step's attention                        */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * A cache of num_pages pages of page_size tokens.  Token t of page p holds, for each of
+ * kv_heads heads, head_dim contiguous keys and values, at element
+ * p * k_page + t * k_token + h * k_head of k (v likewise), so pages may lie token by token
+ * or head by head.  dtype SDT_DTYPE_F16 or SDT_DTYPE_BF16: 16-bit elements, head_dim a
+ * multiple of 8 up to 256, base and strides multiples of 16 bytes.  SDT_DTYPE_Q8: int8
+ * elements with one fp16 scale per 32 (element e of a head is q[e] * scale[e / 32], as in
+ * gemv_m1_q8); head_dim a multiple of 64 up to 256; the scales have strides of their own,
+ * head_dim / 32 contiguous, base and strides multiples of 4 bytes.
+ * num_pages * page_size < 2^31; element offsets may exceed 32 bits.
+ */
+#define SDT_DTYPE_Q8 2
+typedef struct sdt_paged_cache {
+    void *k, *v;
+    void *k_scales, *v_scales; /* NULL unless q8 */
+    int64_t num_pages, page_size, kv_heads, head_dim;
+    int64_t k_page, k_token, k_head; /* strides in elements */
+    int64_t v_page, v_token, v_head;
+    int64_t ks_page, ks_token, ks_head;
+    int64_t vs_page, vs_token, vs_head;
+    int dtype;
+} sdt_paged_cache;
+
+/*
+ * paged_tables -- block tables and slot maps of a step, from the requests' lengths.
+ * Request b of `batch` (1 .. 16384) holds lens[b] tokens and adds new_tokens[b] (0 or
+ * more).  Its row table + b * table_stride holds its ceil(lens[b] / page_size) pages; the
+ * call appends the pages that the new tokens need, taken in request order from the front
+ * of free_pages, and leaves every other entry as it is.  Written besides: kv_lens[b] =
+ * lens[b] + new_tokens[b]; starts[0 .. batch], the exclusive prefix sums of new_tokens;
+ * slots[starts[b] + i] = page * page_size + offset of request b's i-th new token, and -1
+ * for entries from starts[batch] to num_slots; used[0], the number of pages taken.
+ * A table entry or slot for which free_pages has no page is -1 (used[0] > num_free then
+ * says how many were needed), and so is a slot past max_pages; tokens past num_slots get
+ * no slot.  The same call on the same inputs writes the same values.
+ * Negative lengths count as 0, lengths past max_pages * page_size as that; the sum of
+ * new_tokens must be below 2^31.
+ */
+int paged_tables(int64_t batch, int64_t page_size, int64_t max_pages, const int32_t *lens,
+                 const int32_t *new_tokens, const int32_t *free_pages, int64_t num_free, int32_t *table,
+                 int64_t table_stride, int32_t *kv_lens, int32_t *starts, int64_t *slots, int64_t num_slots,
+                 int32_t *used, sdt_stream_t stream);
+
+/*
+ * paged_append -- the keys and values of `tokens` tokens into the cache at their slots
+ * (slot = page * page_size + offset).  k and v: fp16 or bf16 (dtype; a 16-bit cache's own
+ * type), head h of token t at t * k_token + h * k_head elements, head_dim contiguous;
+ * bases 16-byte aligned, strides multiples of 8.  A negative slot's token is left out.  A
+ * slot past the cache is left out too and reported by sdt_check_device_status.  Of two
+ * tokens with one slot either may stay.  q8: scale = fp16(max|x| * fl32(1/127)), at most
+ * 65504, q = x / scale rounded to the nearest integer (ties to even) within +-127, 0 where
+ * the scale is 0 or x is NaN.
+ */
+int paged_append(int64_t tokens, const void *k, int64_t k_token, int64_t k_head, const void *v, int64_t v_token,
+                 int64_t v_head, int dtype, const int64_t *slots, const sdt_paged_cache *cache,
+                 sdt_stream_t stream);
+
+/*
+ * paged_attn_m1 -- attention of one new token per request:
+ *   out[b][i] = sum_n softmax_n(scale * q[b][i] . k[n][h]) v[n][h],  h = i / (q_heads / kv_heads),
+ * over the tokens n of request b that its table row names: max(0, lens[b] - window) <= n <
+ * lens[b] with window > 0, all lens[b] with window == 0.  q, out: [batch][q_heads][head_dim]
+ * fp16 or bf16 (dtype; a 16-bit cache's own type) with strides in elements (q even and
+ * 4-byte aligned, out multiples of 4 and 8-byte aligned).  lse, if not NULL, gets
+ * log(sum exp(scores)) as fp32 [batch][q_heads].  A request without keys, or whose scores
+ * are all -inf, gets zeros and lse -inf.  What lies in the cache outside the named tokens
+ * is not read.  A page id outside the cache, or a length past max_pages * page_size, is not
+ * followed and is reported by sdt_check_device_status.  Results do not depend on the order
+ * in which the CTAs run.
+ *
+ * Workspace: device memory owned by the caller, 256-byte aligned, at least
+ * sdt_paged_attn_workspace_bytes() bytes: the 1 MiB counter region of the split-K
+ * workspaces (zero before the first call, left zero by every completed call; it may be
+ * shared with those), then the pieces of requests that are split over CTAs.  Calls that
+ * share a workspace must not overlap on the GPU.
+ */
+int paged_attn_m1(int64_t batch, int64_t q_heads, const void *q, int64_t q_batch, int64_t q_head, int dtype,
+                  const sdt_paged_cache *cache, const int32_t *table, int64_t table_stride, int64_t max_pages,
+                  const int32_t *lens, int64_t window, float scale, void *out, int64_t out_batch, int64_t out_head,
+                  float *lse, void *workspace, size_t workspace_bytes, sdt_stream_t stream);
+/* Workspace bytes of paged_attn_m1 on the current device, for any batch and lengths (0 on error). */
+size_t sdt_paged_attn_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t head_dim);
+
+/* ------------------------------------------------------------------------ */
 /* Diagnostics                                                               */
 /* ------------------------------------------------------------------------ */
 
@@ -461,7 +551,9 @@ const char *sdt_last_error(void);
  * the current device, and returns SDT_OK or SDT_ERR_TIMEOUT (SDT_ERR_CUDA if
  * the stream itself reports an error).  `where` (may be NULL) receives the
  * recorded code: its low 4 bits are the site (1 producer, 2 MMA issuer,
- * 3 epilogue, 4 drain, 5 probe); the two-CTA kernels add the CTA's rank in the
+ * 3 epilogue, 4 drain, 5 probe); 8, 9 and 10 stand for a page id, slot or length outside
+ * the cache or table that a paged operator met and left out (SDT_ERR_ARG is returned
+ * then); the two-CTA kernels add the CTA's rank in the
  * pair at bit 4 and the loop position from bit 8.
  */
 int sdt_check_device_status(sdt_stream_t stream, int *where);

@@ -1,4 +1,4 @@
-"""Shape-driven fp16 GEMM and M=1 decode GEMV for GB300 (sm_103a).
+"""Shape-driven fp16 GEMM, M=1 decode GEMV and paged decode attention for GB300 (sm_103a).
 
 Thin binding over libsdt.so (C ABI in include/sdt.h): the functions below only
 check and marshal arguments (tensor pointers, shapes, the current CUDA stream)
@@ -12,6 +12,7 @@ import ctypes
 import torch
 
 from ._lib import SdtError, check, lib, sdt_tile_desc
+from .paged import PagedCache, paged_append, paged_attn_m1, paged_attn_workspace, paged_tables
 
 __all__ = [
     "SdtError", "gemm_f16", "gemm_f16_with_tile", "gemv_m1", "gemv_m1_bf16", "gemv_m1_q8",
@@ -22,6 +23,7 @@ __all__ = [
     "splitk_ex_workspace_bytes", "pick_splitk_any", "SPLITK_REDUCE_KERNEL", "SPLITK_IN_KERNEL", "gemm_ex",
     "SPLITK_STREAM", "SPLITK_STREAM_REDUCE", "streamk_ctas", "streamk_workspace_bytes",
     "gemm_f16_ws", "gemm_ex_ws", "gemm_workspace_bytes", "gemm_workspace", "pair_tail_plan",
+    "PagedCache", "paged_tables", "paged_append", "paged_attn_m1", "paged_attn_workspace",
 ]
 
 

@@ -24,6 +24,16 @@ class sdt_tile_desc(ctypes.Structure):
     ]
 
 
+class sdt_paged_cache(ctypes.Structure):
+    _fields_ = [
+        ("k", vp), ("v", vp), ("k_scales", vp), ("v_scales", vp),
+        ("num_pages", i64), ("page_size", i64), ("kv_heads", i64), ("head_dim", i64),
+        ("k_page", i64), ("k_token", i64), ("k_head", i64), ("v_page", i64), ("v_token", i64), ("v_head", i64),
+        ("ks_page", i64), ("ks_token", i64), ("ks_head", i64), ("vs_page", i64), ("vs_token", i64), ("vs_head", i64),
+        ("dtype", cint),
+    ]
+
+
 # name -> (restype, argtypes); every symbol include/sdt.h declares.
 SIGNATURES = {
     "gemm_f16": (cint, [i64, i64, i64, vp, vp, vp, vp]),
@@ -72,6 +82,11 @@ SIGNATURES = {
     "sdt_gemm_workspace_bytes_for": (ctypes.c_size_t, [cint]),
     "sdt_pair_tail_plan": (cint, [i64, i64, i64, cint, cint, cint, cint, cint, ctypes.POINTER(cint),
                                   ctypes.POINTER(cint), ctypes.POINTER(cint), ctypes.POINTER(cint)]),
+    "paged_tables": (cint, [i64, i64, i64, vp, vp, vp, i64, vp, i64, vp, vp, vp, i64, vp, vp]),
+    "paged_append": (cint, [i64, vp, i64, i64, vp, i64, i64, cint, vp, ctypes.POINTER(sdt_paged_cache), vp]),
+    "paged_attn_m1": (cint, [i64, i64, vp, i64, i64, cint, ctypes.POINTER(sdt_paged_cache), vp, i64, i64, vp, i64,
+                             ctypes.c_float, vp, i64, i64, vp, vp, ctypes.c_size_t, vp]),
+    "sdt_paged_attn_workspace_bytes": (ctypes.c_size_t, [i64, i64, i64]),
 }
 
 STATUS = {

@@ -8,6 +8,7 @@
 #include <string>
 
 #include "host_common.cuh"
+#include "paged.cuh"
 #include "ptx.cuh"
 
 namespace sdt {
@@ -159,6 +160,9 @@ int sdt_check_device_status(sdt_stream_t stream, int *where) {
             return fail(SDT_ERR_CUDA, "clearing the device status failed: %s", cudaGetErrorString(e));
         }
         if (where) *where = host;
+        if ((host & 15) == kSitePage) return fail(SDT_ERR_ARG, "a block table named a page outside the cache");
+        if ((host & 15) == kSiteSlot) return fail(SDT_ERR_ARG, "a slot lay outside the cache");
+        if ((host & 15) == kSiteLength) return fail(SDT_ERR_ARG, "a request's length passed its block table");
         return fail(SDT_ERR_TIMEOUT, "a kernel gave up a bounded wait (site %d)", host);
     }
     return SDT_OK;

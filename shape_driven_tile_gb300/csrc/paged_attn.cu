@@ -1,0 +1,99 @@
+// paged_attn.cu -- paged_attn_m1: argument checks and dispatch of the paged attention kernel.
+#include "paged_attn.cuh"
+#include "paged_attn_plan.cuh"
+
+using namespace sdt;
+
+static constexpr size_t kCounterBytes = size_t(1) << 20;  // the counter region of the split-K workspaces
+static constexpr int64_t kMaxTokens = INT32_MAX - 1024;   // a row's tokens; key indices run past them by a unit at most
+
+extern "C" {
+
+size_t sdt_paged_attn_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
+    DeviceInfo dev;
+    if (kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads || head_dim < 8 || head_dim > kPagedMaxHeadDim) {
+        fail(SDT_ERR_SHAPE, "sdt_paged_attn_workspace_bytes: bad sizes");
+        return 0;
+    }
+    if (current_device(&dev)) return 0;
+    const size_t rows = 16 * static_cast<size_t>(paged_attn_wh(q_heads / kv_heads));
+    const size_t slot = rows * (paged_attn_width(head_dim) + 2) * sizeof(float);
+    return kCounterBytes + 2 * 2 * static_cast<size_t>(dev.sm_count) * slot;  // two pieces a CTA, at most two CTAs an SM
+}
+
+int paged_attn_m1(int64_t batch, int64_t q_heads, const void *q, int64_t q_batch, int64_t q_head, int dtype,
+                  const sdt_paged_cache *cache, const int32_t *table, int64_t table_stride, int64_t max_pages,
+                  const int32_t *lens, int64_t window, float scale, void *out, int64_t out_batch, int64_t out_head,
+                  float *lse, void *workspace, size_t workspace_bytes, sdt_stream_t stream) {
+    clear_error();
+    int rc = check_cache(cache);
+    if (rc) return rc;
+    if (dtype != SDT_DTYPE_F16 && dtype != SDT_DTYPE_BF16) return fail(SDT_ERR_ARG, "paged_attn_m1: dtype must be fp16 or bf16 (got %d)", dtype);
+    const bool q8 = cache->dtype == SDT_DTYPE_Q8;
+    if (!q8 && cache->dtype != dtype) return fail(SDT_ERR_ARG, "paged_attn_m1: a 16-bit cache takes queries of its own type");
+    const int64_t kvh = cache->kv_heads;
+    if (batch < 0 || batch > (1 << 20) || q_heads < kvh || q_heads % kvh || q_heads > 65536)
+        return fail(SDT_ERR_SHAPE, "paged_attn_m1: batch in 0 .. 2^20, q_heads a multiple of the cache's %lld heads up to 65536 (got %lld, %lld)",
+                    (long long)kvh, (long long)batch, (long long)q_heads);
+    if (max_pages < 0 || (max_pages && cache->page_size > kMaxTokens / max_pages))
+        return fail(SDT_ERR_SHAPE, "paged_attn_m1: a table row must hold 0 .. %lld tokens", (long long)kMaxTokens);
+    if (table_stride < max_pages) return fail(SDT_ERR_ARG, "paged_attn_m1: table rows of %lld entries, %lld apart", (long long)max_pages, (long long)table_stride);
+    if (window < 0) return fail(SDT_ERR_ARG, "paged_attn_m1: window must be >= 0 (got %lld)", (long long)window);
+    if (batch == 0) return SDT_OK;
+    if (!q || !out || !lens || !workspace || (max_pages && !table)) return fail(SDT_ERR_NULL, "paged_attn_m1: NULL pointer");
+    if (!aligned(q, 4) || !aligned(out, 8) || !aligned(lens, 4) || !aligned(table, 4) || !aligned(lse, 4) || !aligned(workspace, 256))
+        return fail(SDT_ERR_ALIGN, "paged_attn_m1: q must be 4-byte, out 8-byte, lens, table and lse 4-byte, workspace 256-byte aligned");
+    if (q_batch % 2 || q_head % 2 || out_batch % 4 || out_head % 4)
+        return fail(SDT_ERR_ARG, "paged_attn_m1: strides of q must be even, of out multiples of 4 elements");
+    DeviceInfo dev;
+    rc = current_device(&dev);
+    if (rc) return rc;
+    const size_t need = sdt_paged_attn_workspace_bytes(q_heads, kvh, cache->head_dim);
+    if (workspace_bytes < need) return fail(SDT_ERR_ARG, "paged_attn_m1: workspace of %zu bytes, %zu needed", workspace_bytes, need);
+    int *status = nullptr;
+    rc = status_word(&status);
+    if (rc) return rc;
+
+    const int64_t cap = max_pages * cache->page_size;
+    PagedAttnLaunch l{paged_attn_wh(q_heads / kvh), q8, dev.sm_count, window > 0 && window < cap ? window : cap,
+                      reinterpret_cast<cudaStream_t>(stream)};
+    PagedAttnArgs a{};
+    a.q = static_cast<const char *>(q);
+    a.out = static_cast<char *>(out);
+    a.lse = lse;
+    a.q_batch = q_batch * 2;
+    a.q_head = q_head * 2;
+    a.o_batch = out_batch * 2;
+    a.o_head = out_head * 2;
+    a.k = rows_k(*cache);
+    a.v = rows_v(*cache);
+    a.ks = rows_ks(*cache);
+    a.vs = rows_vs(*cache);
+    a.table = table;
+    a.table_stride = table_stride;
+    a.lens = lens;
+    a.batch = static_cast<int>(batch);
+    a.kv_heads = static_cast<int>(kvh);
+    a.group = static_cast<int>(q_heads / kvh);
+    a.head_blocks = (a.group + 16 * l.wh - 1) / (16 * l.wh);
+    a.head_dim = static_cast<int>(cache->head_dim);
+    a.max_pages = static_cast<int>(max_pages);
+    a.num_pages = static_cast<int>(cache->num_pages);
+    a.window = window < INT32_MAX ? static_cast<int>(window) : 0;  // longer than any row: no window
+    a.page = FastDiv::of(static_cast<uint32_t>(cache->page_size));
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.counters = static_cast<unsigned *>(workspace);
+    a.partials = reinterpret_cast<float *>(static_cast<char *>(workspace) + kCounterBytes);
+    a.status = status;
+    const int dp = paged_attn_width(a.head_dim);
+    cudaError_t e;
+    if (dtype == SDT_DTYPE_F16)
+        e = dp == 64 ? launch_paged_attn<__half, 64>(a, l) : dp == 128 ? launch_paged_attn<__half, 128>(a, l) : launch_paged_attn<__half, 256>(a, l);
+    else
+        e = dp == 64 ? launch_paged_attn<__nv_bfloat16, 64>(a, l)
+                     : dp == 128 ? launch_paged_attn<__nv_bfloat16, 128>(a, l) : launch_paged_attn<__nv_bfloat16, 256>(a, l);
+    if (e != cudaSuccess) return fail(SDT_ERR_LAUNCH, "paged_attn_m1 launch failed: %s", cudaGetErrorString(e));
+    return SDT_OK;
+}
+
+}  // extern "C"
