@@ -516,8 +516,8 @@ int paged_append(int64_t tokens, const void *k, int64_t k_token, int64_t k_head,
  *   out[b][i] = sum_n softmax_n(scale * q[b][i] . k[n][h]) v[n][h],  h = i / (q_heads / kv_heads),
  * over the tokens n of request b that its table row names: max(0, lens[b] - window) <= n <
  * lens[b] with window > 0, all lens[b] with window == 0.  q, out: [batch][q_heads][head_dim]
- * fp16 or bf16 (dtype; a 16-bit cache's own type) with strides in elements (q even and
- * 4-byte aligned, out multiples of 4 and 8-byte aligned).  lse, if not NULL, gets
+ * fp16 or bf16 (dtype; a 16-bit cache's own type) with strides in elements (q multiples of
+ * 8 and 16-byte aligned, out multiples of 4 and 8-byte aligned).  lse, if not NULL, gets
  * log(sum exp(scores)) as fp32 [batch][q_heads].  A request without keys, or whose scores
  * are all -inf, gets zeros and lse -inf.  What lies in the cache outside the named tokens
  * is not read.  A page id outside the cache, or a length past max_pages * page_size, is not

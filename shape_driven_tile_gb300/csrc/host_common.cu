@@ -30,7 +30,6 @@ void clear_error() { t_last_error.clear(); }
 // The status word: first bounded wait that gives up writes its site code here.
 __device__ int g_sdt_status = 0;
 
-static constexpr int kMaxDevices = 64;
 static std::mutex g_dev_mu;
 static DeviceInfo g_dev[kMaxDevices];
 static bool g_dev_ok[kMaxDevices];

@@ -14,6 +14,8 @@ namespace sdt {
 int fail(int code, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
 void clear_error();
 
+constexpr int kMaxDevices = 64;  // device ordinals that the per-device caches hold
+
 struct DeviceInfo {
     int device = -1;
     int sm_count = 0;

@@ -1,4 +1,6 @@
 // paged_attn.cu -- paged_attn_m1: argument checks and dispatch of the paged attention kernel.
+#include <algorithm>
+
 #include "paged_attn.cuh"
 #include "paged_attn_plan.cuh"
 
@@ -16,9 +18,13 @@ size_t sdt_paged_attn_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t
         return 0;
     }
     if (current_device(&dev)) return 0;
-    const size_t rows = 16 * static_cast<size_t>(paged_attn_wh(q_heads / kv_heads));
-    const size_t slot = rows * (paged_attn_width(head_dim) + 2) * sizeof(float);
-    return kCounterBytes + 2 * 2 * static_cast<size_t>(dev.sm_count) * slot;  // two pieces a CTA, at most two CTAs an SM
+    size_t most = 0;  // of the variants that the sizes may take with any batch
+    for (int64_t items : {int64_t(1), INT64_MAX}) {
+        const PagedAttnVariant v = paged_attn_variant(q_heads / kv_heads, items, dev.sm_count);
+        const size_t slot = static_cast<size_t>(8 * v.nh * v.wh) * (paged_attn_width(head_dim) + 2) * sizeof(float);
+        most = std::max(most, 2 * static_cast<size_t>(dev.sm_count) * paged_attn_ctas(v.nw) * slot);  // two pieces a CTA
+    }
+    return kCounterBytes + most;
 }
 
 int paged_attn_m1(int64_t batch, int64_t q_heads, const void *q, int64_t q_batch, int64_t q_head, int dtype,
@@ -41,10 +47,10 @@ int paged_attn_m1(int64_t batch, int64_t q_heads, const void *q, int64_t q_batch
     if (window < 0) return fail(SDT_ERR_ARG, "paged_attn_m1: window must be >= 0 (got %lld)", (long long)window);
     if (batch == 0) return SDT_OK;
     if (!q || !out || !lens || !workspace || (max_pages && !table)) return fail(SDT_ERR_NULL, "paged_attn_m1: NULL pointer");
-    if (!aligned(q, 4) || !aligned(out, 8) || !aligned(lens, 4) || !aligned(table, 4) || !aligned(lse, 4) || !aligned(workspace, 256))
-        return fail(SDT_ERR_ALIGN, "paged_attn_m1: q must be 4-byte, out 8-byte, lens, table and lse 4-byte, workspace 256-byte aligned");
-    if (q_batch % 2 || q_head % 2 || out_batch % 4 || out_head % 4)
-        return fail(SDT_ERR_ARG, "paged_attn_m1: strides of q must be even, of out multiples of 4 elements");
+    if (!aligned(q, 16) || !aligned(out, 8) || !aligned(lens, 4) || !aligned(table, 4) || !aligned(lse, 4) || !aligned(workspace, 256))
+        return fail(SDT_ERR_ALIGN, "paged_attn_m1: q must be 16-byte, out 8-byte, lens, table and lse 4-byte, workspace 256-byte aligned");
+    if (q_batch % 8 || q_head % 8 || out_batch % 4 || out_head % 4)
+        return fail(SDT_ERR_ARG, "paged_attn_m1: strides of q must be multiples of 8, of out of 4 elements");
     DeviceInfo dev;
     rc = current_device(&dev);
     if (rc) return rc;
@@ -55,8 +61,8 @@ int paged_attn_m1(int64_t batch, int64_t q_heads, const void *q, int64_t q_batch
     if (rc) return rc;
 
     const int64_t cap = max_pages * cache->page_size;
-    PagedAttnLaunch l{paged_attn_wh(q_heads / kvh), q8, dev.sm_count, window > 0 && window < cap ? window : cap,
-                      reinterpret_cast<cudaStream_t>(stream)};
+    PagedAttnLaunch l{paged_attn_variant(q_heads / kvh, batch * kvh, dev.sm_count), q8, dev.device, dev.sm_count,
+                      window > 0 && window < cap ? window : cap, reinterpret_cast<cudaStream_t>(stream)};
     PagedAttnArgs a{};
     a.q = static_cast<const char *>(q);
     a.out = static_cast<char *>(out);
@@ -75,7 +81,8 @@ int paged_attn_m1(int64_t batch, int64_t q_heads, const void *q, int64_t q_batch
     a.batch = static_cast<int>(batch);
     a.kv_heads = static_cast<int>(kvh);
     a.group = static_cast<int>(q_heads / kvh);
-    a.head_blocks = (a.group + 16 * l.wh - 1) / (16 * l.wh);
+    const int heads = 8 * l.variant.nh * l.variant.wh;  // query heads of a CTA
+    a.head_blocks = (a.group + heads - 1) / heads;
     a.head_dim = static_cast<int>(cache->head_dim);
     a.max_pages = static_cast<int>(max_pages);
     a.num_pages = static_cast<int>(cache->num_pages);

@@ -3,34 +3,39 @@
 // For request b, query head i of key head h = i / G, and keys n in [lo_b, len_b):
 //     o = sum_n 2^(s_n - m) v_n / sum_n 2^(s_n - m),   s_n = (scale log2 e) q . k_n
 // for any reference m; a range of keys is summed up by (m, l = sum 2^(s_n - m),
-// o = sum 2^(s_n - m) v_n), and two ranges join as m' = max(m1, m2),
-// l' = l1 2^(m1 - m') + l2 2^(m2 - m'), o' likewise.
+// o = sum 2^(s_n - m) v_n), and ranges join as m' = max m_i, l' = sum l_i 2^(m_i - m'),
+// o' likewise.
 //
 // What bounds it: HBM.  A cached token costs 4 G flops per key and value element pair of 4
-// bytes (2 in q8), so with up to 16 query heads per key head the matrix instructions need
-// to run at a fraction of their rate; the design keeps enough bytes in flight.
+// bytes (2 in q8), which the matrix instructions do at a fraction of their rate; the design
+// keeps enough bytes in flight and few instructions per byte.
 //
-// Work: a unit is TK consecutive keys of one (request, key head, block of 16 WH query
-// heads).  The units of all requests, in that order, are dealt out evenly over one
-// resident grid, so a batch of any mix of lengths keeps every SM streaming to the end; a
-// CTA computes its share from `lens` by itself.  A share may begin and end inside a
-// (request, head) item: such pieces go to the workspace as (m, l, o) in fp32 and the last
-// CTA to arrive at the item joins them in the order of the keys, so results do not depend
-// on the order of arrival.
+// Work: a unit is TK consecutive keys of one (request, key head, block of query heads).
+// The units of all requests, in that order, are dealt out evenly over one resident grid, so
+// a batch of any mix of lengths keeps every SM streaming to the end; a CTA computes its
+// share from `lens` by itself.  A share may begin and end inside a (request, head) item:
+// such pieces go to the workspace as (m, l, o) in fp32 and the last CTA to arrive at the
+// item joins them in the order of the keys, so results do not depend on the order of
+// arrival.
 //
-// CTA: four warps.  WH warps work on the same keys for 16 query heads each, WK = 4 / WH
-// such groups on neighbouring keys; each has its own ring of S stages in shared memory,
-// filled by cp.async 16 bytes at a time (rows of any page size and stride; rows past the
-// range are filled with zeros, so what lies there is never read) and waits for nobody
-// else.  Page ids are read one unit ahead.  Products run on mma.sync m16n8k16 (16 query
-// heads x 8 keys, then 16 query heads x 8 value columns): the accumulators of one product
-// are the operand of the next without leaving their registers.  (tcgen05.mma wants 64 or
-// more rows of queries; one new token has G.)
+// CTA: NW warps, four or one.  WH warps work on the same keys for 8 NH query heads each,
+// NW / WH such groups on neighbouring keys; each group has its own ring of S stages in
+// shared memory, filled by cp.async 16 bytes at a time (rows of any page size and stride;
+// rows past the range are filled with zeros, so what lies there is never read) and waits
+// for nobody else.  Page ids are read one unit ahead, and an item's queries travel with its
+// first unit.
 //
-// Numbers: scores, maxima, sums and outputs stay in fp32.  The weights 2^(s - m) enter the
-// second product as the sum of two 16-bit values (the rounded weight and the rounded
-// rest): one rounding to 8 bits would cost as much accuracy as the output's own, and the
-// matrix unit has the time.
+// Products run on mma.sync m16n8k16 with the keys as the 16 rows and the query heads as the
+// 8 columns (scores), then the value columns as rows (outputs), so that 8 query heads, the
+// common case, waste nothing; tcgen05.mma would want 128 rows with 8 columns and a trip
+// through tensor memory for a softmax over every column.  The weights turn from a result
+// into an operand by movmatrix.
+//
+// Numbers: scores, maxima, sums and outputs stay in fp32.  The reference m moves only when
+// a score passes it by kAttnSlack, so most units rescale nothing; weights are then at most
+// 2^kAttnSlack.  They enter the second product as the sum of two 16-bit values (the rounded
+// weight and the rounded rest): one rounding to 8 bits would cost as much accuracy as the
+// output's own, and the matrix unit has the time.
 #pragma once
 
 #include <type_traits>
@@ -40,8 +45,9 @@
 
 namespace sdt {
 
-constexpr int kAttnWarps = 4;
-constexpr int kAttnThreads = kAttnWarps * 32;
+constexpr float kAttnSlack = 8.f;  // log2 of the largest weight
+constexpr int kAttnJoin = 32;      // most pieces that one CTA joins at a time
+constexpr int kAttnFlat = 24;      // most pieces that are joined in one level
 
 struct PagedAttnArgs {
     const char *q;             // strides in bytes
@@ -56,26 +62,37 @@ struct PagedAttnArgs {
     int head_dim, max_pages, num_pages, window;
     FastDiv page;
     float scale_log2;          // scale * log2(e)
+    int q_rows;                // query rows that a CTA keeps in shared memory: min(group, 8 NH WH)
     float *partials;           // 2 slots per CTA: [rows][DP] o, [rows] m, [rows] l
-    unsigned *counters;        // one per CTA, zero between calls
+    unsigned *counters;        // 3 per CTA, zero between calls
     int *status;
 };
 
-template <int DP, int WH, bool Q8>
+template <int DP, int NH, int WH, int NW, bool Q8>
 struct AttnCfg {
-    static constexpr int ROWB = DP * (Q8 ? 1 : 2);       // bytes of a cached row in shared memory
-    static constexpr int TK = ROWB >= 256 && !Q8 ? 64 : 128;  // keys of a unit: the stage also holds the warps' o (fp32)
-    static constexpr int WK = kAttnWarps / WH;
-    static constexpr int KS = TK / WK;                    // keys of one group of warps
-    static constexpr int RW = TK / kAttnWarps;            // rows that one warp loads
+    static constexpr int THREADS = NW * 32;
+    static constexpr int ROWB = DP * (Q8 ? 1 : 2);        // bytes of a cached row in shared memory
+    // Keys per warp of a unit: about 8 KB of keys and values, and room for the warp's o (8 NH x DP
+    // fp32), which passes through the stage at an item's end.
+    static constexpr int KW = Q8 ? (DP == 256 && NH == 1 ? 16 : 32) : (DP == 64 ? 32 : 16);
+    static constexpr int TK = KW * NW;                    // keys of a unit
+    static constexpr int WK = NW / WH;                    // groups of warps with keys of their own
+    static constexpr int KS = TK / WK;                    // keys of one group
+    static constexpr int RW = KW;                         // rows that one warp loads
     static constexpr int SCB = Q8 ? DP / 16 : 0;          // bytes of a row's scales
     static constexpr int STAGE = TK * 2 * (ROWB + SCB);
-    static constexpr int S = 3;
-    static constexpr int ROWS = 16 * WH;                  // query heads of a CTA
+    static constexpr int HEADS = 8 * NH;                  // query heads of a warp
+    static constexpr int ROWS = HEADS * WH;               // query heads of a CTA
     static constexpr int SLOT = ROWS * (DP + 2);          // floats of a partial
-    static constexpr int SMEM = S * STAGE;
-    static constexpr int CTAS = SMEM <= 112 * 1024 ? 2 : 1;
-    static_assert(STAGE >= ROWS * WK * DP * 4, "the stage must hold every warp's o");
+    static constexpr int QROW = DP * 2;                   // bytes of a query row in shared memory
+    // Three stages where two CTAs (or more of one warp) still share an SM, else two; wide heads
+    // have the SM to themselves.
+    static constexpr bool fits(int s, int bytes) { return s * (STAGE + ROWS * QROW) + 2048 <= bytes; }
+    static constexpr int S = fits(3, 113 * 1024) || (!fits(2, 113 * 1024) && fits(3, 227 * 1024)) ? 3 : 2;
+    static constexpr int smem(int q_rows) { return S * (STAGE + q_rows * QROW); }
+    static_assert(fits(S, 227 * 1024), "shared memory of an SM");
+    static_assert(STAGE >= NW * HEADS * DP * 4, "the stage must hold every warp's o");
+    static_assert(STAGE >= kAttnJoin * ROWS * 4, "the stage must hold a join's weights");
     static_assert(RW <= 32, "a lane describes one row");
 };
 
@@ -102,52 +119,51 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
                  : "r"(addr)
                  : "memory");
 }
-// d (16 x 8, fp32) += a (16 x 16) . b (16 x 8)
+// An 8 x 8 matrix of 16-bit elements, row lane / 4 and columns 2 (lane % 4) + {0, 1} a lane, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+// d (16 x 8, fp32) = a (16 x 16) . b (16 x 8) + c
 template <typename T>
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, const float (&c)[4]) {
     if constexpr (std::is_same_v<T, __half>)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
     else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {  // x in the low half
+    if constexpr (std::is_same_v<T, __half>) {
+        const __half2 h = __floats2half2_rn(x, y);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+    if constexpr (std::is_same_v<T, __half>) return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+    else return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&v));
 }
 // Two fp32 -> packed 16-bit pair (x in the low half), and the pair of what the rounding left.
 template <typename T>
 __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
-    if constexpr (std::is_same_v<T, __half>) {
-        const __half2 h = __floats2half2_rn(x, y);
-        const float2 f = __half22float2(h);
-        const __half2 l = __floats2half2_rn(x - f.x, y - f.y);
-        hi = *reinterpret_cast<const uint32_t *>(&h);
-        lo = *reinterpret_cast<const uint32_t *>(&l);
-    } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-        const float2 f = __bfloat1622float2(h);
-        const __nv_bfloat162 l = __floats2bfloat162_rn(x - f.x, y - f.y);
-        hi = *reinterpret_cast<const uint32_t *>(&h);
-        lo = *reinterpret_cast<const uint32_t *>(&l);
-    }
+    hi = pack2<T>(x, y);
+    const float2 f = unpack2<T>(hi);
+    lo = pack2<T>(x - f.x, y - f.y);
 }
-// int8 bytes in the low and third byte of t (others anything) -> two exact bf16 (T =
-// __nv_bfloat16) or fp16 values.  bf16: 0x43 in front of seven bits b reads 128 + b, and in
-// front of the sign bit alone 128 or 256: the difference is the signed value.  fp16: 0x64 in
-// front of the byte with its sign bit flipped reads 1024 + 128 + value.
-template <typename T>
-__device__ __forceinline__ uint32_t widen_s8(uint32_t t) {
-    uint32_t r;
-    if constexpr (std::is_same_v<T, __half>) {
-        const uint32_t x = ((t ^ 0x00800080u) & 0x00ff00ffu) | 0x64006400u;
-        const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&x), __half2half2(__ushort_as_half(0x6480)));
-        r = *reinterpret_cast<const uint32_t *>(&d);
-    } else {
-        const uint32_t x = (t & 0x007f007fu) | 0x43004300u, y = (t & 0x00800080u) | 0x43004300u;
-        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&x), *reinterpret_cast<const __nv_bfloat162 *>(&y));
-        r = *reinterpret_cast<const uint32_t *>(&d);
-    }
-    return r;
+// Bytes 0 and 2 of t, int8 with their sign bits flipped (bytes 1 and 3 are ignored) -> two
+// fp16 values, exact: 0x64 in front of a byte u reads 1024 + u, and u = value + 128.
+__device__ __forceinline__ uint32_t widen_u8(uint32_t t) {
+    const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&t), __half2half2(__ushort_as_half(0x6480)));
+    return *reinterpret_cast<const uint32_t *>(&d);
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t v;
@@ -173,95 +189,90 @@ struct AttnWalk {
     int b, h, j, n, lo, len;
 };
 
-template <typename T, int DP, int WH, bool Q8>
-__global__ void __launch_bounds__(kAttnThreads, (AttnCfg<DP, WH, Q8>::CTAS)) paged_attn_kernel(const PagedAttnArgs p) {
-    using C = AttnCfg<DP, WH, Q8>;
-    constexpr int TK = C::TK, KS = C::KS, RW = C::RW, ROWB = C::ROWB, S = C::S;
-    constexpr int NT = DP / 8;        // 8-wide column tiles of o
+template <typename T, int DP, int NH, int WH, int NW, bool Q8>
+__global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs p) {
+    using C = AttnCfg<DP, NH, WH, NW, Q8>;
+    constexpr int TK = C::TK, KS = C::KS, RW = C::RW, ROWB = C::ROWB, S = C::S, NTH = C::THREADS;
+    constexpr int MT = DP / 16;       // 16-wide row tiles of o
     constexpr int SUB = KS < 32 ? KS : 32;  // keys between two looks at the running maximum
-    using PT = std::conditional_t<Q8, __nv_bfloat16, T>;  // type of the second product: a q8 weight times its
-                                                          // scale needs bf16's range
+    using PT = std::conditional_t<Q8, __half, T>;            // operand type of both products
+    constexpr bool LOW = !Q8 || std::is_same_v<T, __half>;   // weights in two parts
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float st_m[kAttnWarps][16], st_l[kAttnWarps][16];
-    __shared__ long long sh_sum[kAttnWarps];
-    __shared__ int sh_b;
-    __shared__ long long sh_rest;
-    __shared__ unsigned sh_last;
+    __shared__ float st_m[NW][C::HEADS], st_l[NW][C::HEADS];
+    __shared__ long long sh_sum[NW], sh_rest;
+    __shared__ int sh_b, sh_last;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int wk = warp / WH, hw = warp % WH;
     const int g = lane >> 2, c = lane & 3;
     const uint32_t smem0 = smem_u32(smem);
+    const uint32_t q_smem = smem0 + S * C::STAGE, q_slot = p.q_rows * C::QROW;  // the stages' queries
+    const int q_own = min(max(p.q_rows - hw * C::HEADS, 0), C::HEADS);           // rows of them that are this warp's
     const int H = p.kv_heads * p.head_blocks;
+    auto cta_sync = [] {
+        if constexpr (NW == 1) __syncwarp();
+        else __syncthreads();
+    };
 
     griddep_launch_dependents();
     griddep_wait();
 
     // ---- this CTA's share ----
+    const int cap = p.max_pages * static_cast<int>(p.page.d);  // < 2^31: checked on the host
     auto range_of = [&](int b, int &lo, int &len) {
-        const int cap = p.max_pages * static_cast<int>(p.page.d);  // < 2^31: checked on the host
-        int n = __ldg(p.lens + b);
-        n = n < 0 ? 0 : n;
-        len = n > cap ? cap : n;
+        const int n = __ldg(p.lens + b);
+        len = min(max(n, 0), cap);
         lo = p.window > 0 && len > p.window ? len - p.window : 0;
         return n > cap;
     };
-    auto units_of = [&](int b) {
-        int lo, len;
-        range_of(b, lo, len);
-        const int n = (len - lo + TK - 1) / TK;
-        return n < 1 ? 1 : n;  // a request without keys still has zeros to write
-    };
+    auto units_in = [&](int lo, int len) { return max((len - lo + TK - 1) / TK, 1); };  // (a request without keys has zeros to write)
+    // a thread's requests are consecutive: one scan over the threads' sums finds everything
+    const int per = (p.batch + NTH - 1) / NTH;
+    const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
     long long mine = 0;
-    for (int b = tid; b < p.batch; b += kAttnThreads) {
-        mine += units_of(b);
+#pragma unroll 4
+    for (int b = b0; b < b1; ++b) {
         int lo, len;
         if (range_of(b, lo, len) && blockIdx.x == 0) paged_status(p.status, kSiteLength);
+        mine += units_in(lo, len);
     }
+    long long inc = mine;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0) sh_sum[warp] = mine;
-    __syncthreads();
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += t;
+    }
+    if (lane == 31) sh_sum[warp] = inc;
+    cta_sync();
     long long U = 0;
 #pragma unroll
-    for (int w = 0; w < kAttnWarps; ++w) U += sh_sum[w];
+    for (int w = 0; w < NW; ++w) {
+        if (w < warp) inc += sh_sum[w];
+        U += sh_sum[w];
+    }
     U *= H;
     const long long P = U < gridDim.x ? U : gridDim.x;  // CTAs with work
     const long long cta = blockIdx.x;
     if (cta >= P) return;
     const long long u0 = U * cta / P, u1 = U * (cta + 1) / P;
-    // the request of unit u0: scan the requests 128 at a time
-    {
-        long long before = 0;
-        for (int b0 = 0; b0 < p.batch; b0 += kAttnThreads) {
-            const int b = b0 + tid;
-            const long long n = b < p.batch ? static_cast<long long>(units_of(b)) * H : 0;
-            long long inc = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long t = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += t;
-            }
-            __syncthreads();
-            if (lane == 31) sh_sum[warp] = inc;
-            __syncthreads();
-            long long off = before;
-            for (int w = 0; w < warp; ++w) off += sh_sum[w];
-            inc += off;
-            if (u0 < inc && u0 >= inc - n) {
-                sh_b = b;
-                sh_rest = u0 - (inc - n);
-            }
-            for (int w = 0; w < kAttnWarps; ++w) before += sh_sum[w];
-            if (before > u0) break;
+    if (u0 < inc * H && u0 >= (inc - mine) * H) {  // the first unit's request is one of this thread's
+        long long at = (inc - mine) * H;
+        int b = b0;
+        for (; b < b1; ++b) {
+            int lo, len;
+            range_of(b, lo, len);
+            const long long n = static_cast<long long>(units_in(lo, len)) * H;
+            if (u0 < at + n) break;
+            at += n;
         }
-        __syncthreads();
+        sh_b = b;
+        sh_rest = u0 - at;
     }
+    cta_sync();
     auto enter = [&](AttnWalk &w) {  // the walk stands on request w.b
         if (w.b >= p.batch) return;
         range_of(w.b, w.lo, w.len);
-        const int n = (w.len - w.lo + TK - 1) / TK;
-        w.n = n < 1 ? 1 : n;
+        w.n = units_in(w.lo, w.len);
     };
     auto advance = [&](AttnWalk &w) {
         if (++w.j == w.n) {
@@ -294,6 +305,7 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<DP, WH, Q8>::CTAS)) pag
         }
     };
     const int pieces = p.head_dim * (Q8 ? 1 : 2) / 16;  // 16-byte pieces of a row that exist
+    bool first_unit_of_cta = true;
     auto issue = [&](int stage) {
         if (pg_ok && (pg_id < 0 || pg_id >= p.num_pages)) {
             paged_status(p.status, kSitePage);
@@ -326,36 +338,83 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<DP, WH, Q8>::CTAS)) pag
                 }
             }
         }
+        if (pw.j == 0 || first_unit_of_cta) {  // the item's queries
+            first_unit_of_cta = false;
+            const int h0 = (pw.h % p.head_blocks) * C::ROWS + hw * C::HEADS;
+            const char *q = p.q + pw.b * p.q_batch + static_cast<int64_t>(pg_head * p.group + h0) * p.q_head;
+            constexpr int QP = DP / 8;  // 16-byte pieces of a padded row
+            for (int e = wk * 32 + lane; e < q_own * QP; e += C::WK * 32) {
+                const int r = e / QP, x = e % QP;
+                const int n = h0 + r < p.group && x * 8 < p.head_dim ? 16 : 0;
+                cp_async16(q_smem + stage * q_slot + (hw * C::HEADS + r) * C::QROW + ((x ^ (r & 7)) << 4),
+                           n ? q + r * p.q_head + x * 16 : p.q, n);
+            }
+        }
     };
     auto group_sync = [&] {
         if constexpr (WH == 1) __syncwarp();
+        else if constexpr (WH == NW) __syncthreads();
         else asm volatile("bar.sync %0, %1;" ::"r"(1 + wk), "n"(WH * 32) : "memory");
     };
 
-    // ---- per item state ----
-    uint32_t qf[DP / 16][4];
-    float o[NT][4];
-    float m0, m1, l0, l1;  // rows g and g + 8: running reference and this thread's part of the sum
-    auto load_q = [&] {
-        const int hb = cw.h % p.head_blocks, kvh = cw.h / p.head_blocks;
-        const int r0 = hb * C::ROWS + hw * 16 + g, r1 = r0 + 8;
-        const char *q0 = p.q + cw.b * p.q_batch + static_cast<int64_t>(kvh * p.group + r0) * p.q_head;
-        const char *q1 = q0 + 8 * p.q_head;
-        const bool ok0 = r0 < p.group, ok1 = r1 < p.group;
+    // ---- per item state: tile t of o holds value columns 16 t + {g, g + 8}, query heads 2c, 2c + 1 ----
+    uint32_t qf[MT][NH][2];
+    float o[MT][NH][4];
+    float m[NH][2], l[NH][2];  // running reference and this thread's part of the sum, heads 2c, 2c + 1
+    float q_unit[NH][2];       // q8: what one unit of a head's staged query stands for
+    int v_exp = 0;             // q8: o holds sum w v 2^(30 - kAttnSlack - v_exp), every value scale so far < 2^(v_exp - 15)
+    auto load_q = [&](int stage) {
 #pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk) {
-            // columns of this thread's two pairs (any order of d does, the keys' operand has the same)
-            const int d0 = Q8 ? (kk >> 1) * 32 + c * 8 + (kk & 1) * 4 : kk * 16 + c * 2, d1 = Q8 ? d0 + 2 : d0 + 8;
-            const bool in0 = d0 < p.head_dim, in1 = d1 < p.head_dim;
-            qf[kk][0] = ok0 && in0 ? __ldg(reinterpret_cast<const unsigned *>(q0 + d0 * 2)) : 0u;
-            qf[kk][1] = ok1 && in0 ? __ldg(reinterpret_cast<const unsigned *>(q1 + d0 * 2)) : 0u;
-            qf[kk][2] = ok0 && in1 ? __ldg(reinterpret_cast<const unsigned *>(q0 + d1 * 2)) : 0u;
-            qf[kk][3] = ok1 && in1 ? __ldg(reinterpret_cast<const unsigned *>(q1 + d1 * 2)) : 0u;
+        for (int nt = 0; nt < NH; ++nt) {
+            const int r = nt * 8 + g;
+            const bool ok = r < q_own;
+            const uint32_t row = q_smem + stage * q_slot + (hw * C::HEADS + r) * C::QROW;
+#pragma unroll
+            for (int kk = 0; kk < MT; ++kk) {
+                // this thread's two pairs of columns (any order of d does, the keys' operand has the same)
+                if constexpr (!Q8) {
+                    qf[kk][nt][0] = ok ? lds32(row + (((2 * kk) ^ g) << 4) + c * 4) : 0u;
+                    qf[kk][nt][1] = ok ? lds32(row + (((2 * kk + 1) ^ g) << 4) + c * 4) : 0u;
+                } else {  // 8 values of a group are two k-steps' share
+                    const uint2 x = ok ? lds64(row + ((((kk >> 1) * 4 + c) ^ g) << 4) + (kk & 1) * 8) : make_uint2(0, 0);
+                    qf[kk][nt][0] = x.x;
+                    qf[kk][nt][1] = x.y;
+                }
+            }
+            if constexpr (Q8 && !std::is_same_v<T, __half>) {
+                // bf16 queries as fp16: scaled by a power of two so that the head's largest lies in [1, 2);
+                // what falls below fp16's range is 2^-24 of it
+                float top = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < MT; ++kk)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 f = unpack2<T>(qf[kk][nt][i]);
+                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // exponent field of the largest, kept where its inverse is a normal number too
+                const uint32_t ex = min(max(__float_as_uint(top) >> 23, 1u), 252u);
+                const float down = __uint_as_float((254u - ex) << 23), up = __uint_as_float(ex << 23);
+#pragma unroll
+                for (int kk = 0; kk < MT; ++kk)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 f = unpack2<T>(qf[kk][nt][i]);
+                        qf[kk][nt][i] = pack2<__half>(f.x * down, f.y * down);
+                    }
+                q_unit[nt][0] = __shfl_sync(0xffffffffu, up, 8 * c);      // heads 2c and 2c + 1 lie in lane groups
+                q_unit[nt][1] = __shfl_sync(0xffffffffu, up, 8 * c + 4);  // 2c and 2c + 1
+            } else {
+                q_unit[nt][0] = q_unit[nt][1] = 1.f;
+            }
+            m[nt][0] = m[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+            for (int t = 0; t < MT; ++t) o[t][nt][0] = o[t][nt][1] = o[t][nt][2] = o[t][nt][3] = 0.f;
         }
-#pragma unroll
-        for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-        m0 = m1 = -INFINITY;
-        l0 = l1 = 0.f;
+        v_exp = 0;
     };
 
     // ---- prologue: S - 1 units in flight, the page ids of the next ----
@@ -388,7 +447,10 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<DP, WH, Q8>::CTAS)) pag
             cp_async_commit();
         }
         if (fresh) {
-            load_q();
+            if constexpr (C::WK > 1) __syncthreads();  // the groups load shares of the queries
+            load_q(stage);
+            if constexpr (NW > 1) __syncthreads();     // ... and may load others over them
+            else __syncwarp();
             fresh = false;
         }
         const uint32_t kt = smem0 + stage * C::STAGE + wk * KS * ROWB, vt = kt + TK * ROWB;
@@ -397,134 +459,218 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<DP, WH, Q8>::CTAS)) pag
 #pragma unroll 1
         for (int k0 = 0; k0 < KS; k0 += SUB) {
             if (k0 >= left) break;
-            float s[SUB / 8][4];
-#pragma unroll
-            for (int i = 0; i < SUB / 8; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
-            // scores: 16 query heads x SUB keys
+            constexpr int KT = SUB / 16;  // 16-key tiles: keys 16 kt + g and + 8 are this thread's
+            float s[KT][NH][4];
+            // scores: SUB keys x 8 NH query heads
             if constexpr (!Q8) {
-                const uint32_t row = kt + (k0 + (lane & 7) + ((lane >> 4) << 3)) * ROWB;
-                const uint32_t sw = (((lane >> 3) & 1) ^ (lane & 7)) << 4;
 #pragma unroll
-                for (int kk = 0; kk < DP / 16; ++kk) {
+                for (int i = 0; i < KT; ++i)
 #pragma unroll
-                    for (int i = 0; i < SUB / 16; ++i) {
-                        uint32_t b[4];
-                        ldsm_x4(row + i * 16 * ROWB + ((kk << 5) ^ sw), b);
-                        mma16816<T>(s[2 * i], qf[kk], b[0], b[1]);
-                        mma16816<T>(s[2 * i + 1], qf[kk], b[2], b[3]);
+                    for (int nt = 0; nt < NH; ++nt) s[i][nt][0] = s[i][nt][1] = s[i][nt][2] = s[i][nt][3] = 0.f;
+                const uint32_t row = kt + (k0 + (lane & 15)) * ROWB;
+                const uint32_t sw = ((lane >> 4) ^ (lane & 7)) << 4;
+#pragma unroll
+                for (int kk = 0; kk < MT; ++kk)
+#pragma unroll
+                    for (int i = 0; i < KT; ++i) {
+                        uint32_t a[4];
+                        ldsm_x4(row + i * 16 * ROWB + ((kk << 5) ^ sw), a);
+#pragma unroll
+                        for (int nt = 0; nt < NH; ++nt) mma16816<PT>(s[i][nt], a, qf[kk][nt][0], qf[kk][nt][1], s[i][nt]);
+                    }
+            } else {
+                const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < KT; ++i) {
+                    const uint32_t r = k0 + i * 16 + g;  // this thread's keys: r, r + 8
+                    float2 sc0[DP / 64], sc1[DP / 64];   // and their scales
+#pragma unroll
+                    for (int x = 0; x < DP / 64; ++x) {
+                        sc0[x] = unpack2<__half>(lds32(kst + r * C::SCB + x * 4));
+                        sc1[x] = unpack2<__half>(lds32(kst + (r + 8) * C::SCB + x * 4));
+                    }
+#pragma unroll
+                    for (int gr = 0; gr < DP / 32; ++gr) {
+                        const uint32_t piece = gr * 2 + (c >> 1), half8 = (c & 1) * 8;
+                        uint2 w0 = lds64(kt + r * ROWB + q8_piece<DP>(r, piece) * 16 + half8);
+                        uint2 w1 = lds64(kt + (r + 8) * ROWB + q8_piece<DP>(r + 8, piece) * 16 + half8);
+                        w0.x ^= 0x80808080u;
+                        w0.y ^= 0x80808080u;
+                        w1.x ^= 0x80808080u;
+                        w1.y ^= 0x80808080u;
+                        const uint32_t front = 0x64646464u;
+                        const uint32_t a0[4] = {widen_u8(__byte_perm(w0.x, front, 0x4140)), widen_u8(__byte_perm(w1.x, front, 0x4140)),
+                                                widen_u8(__byte_perm(w0.x, front, 0x4342)), widen_u8(__byte_perm(w1.x, front, 0x4342))};
+                        const uint32_t a1[4] = {widen_u8(__byte_perm(w0.y, front, 0x4140)), widen_u8(__byte_perm(w1.y, front, 0x4140)),
+                                                widen_u8(__byte_perm(w0.y, front, 0x4342)), widen_u8(__byte_perm(w1.y, front, 0x4342))};
+                        const float f0 = gr & 1 ? sc0[gr >> 1].y : sc0[gr >> 1].x, f1 = gr & 1 ? sc1[gr >> 1].y : sc1[gr >> 1].x;
+#pragma unroll
+                        for (int nt = 0; nt < NH; ++nt) {
+                            float t[4];
+                            mma16816<PT>(t, a0, qf[2 * gr][nt][0], qf[2 * gr][nt][1], zero);
+                            mma16816<PT>(t, a1, qf[2 * gr + 1][nt][0], qf[2 * gr + 1][nt][1], t);
+                            s[i][nt][0] = gr ? s[i][nt][0] + t[0] * f0 : t[0] * f0;
+                            s[i][nt][1] = gr ? s[i][nt][1] + t[1] * f0 : t[1] * f0;
+                            s[i][nt][2] = gr ? s[i][nt][2] + t[2] * f1 : t[2] * f1;
+                            s[i][nt][3] = gr ? s[i][nt][3] + t[3] * f1 : t[3] * f1;
+                        }
+                    }
+                }
+            }
+            // scaled scores; keys past the range drop out; the largest of this thread's
+            bool past = false;
+            float x[NH][2];
+#pragma unroll
+            for (int nt = 0; nt < NH; ++nt) {
+                const float sc0 = Q8 ? p.scale_log2 * q_unit[nt][0] : p.scale_log2, sc1 = Q8 ? p.scale_log2 * q_unit[nt][1] : p.scale_log2;
+                x[nt][0] = x[nt][1] = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < KT; ++i) {
+                    s[i][nt][0] *= sc0;
+                    s[i][nt][1] *= sc1;
+                    s[i][nt][2] *= sc0;
+                    s[i][nt][3] *= sc1;
+                    if (k0 + SUB > left) {
+                        const int n = k0 + i * 16 + g;
+                        if (n >= left) s[i][nt][0] = s[i][nt][1] = -INFINITY;
+                        if (n + 8 >= left) s[i][nt][2] = s[i][nt][3] = -INFINITY;
+                    }
+                    x[nt][0] = fmaxf(x[nt][0], fmaxf(s[i][nt][0], s[i][nt][2]));
+                    x[nt][1] = fmaxf(x[nt][1], fmaxf(s[i][nt][1], s[i][nt][3]));
+                }
+                past = past || x[nt][0] > m[nt][0] + kAttnSlack || x[nt][1] > m[nt][1] + kAttnSlack;
+            }
+            if (__any_sync(0xffffffffu, past)) {  // the reference moves to the largest score so far
+#pragma unroll
+                for (int nt = 0; nt < NH; ++nt) {
+                    float a[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float y = x[nt][i];
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+                        y = fmaxf(y, m[nt][i]);
+                        a[i] = y == m[nt][i] ? 1.f : exp2f(m[nt][i] - y);
+                        m[nt][i] = y;
+                        l[nt][i] *= a[i];
+                    }
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        o[t][nt][0] *= a[0];
+                        o[t][nt][1] *= a[1];
+                        o[t][nt][2] *= a[0];
+                        o[t][nt][3] *= a[1];
+                    }
+                }
+            }
+            // weights (a head that has seen only -inf keeps its weights at zero)
+#pragma unroll
+            for (int nt = 0; nt < NH; ++nt) {
+                const float e0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], e1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+#pragma unroll
+                for (int i = 0; i < KT; ++i) {
+                    s[i][nt][0] = exp2f(s[i][nt][0] - e0);
+                    s[i][nt][1] = exp2f(s[i][nt][1] - e1);
+                    s[i][nt][2] = exp2f(s[i][nt][2] - e0);
+                    s[i][nt][3] = exp2f(s[i][nt][3] - e1);
+                    l[nt][0] += s[i][nt][0] + s[i][nt][2];
+                    l[nt][1] += s[i][nt][1] + s[i][nt][3];
+                }
+            }
+            // o += values . weights
+            if constexpr (!Q8) {
+#pragma unroll
+                for (int i = 0; i < KT; ++i) {
+                    uint32_t hi[NH][2], lo[NH][2];
+#pragma unroll
+                    for (int nt = 0; nt < NH; ++nt)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            split2<PT>(s[i][nt][2 * y], s[i][nt][2 * y + 1], hi[nt][y], lo[nt][y]);
+                            hi[nt][y] = transpose8x8(hi[nt][y]);
+                            lo[nt][y] = transpose8x8(lo[nt][y]);
+                        }
+                    // values stored key by key: transposed on the way into registers
+                    const uint32_t row = vt + (k0 + i * 16 + (lane & 7) + ((lane >> 4) << 3)) * ROWB;
+                    const uint32_t sw = (((lane >> 3) & 1) ^ (lane & 7)) << 4;
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        uint32_t a[4];
+                        ldsm_x4_t(row + ((t << 5) ^ sw), a);
+#pragma unroll
+                        for (int nt = 0; nt < NH; ++nt) {
+                            mma16816<PT>(o[t][nt], a, hi[nt][0], hi[nt][1], o[t][nt]);
+                            mma16816<PT>(o[t][nt], a, lo[nt][0], lo[nt][1], o[t][nt]);
+                        }
                     }
                 }
             } else {
+                // the exponents of this block's value scales: o is kept so that weight times scale fits fp16
+                uint32_t xs[KT][2][DP / 64], top = 0;
 #pragma unroll
-                for (int gr = 0; gr < DP / 32; ++gr) {
+                for (int i = 0; i < KT; ++i)
 #pragma unroll
-                    for (int i = 0; i < SUB / 8; ++i) {
-                        const uint32_t r = k0 + i * 8 + g;
-                        const uint2 w = lds64(kt + r * ROWB + q8_piece<DP>(r, gr * 2 + (c >> 1)) * 16 + (c & 1) * 8);
-                        float t[4] = {0.f, 0.f, 0.f, 0.f};
-                        mma16816<T>(t, qf[2 * gr], widen_s8<T>(__byte_perm(w.x, 0, 0x4140)), widen_s8<T>(__byte_perm(w.x, 0, 0x4342)));
-                        mma16816<T>(t, qf[2 * gr + 1], widen_s8<T>(__byte_perm(w.y, 0, 0x4140)), widen_s8<T>(__byte_perm(w.y, 0, 0x4342)));
-                        // columns 2c, 2c + 1 of the tile are keys with scales of their own
-                        const uint32_t sa = kst + (k0 + i * 8 + 2 * c) * C::SCB + gr * 2;
-                        unsigned short x0, x1;
-                        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x0) : "r"(sa) : "memory");
-                        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x1) : "r"(sa + C::SCB) : "memory");
-                        const float f0 = __half2float(__ushort_as_half(x0)), f1 = __half2float(__ushort_as_half(x1));
-                        s[i][0] += t[0] * f0;
-                        s[i][1] += t[1] * f1;
-                        s[i][2] += t[2] * f0;
-                        s[i][3] += t[3] * f1;
-                    }
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int x = 0; x < DP / 64; ++x) {
+                            xs[i][y][x] = lds32(vst + (k0 + i * 16 + g + 8 * y) * C::SCB + x * 4);
+                            top = __vmaxu2(top, xs[i][y][x] & 0x7fff7fffu);
+                        }
+                int ex = static_cast<int>(max(top & 0xffffu, top >> 16) >> 10) + 1;  // scales < 2^(ex - 15)
+                if (__any_sync(0xffffffffu, ex > v_exp)) {
+                    ex = max(__reduce_max_sync(0xffffffffu, ex), v_exp);
+                    const float f = __uint_as_float(static_cast<uint32_t>(127 + v_exp - ex) << 23);
+                    v_exp = ex;
+#pragma unroll
+                    for (int t = 0; t < MT; ++t)
+#pragma unroll
+                        for (int nt = 0; nt < NH; ++nt)
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) o[t][nt][y] *= f;
                 }
-            }
-            // running maximum; keys past the range drop out
-            float x0 = -INFINITY, x1 = -INFINITY;
+                const float up = __uint_as_float(static_cast<uint32_t>(127 + 30 - static_cast<int>(kAttnSlack) - v_exp) << 23);
 #pragma unroll
-            for (int i = 0; i < SUB / 8; ++i) {
-                const int n = k0 + i * 8 + 2 * c;
-                s[i][0] = n < left ? s[i][0] * p.scale_log2 : -INFINITY;
-                s[i][1] = n + 1 < left ? s[i][1] * p.scale_log2 : -INFINITY;
-                s[i][2] = n < left ? s[i][2] * p.scale_log2 : -INFINITY;
-                s[i][3] = n + 1 < left ? s[i][3] * p.scale_log2 : -INFINITY;
-                x0 = fmaxf(x0, fmaxf(s[i][0], s[i][1]));
-                x1 = fmaxf(x1, fmaxf(s[i][2], s[i][3]));
-            }
-            x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
-            x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
-            x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
-            x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
-            if (__any_sync(0xffffffffu, x0 > m0 || x1 > m1)) {
-                const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-                const float a0 = m0 == n0 ? 1.f : exp2f(m0 - n0), a1 = m1 == n1 ? 1.f : exp2f(m1 - n1);
-                m0 = n0;
-                m1 = n1;
-                l0 *= a0;
-                l1 *= a1;
-#pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    o[i][0] *= a0;
-                    o[i][1] *= a0;
-                    o[i][2] *= a1;
-                    o[i][3] *= a1;
-                }
-            }
-            // weights (a row that has seen only -inf keeps its weights at zero)
-            const float e0 = m0 == -INFINITY ? 0.f : m0, e1 = m1 == -INFINITY ? 0.f : m1;
-#pragma unroll
-            for (int i = 0; i < SUB / 8; ++i) {
-                s[i][0] = exp2f(s[i][0] - e0);
-                s[i][1] = exp2f(s[i][1] - e0);
-                s[i][2] = exp2f(s[i][2] - e1);
-                s[i][3] = exp2f(s[i][3] - e1);
-                l0 += s[i][0] + s[i][1];
-                l1 += s[i][2] + s[i][3];
-            }
-            // o += weights . values
-#pragma unroll
-            for (int kb = 0; kb < SUB / 16; ++kb) {
-                if constexpr (!Q8) {
-                    uint32_t hi[4], lo[4];
-                    split2<PT>(s[2 * kb][0], s[2 * kb][1], hi[0], lo[0]);
-                    split2<PT>(s[2 * kb][2], s[2 * kb][3], hi[1], lo[1]);
-                    split2<PT>(s[2 * kb + 1][0], s[2 * kb + 1][1], hi[2], lo[2]);
-                    split2<PT>(s[2 * kb + 1][2], s[2 * kb + 1][3], hi[3], lo[3]);
-                    const uint32_t row = vt + (k0 + kb * 16 + (lane & 15)) * ROWB;
-                    const uint32_t sw = ((lane >> 4) ^ (lane & 7)) << 4;
-#pragma unroll
-                    for (int i = 0; i < NT / 2; ++i) {
-                        uint32_t b[4];
-                        ldsm_x4_t(row + ((i << 5) ^ sw), b);
-                        mma16816<PT>(o[2 * i], hi, b[0], b[1]);
-                        mma16816<PT>(o[2 * i], lo, b[0], b[1]);
-                        mma16816<PT>(o[2 * i + 1], hi, b[2], b[3]);
-                        mma16816<PT>(o[2 * i + 1], lo, b[2], b[3]);
-                    }
-                } else {
-                    const uint32_t r = k0 + kb * 16 + 2 * c;  // this thread's keys: r, r+1, r+8, r+9
+                for (int i = 0; i < KT; ++i) {
+                    const uint32_t r = k0 + i * 16 + 2 * c;  // this thread's keys in the values: r, r+1, r+8, r+9
 #pragma unroll
                     for (int gr = 0; gr < DP / 32; ++gr) {
-                        float f[4];
                         uint32_t w[4];
 #pragma unroll
                         for (int t = 0; t < 4; ++t) {
                             const uint32_t rt = r + (t & 1) + (t >> 1) * 8;
-                            unsigned short x;
-                            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(vst + rt * C::SCB + gr * 2) : "memory");
-                            f[t] = __half2float(__ushort_as_half(x));
-                            w[t] = lds32(vt + rt * ROWB + q8_piece<DP>(rt, gr * 2 + (g >> 2)) * 16 + (g & 3) * 4);
+                            w[t] = lds32(vt + rt * ROWB + q8_piece<DP>(rt, gr * 2 + (g >> 2)) * 16 + (g & 3) * 4) ^ 0x80808080u;
                         }
-                        uint32_t hi[4], lo[4];
-                        split2<PT>(s[2 * kb][0] * f[0], s[2 * kb][1] * f[1], hi[0], lo[0]);
-                        split2<PT>(s[2 * kb][2] * f[0], s[2 * kb][3] * f[1], hi[1], lo[1]);
-                        split2<PT>(s[2 * kb + 1][0] * f[2], s[2 * kb + 1][1] * f[3], hi[2], lo[2]);
-                        split2<PT>(s[2 * kb + 1][2] * f[2], s[2 * kb + 1][3] * f[3], hi[3], lo[3]);
+                        const float2 y0 = unpack2<__half>(xs[i][0][gr >> 1]), y1 = unpack2<__half>(xs[i][1][gr >> 1]);
+                        const float f0 = (gr & 1 ? y0.y : y0.x) * up, f1 = (gr & 1 ? y1.y : y1.x) * up;
+                        uint32_t hi[NH][2], lo[NH][2];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {  // column tile j: value g * 4 + j of the group
-                            const uint32_t sel = static_cast<uint32_t>(j) | (static_cast<uint32_t>(4 + j) << 8);
-                            const uint32_t b0 = widen_s8<PT>(__byte_perm(w[0], w[1], sel));
-                            const uint32_t b1 = widen_s8<PT>(__byte_perm(w[2], w[3], sel));
-                            mma16816<PT>(o[gr * 4 + j], hi, b0, b1);
-                            mma16816<PT>(o[gr * 4 + j], lo, b0, b1);
+                        for (int nt = 0; nt < NH; ++nt)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const float wx = s[i][nt][2 * y] * (y ? f1 : f0), wy = s[i][nt][2 * y + 1] * (y ? f1 : f0);
+                                if constexpr (LOW) {
+                                    split2<PT>(wx, wy, hi[nt][y], lo[nt][y]);
+                                    lo[nt][y] = transpose8x8(lo[nt][y]);
+                                } else {
+                                    hi[nt][y] = pack2<PT>(wx, wy);
+                                }
+                                hi[nt][y] = transpose8x8(hi[nt][y]);
+                            }
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {  // rows g and g + 8 of the tile: values 4 g + 2 t and + 1 of the group
+                            uint32_t a[4];
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                const uint32_t j = 2 * t + (y & 1), pair = (y >> 1) * 2;
+                                a[y] = __byte_perm(w[pair], w[pair + 1], j | ((4 + j) << 8));
+                                a[y] = widen_u8((a[y] & 0x00ff00ffu) | 0x64006400u);
+                            }
+#pragma unroll
+                            for (int nt = 0; nt < NH; ++nt) {
+                                mma16816<PT>(o[2 * gr + t][nt], a, hi[nt][0], hi[nt][1], o[2 * gr + t][nt]);
+                                if constexpr (LOW) mma16816<PT>(o[2 * gr + t][nt], a, lo[nt][0], lo[nt][1], o[2 * gr + t][nt]);
+                            }
                         }
                     }
                 }
@@ -534,65 +680,61 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<DP, WH, Q8>::CTAS)) pag
         const bool item_done = cw.j == cw.n - 1;
         if (item_done || u == u1 - 1) {
             // ---- the CTA's piece of the item: join the warps through the stage just read ----
-            l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-            l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-            l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-            l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-            __syncthreads();  // every warp has read the stage
-            if (c == 0) {
-                st_m[warp][g] = m0;
-                st_m[warp][g + 8] = m1;
-                st_l[warp][g] = l0;
-                st_l[warp][g + 8] = l1;
-            }
+            const float back = Q8 ? __uint_as_float(static_cast<uint32_t>(127 - 30 + static_cast<int>(kAttnSlack) + v_exp) << 23) : 1.f;
+#pragma unroll
+            for (int nt = 0; nt < NH; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], 4);
+                    l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], 8);
+                    l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], 16);
+                }
+            cta_sync();  // every warp has read the stage
             float *ob = reinterpret_cast<float *>(smem + stage * C::STAGE);
             const int valid = min(p.group - (cw.h % p.head_blocks) * C::ROWS, C::ROWS);  // query heads of this block
-            const int sw = (g & 3) << 3;  // 32-byte pieces of a row swapped by row: no bank conflicts
-            float *w0 = ob + (warp * 16 + g) * DP, *w1 = w0 + 8 * DP;
-            if constexpr (!Q8) {
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    if (hw * 16 + g < valid) *reinterpret_cast<float2 *>(w0 + ((i * 8 + 2 * c) ^ sw)) = make_float2(o[i][0], o[i][1]);
-                    if (hw * 16 + g + 8 < valid) *reinterpret_cast<float2 *>(w1 + ((i * 8 + 2 * c) ^ sw)) = make_float2(o[i][2], o[i][3]);
-                }
-            } else {  // column n of tile j of a group is its value 4 n + j
+            for (int nt = 0; nt < NH; ++nt)
 #pragma unroll
-                for (int gr = 0; gr < DP / 32; ++gr) {
+                for (int i = 0; i < 2; ++i) {
+                    const int r = nt * 8 + 2 * c + i;
+                    if (g == 0) {
+                        st_m[warp][r] = m[nt][i];
+                        st_l[warp][r] = l[nt][i];
+                    }
+                    if (hw * C::HEADS + r >= valid) continue;
+                    float *row = ob + (warp * C::HEADS + r) * DP;
+                    const int sw = c << 3;  // 32-byte pieces of a row swapped by head: no bank conflicts
+                    if constexpr (!Q8) {
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int at = (gr * 32 + c * 8 + x * 4) ^ sw;
-                        if (hw * 16 + g < valid)
-                            *reinterpret_cast<float4 *>(w0 + at) = make_float4(o[gr * 4][x], o[gr * 4 + 1][x], o[gr * 4 + 2][x], o[gr * 4 + 3][x]);
-                        if (hw * 16 + g + 8 < valid)
-                            *reinterpret_cast<float4 *>(w1 + at) = make_float4(o[gr * 4][2 + x], o[gr * 4 + 1][2 + x], o[gr * 4 + 2][2 + x], o[gr * 4 + 3][2 + x]);
+                        for (int t = 0; t < MT; ++t) {
+                            row[(t * 16 + g) ^ sw] = o[t][nt][i];
+                            row[(t * 16 + g + 8) ^ sw] = o[t][nt][2 + i];
+                        }
+                    } else {
+#pragma unroll
+                        for (int gr = 0; gr < DP / 32; ++gr)
+                            *reinterpret_cast<float4 *>(row + ((gr * 32 + g * 4) ^ sw)) =
+                                make_float4(o[2 * gr][nt][i] * back, o[2 * gr][nt][2 + i] * back, o[2 * gr + 1][nt][i] * back,
+                                            o[2 * gr + 1][nt][2 + i] * back);
                     }
                 }
-            }
-            __syncthreads();
+            cta_sync();
 
             const long long first_unit = u - cw.j, end_unit = first_unit + cw.n;
             const bool whole = first_unit >= u0 && end_unit <= u1;
             const int head0 = (cw.h / p.head_blocks) * p.group + (cw.h % p.head_blocks) * C::ROWS;
             auto store = [&](int r, int col, const float4 &v, float M, float L) {
                 const float inv = L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;  // no key: zeros; a NaN sum stays NaN
-                if (col < p.head_dim) {
-                    uint2 b;
-                    if constexpr (std::is_same_v<T, __half>) {
-                        const __half2 a0 = __floats2half2_rn(v.x * inv, v.y * inv), a1 = __floats2half2_rn(v.z * inv, v.w * inv);
-                        b = make_uint2(*reinterpret_cast<const uint32_t *>(&a0), *reinterpret_cast<const uint32_t *>(&a1));
-                    } else {
-                        const __nv_bfloat162 a0 = __floats2bfloat162_rn(v.x * inv, v.y * inv), a1 = __floats2bfloat162_rn(v.z * inv, v.w * inv);
-                        b = make_uint2(*reinterpret_cast<const uint32_t *>(&a0), *reinterpret_cast<const uint32_t *>(&a1));
-                    }
-                    *reinterpret_cast<uint2 *>(p.out + cw.b * p.o_batch + static_cast<int64_t>(head0 + r) * p.o_head + col * 2) = b;
-                }
+                if (col < p.head_dim)
+                    *reinterpret_cast<uint2 *>(p.out + cw.b * p.o_batch + static_cast<int64_t>(head0 + r) * p.o_head + col * 2) =
+                        make_uint2(pack2<T>(v.x * inv, v.y * inv), pack2<T>(v.z * inv, v.w * inv));
                 if (p.lse && col == 0)
                     p.lse[static_cast<int64_t>(cw.b) * p.kv_heads * p.group + head0 + r] =
                         L == 0.f ? -INFINITY : M * 0.6931471805599453f + logf(L);
             };
             float *slot = p.partials + static_cast<size_t>(2 * cta + (first_unit >= u0 ? 1 : 0)) * C::SLOT;
-            for (int e = tid; e < valid * (DP / 4); e += kAttnThreads) {
-                const int r = e / (DP / 4), col = (e % (DP / 4)) * 4, rw = r >> 4, rr = r & 15;
+            for (int e = tid; e < valid * (DP / 4); e += NTH) {
+                const int r = e / (DP / 4), col = (e % (DP / 4)) * 4, rw = r / C::HEADS, rr = r % C::HEADS;
                 float M = st_m[rw][rr];
 #pragma unroll
                 for (int w = 1; w < C::WK; ++w) M = fmaxf(M, st_m[w * WH + rw][rr]);
@@ -602,7 +744,7 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<DP, WH, Q8>::CTAS)) pag
                 for (int w = 0; w < C::WK; ++w) {
                     const float mw = st_m[w * WH + rw][rr];
                     const float f = mw == M ? 1.f : exp2f(mw - M);  // (both -inf: zeros either way)
-                    const float4 v = *reinterpret_cast<const float4 *>(ob + ((w * WH + rw) * 16 + rr) * DP + (col ^ ((rr & 3) << 3)));
+                    const float4 v = *reinterpret_cast<const float4 *>(ob + ((w * WH + rw) * C::HEADS + rr) * DP + (col ^ (((rr >> 1) & 3) << 3)));
                     L += st_l[w * WH + rw][rr] * f;
                     acc.x += v.x * f;
                     acc.y += v.y * f;
@@ -619,42 +761,90 @@ __global__ void __launch_bounds__(kAttnThreads, (AttnCfg<DP, WH, Q8>::CTAS)) pag
                     }
                 }
             }
+            cta_sync();  // the stage and the statistics may be written again
             if (!whole) {
-                // ---- the item's pieces: the last CTA to arrive joins them ----
+                // ---- the item's pieces: the last CTA to arrive joins them.  More than kAttnFlat pieces
+                // join in two levels of at most kAttnJoin (the grid has at most its square of CTAs) ----
                 const long long first_cta = ((first_unit + 1) * P - 1) / U, last_cta = (end_unit * P - 1) / U;
-                const int pieces_n = static_cast<int>(last_cta - first_cta) + 1;
-                __threadfence();
-                __syncthreads();
-                if (tid == 0) sh_last = atomicAdd(p.counters + first_cta, 1u) == static_cast<unsigned>(pieces_n - 1);
-                __syncthreads();
-                if (sh_last) {
-                    __threadfence();
-                    // piece 0 lies in its CTA's second slot, the others in their first
-                    auto piece = [&](int i) { return p.partials + static_cast<size_t>(2 * (first_cta + i) + (i == 0 ? 1 : 0)) * C::SLOT; };
-                    for (int e = tid; e < valid * (DP / 4); e += kAttnThreads) {
+                const int n = static_cast<int>(last_cta - first_cta) + 1;
+                // piece 0 lies in its CTA's second slot, the others in their first
+                auto piece = [&](int i) { return p.partials + static_cast<size_t>(2 * (first_cta + i) + (i == 0 ? 1 : 0)) * C::SLOT; };
+                float *weights = ob;  // [pieces][ROWS]
+                // Counts an arrival; true in all threads of the last of `all` to arrive.
+                auto arrive = [&](unsigned *counter, int all) {
+                    if (tid == 0) {
+                        __threadfence();
+                        const bool last = atomicAdd(counter, 1u) == static_cast<unsigned>(all - 1);
+                        if (last) {
+                            *counter = 0;
+                            __threadfence();
+                        }
+                        sh_last = last;
+                    }
+                    cta_sync();
+                    return sh_last != 0;
+                };
+                // Joins `count` pieces i0, i0 + step, ...; to the output or over piece i0.
+                auto join = [&](int i0, int step, int count, bool final) {
+                    for (int r = warp; r < valid; r += NW) {
+                        float M = -INFINITY, L = 0.f;
+                        const float mi = lane < count ? __ldcg(piece(i0 + lane * step) + C::ROWS * DP + r) : -INFINITY;
+                        const float li = lane < count ? __ldcg(piece(i0 + lane * step) + C::ROWS * (DP + 1) + r) : 0.f;
+                        M = mi;
+#pragma unroll
+                        for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+                        const float f = mi == M ? 1.f : exp2f(mi - M);
+                        L = li * f;
+#pragma unroll
+                        for (int x = 16; x > 0; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
+                        if (lane < count) weights[lane * C::ROWS + r] = f;
+                        if (lane == 0) {
+                            st_m[r / C::HEADS][r % C::HEADS] = M;
+                            st_l[r / C::HEADS][r % C::HEADS] = L;
+                        }
+                    }
+                    cta_sync();
+                    for (int e = tid; e < valid * (DP / 4); e += NTH) {
                         const int r = e / (DP / 4), col = (e % (DP / 4)) * 4;
-                        float M = -INFINITY;
-                        for (int i = 0; i < pieces_n; ++i) M = fmaxf(M, __ldcg(piece(i) + C::ROWS * DP + r));
-                        float L = 0.f;
                         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                        for (int i = 0; i < pieces_n; ++i) {
-                            const float *s = piece(i);
-                            const float mi = __ldcg(s + C::ROWS * DP + r);
-                            const float f = mi == M ? 1.f : exp2f(mi - M);
-                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(s + r * DP + col));
-                            L += __ldcg(s + C::ROWS * (DP + 1) + r) * f;
+#pragma unroll 8
+                        for (int i = 0; i < count; ++i) {
+                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(piece(i0 + i * step) + r * DP + col));
+                            const float f = weights[i * C::ROWS + r];
                             acc.x += v.x * f;
                             acc.y += v.y * f;
                             acc.z += v.z * f;
                             acc.w += v.w * f;
                         }
-                        store(r, col, acc, M, L);
+                        const float M = st_m[r / C::HEADS][r % C::HEADS], L = st_l[r / C::HEADS][r % C::HEADS];
+                        if (final) {
+                            store(r, col, acc, M, L);
+                        } else {
+                            float *to = piece(i0);
+                            *reinterpret_cast<float4 *>(to + r * DP + col) = acc;
+                            if (col == 0) {
+                                to[C::ROWS * DP + r] = M;
+                                to[C::ROWS * (DP + 1) + r] = L;
+                            }
+                        }
                     }
-                    if (tid == 0) p.counters[first_cta] = 0;
+                    cta_sync();
+                };
+                unsigned *count_item = p.counters + first_cta;
+                if (n <= kAttnFlat) {
+                    if (arrive(count_item, n)) join(0, 1, n, true);
+                } else {
+                    const int per_group = max((n + kAttnJoin - 1) / kAttnJoin, 16), groups = (n + per_group - 1) / per_group;
+                    const int mine = static_cast<int>(cta - first_cta) / per_group, i0 = mine * per_group, in = min(per_group, n - i0);
+                    // an item's first group counts beside the item's own counter, the others at their first
+                    // CTA, where no other item has a group that is not its first
+                    unsigned *count_group = p.counters + (mine == 0 ? gridDim.x + first_cta : 2 * gridDim.x + first_cta + i0);
+                    if (arrive(count_group, in)) {
+                        join(i0, 1, in, false);
+                        if (arrive(count_item, groups)) join(0, per_group, groups, true);
+                    }
                 }
             }
-            __syncthreads();  // the stage may be loaded again, the statistics written again
             fresh = true;
         }
         advance(cw);

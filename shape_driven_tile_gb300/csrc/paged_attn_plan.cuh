@@ -7,17 +7,31 @@ namespace sdt {
 
 struct PagedAttnArgs;
 
+struct PagedAttnVariant {
+    int nh;  // a warp's query heads / 8
+    int wh;  // warps of a CTA that share keys, with query heads of their own
+    int nw;  // warps of a CTA
+};
+
 struct PagedAttnLaunch {
-    int wh;            // warps of a CTA that share keys, 16 query heads each
+    PagedAttnVariant variant;
     bool q8;
-    int sm_count;
+    int device, sm_count;
     int64_t max_keys;  // of one request
     cudaStream_t stream;
 };
 
-// Warps on the same keys: enough for the query heads of one key head, so that keys are read
-// once for up to 64 of them.
-inline int paged_attn_wh(int64_t group) { return group <= 16 ? 1 : group <= 32 ? 2 : 4; }
+// CTAs of nw warps per SM, at most: more of one warp would pass the join's 1024 on 152 SMs.
+inline int paged_attn_ctas(int nw) { return nw == 1 ? 6 : 2; }
+
+// `group` query heads per key head; keys are read once for up to 64 of them.  `items`:
+// requests x key heads.
+inline PagedAttnVariant paged_attn_variant(int64_t group, int64_t items, int sm_count) {
+    if (group > 32) return {2, 4, 4};
+    if (group > 16) return {2, 2, 4};
+    const int nw = items >= static_cast<int64_t>(sm_count) * paged_attn_ctas(1) ? 1 : 4;
+    return {group > 8 ? 2 : 1, 1, nw};
+}
 // Head width the kernel is built for.
 inline int paged_attn_width(int64_t head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
 
