@@ -123,8 +123,9 @@ int check_cache(const sdt_paged_cache *c) {
         return fail(SDT_ERR_SHAPE, "paged cache: pages, page size and heads must be positive, heads at most 65535 and pages * page size < 2^31");
     int rc = check_rows("k", c->k, c->k_page, c->k_token, c->k_head, q8 ? 1 : 2, 16);
     if (!rc) rc = check_rows("v", c->v, c->v_page, c->v_token, c->v_head, q8 ? 1 : 2, 16);
-    if (!rc && q8) rc = check_rows("k_scales", c->k_scales, c->ks_page, c->ks_token, c->ks_head, 2, 4);
-    if (!rc && q8) rc = check_rows("v_scales", c->v_scales, c->vs_page, c->vs_token, c->vs_head, 2, 4);
+    const int row = c->head_dim == 128 ? 8 : 4;  // scales are copied in pieces of this size
+    if (!rc && q8) rc = check_rows("k_scales", c->k_scales, c->ks_page, c->ks_token, c->ks_head, 2, row);
+    if (!rc && q8) rc = check_rows("v_scales", c->v_scales, c->vs_page, c->vs_token, c->vs_head, 2, row);
     return rc;
 }
 

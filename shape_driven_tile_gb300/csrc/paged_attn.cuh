@@ -46,8 +46,7 @@
 namespace sdt {
 
 constexpr float kAttnSlack = 8.f;  // log2 of the largest weight
-constexpr int kAttnJoin = 32;      // most pieces that one CTA joins at a time
-constexpr int kAttnFlat = 24;      // most pieces that are joined in one level
+constexpr int kAttnFlat = 256;     // most pieces x query heads that are joined in one level
 
 struct PagedAttnArgs {
     const char *q;             // strides in bytes
@@ -60,6 +59,7 @@ struct PagedAttnArgs {
     const int *lens;
     int batch, kv_heads, group, head_blocks;  // group: query heads per key head
     int head_dim, max_pages, num_pages, window;
+    int whole_pages;           // 1: any 16 consecutive keys of a unit lie in one page, fewer than 2^31 bytes apart
     FastDiv page;
     float scale_log2;          // scale * log2(e)
     int q_rows;                // query rows that a CTA keeps in shared memory: min(group, 8 NH WH)
@@ -86,18 +86,23 @@ struct AttnCfg {
     static constexpr int SLOT = ROWS * (DP + 2);          // floats of a partial
     static constexpr int QROW = DP * 2;                   // bytes of a query row in shared memory
     // Three stages where two CTAs (or more of one warp) still share an SM, else two; wide heads
-    // have the SM to themselves.
+    // have the SM to themselves.  q8 is bound by its arithmetic first: two stages and three CTAs.
     static constexpr bool fits(int s, int bytes) { return s * (STAGE + ROWS * QROW) + 2048 <= bytes; }
-    static constexpr int S = fits(3, 113 * 1024) || (!fits(2, 113 * 1024) && fits(3, 227 * 1024)) ? 3 : 2;
+    // An item costs about this many units besides its own (queries, join of the warps, output).  Four
+    // warps have larger units and few items: counting it would only leave CTAs without a unit.
+    static constexpr int COST = NW == 1 ? 1 : 0;
+    static constexpr int S = Q8 && DP <= 128 ? 2 : fits(3, 113 * 1024) || (!fits(2, 113 * 1024) && fits(3, 227 * 1024)) ? 3 : 2;
     static constexpr int smem(int q_rows) { return S * (STAGE + q_rows * QROW); }
     static_assert(fits(S, 227 * 1024), "shared memory of an SM");
     static_assert(STAGE >= NW * HEADS * DP * 4, "the stage must hold every warp's o");
-    static_assert(STAGE >= kAttnJoin * ROWS * 4, "the stage must hold a join's weights");
     static_assert(RW <= 32, "a lane describes one row");
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -165,6 +170,12 @@ __device__ __forceinline__ uint32_t widen_u8(uint32_t t) {
     const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&t), __half2half2(__ushort_as_half(0x6480)));
     return *reinterpret_cast<const uint32_t *>(&d);
 }
+// 2^x within 2^-22 (below 2^-126: 0); 2^-inf = 0.
+__device__ __forceinline__ float pow2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t v;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
@@ -184,10 +195,33 @@ __device__ __forceinline__ uint32_t q8_piece(uint32_t r, uint32_t c) {
     return DP >= 128 ? c ^ (((r & 3) ^ ((r >> 2) & 1)) << 1) : c ^ (((r >> 1) & 1) << 1);
 }
 
-// Where in the work a reader stands: unit j of n of item (b, h), keys [lo, len).
+// Where in the work a reader stands: unit j of n of item (b, h), keys [lo, len), at place v
+// of the whole work, where an item takes COST places and then one for each unit.
 struct AttnWalk {
     int b, h, j, n, lo, len;
+    long long v;
 };
+// What a CTA has computed of an item that it does not have whole.  An item's pieces lie with the
+// CTAs first .. first + n - 1, the first one's in its second slot, the others' in their first.  The
+// last CTA to arrive joins them; with many pieces, the last of a group of per_group joins the
+// group's over the group's first piece, and the last group's those.
+struct AttnPiece {
+    int b, h;
+    int first, n, per_group;
+};
+
+// a / b for 0 <= a, 0 < b: in 32 bits where they do
+__device__ __forceinline__ long long div_small(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+// Adds 1 and returns what was there; writes of this thread, and of those that it has met at a
+// barrier, are seen by whoever reads a later value here the same way.
+__device__ __forceinline__ unsigned add_acq_rel(unsigned *p) {
+    unsigned v;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
 
 template <typename T, int DP, int NH, int WH, int NW, bool Q8>
 __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs p) {
@@ -215,6 +249,13 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
     };
 
     griddep_launch_dependents();
+    // The chain lengths -> pages -> keys is three trips to memory: the tables set out for L2 with the
+    // lengths (all of them, spread over the grid; L2 is where memory is coherent, so before the wait).
+    {
+        const int64_t line = static_cast<int64_t>(blockIdx.x) * NTH + tid;
+        const int64_t bytes = ((p.batch - 1) * p.table_stride + p.max_pages) * 4;
+        if (line * 128 < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(p.table) + line * 128));
+    }
     griddep_wait();
 
     // ---- this CTA's share ----
@@ -229,13 +270,14 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
     // a thread's requests are consecutive: one scan over the threads' sums finds everything
     const int per = (p.batch + NTH - 1) / NTH;
     const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
-    long long mine = 0;
+    long long mine = 0, real = 0;  // places and units of this thread's requests, one head
 #pragma unroll 4
     for (int b = b0; b < b1; ++b) {
         int lo, len;
         if (range_of(b, lo, len) && blockIdx.x == 0) paged_status(p.status, kSiteLength);
-        mine += units_in(lo, len);
+        real += units_in(lo, len);
     }
+    mine = real + static_cast<long long>(b1 - b0) * C::COST;
     long long inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -244,29 +286,39 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
     }
     if (lane == 31) sh_sum[warp] = inc;
     cta_sync();
-    long long U = 0;
+    long long V = 0;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
         if (w < warp) inc += sh_sum[w];
-        U += sh_sum[w];
+        V += sh_sum[w];
     }
-    U *= H;
+    const long long U = (V - static_cast<long long>(p.batch) * C::COST) * H;  // units
+    V *= H;                                                                   // places
     const long long P = U < gridDim.x ? U : gridDim.x;  // CTAs with work
     const long long cta = blockIdx.x;
     if (cta >= P) return;
-    const long long u0 = U * cta / P, u1 = U * (cta + 1) / P;
-    if (u0 < inc * H && u0 >= (inc - mine) * H) {  // the first unit's request is one of this thread's
+    const long long v0 = div_small(V * cta, P), v1 = div_small(V * (cta + 1), P);
+    // The CTA i with place v, floor(V i / P) <= v < floor(V (i + 1) / P): V i < (v + 1) P <= V (i + 1).  In
+    // floats, with P < 2^12, the guess is off by one at most.
+    const float per_place = static_cast<float>(P) / static_cast<float>(V);
+    auto cta_of = [&](long long v) {
+        int i = static_cast<int>(static_cast<float>(v + 1) * per_place);
+        if (V * i >= (v + 1) * P) --i;
+        else if (V * (i + 1) < (v + 1) * P) ++i;
+        return i;
+    };
+    if (v0 < inc * H && v0 >= (inc - mine) * H) {  // place v0 is in one of this thread's requests
         long long at = (inc - mine) * H;
         int b = b0;
         for (; b < b1; ++b) {
             int lo, len;
             range_of(b, lo, len);
-            const long long n = static_cast<long long>(units_in(lo, len)) * H;
-            if (u0 < at + n) break;
+            const long long n = static_cast<long long>(units_in(lo, len) + C::COST) * H;
+            if (v0 < at + n) break;
             at += n;
         }
         sh_b = b;
-        sh_rest = u0 - at;
+        sh_rest = v0 - at;
     }
     cta_sync();
     auto enter = [&](AttnWalk &w) {  // the walk stands on request w.b
@@ -275,8 +327,10 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
         w.n = units_in(w.lo, w.len);
     };
     auto advance = [&](AttnWalk &w) {
+        ++w.v;
         if (++w.j == w.n) {
             w.j = 0;
+            w.v += C::COST;
             if (++w.h == H) {
                 w.h = 0;
                 ++w.b;
@@ -287,9 +341,14 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
     AttnWalk pw;  // the loads' place
     pw.b = sh_b;
     enter(pw);
-    pw.h = static_cast<int>(sh_rest / pw.n);
-    pw.j = static_cast<int>(sh_rest - static_cast<long long>(pw.h) * pw.n);
-    AttnWalk cw = pw;  // the products' place
+    pw.h = static_cast<int>(div_small(sh_rest, pw.n + C::COST));
+    {
+        const int at = static_cast<int>(sh_rest - static_cast<long long>(pw.h) * (pw.n + C::COST));
+        pw.j = max(at - C::COST, 0);
+        pw.v = v0 + pw.j + C::COST - at;
+    }
+    if (pw.v >= v1) return;  // a share without units
+    AttnWalk cw = pw;        // the products' place
 
     // ---- loads: lane r < RW describes row warp * RW + r of the unit ----
     int pg_id = -1, pg_off = 0, pg_head = 0;
@@ -311,30 +370,57 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
             paged_status(p.status, kSitePage);
             pg_ok = false;
         }
-        const int64_t ko = pg_ok ? p.k.at(pg_id, pg_off, pg_head) : -1;
-        const int64_t vo = pg_ok ? p.v.at(pg_id, pg_off, pg_head) : -1;
         constexpr int CPR = ROWB / 16, RPI = 32 / CPR;  // pieces per row, rows per instruction
         const uint32_t kdst = smem0 + stage * C::STAGE + warp * RW * ROWB, vdst = kdst + TK * ROWB;
         const int cc = lane % CPR, rr = lane / CPR;
+        auto place = [&](int r) { return r * ROWB + (Q8 ? q8_piece<DP>(r, cc) : static_cast<uint32_t>(cc ^ (r & 7))) * 16u; };
+        if (p.whole_pages) {
+            // 16 rows at a time lie in one page, token after token: one address and steps from it.  (A row
+            // past the range has zeros copied, but its address is still one of the page, or of page 0.)
 #pragma unroll
-        for (int it = 0; it < RW / RPI; ++it) {
-            const int r = it * RPI + rr;
-            const int64_t ka = __shfl_sync(0xffffffffu, ko, r), va = __shfl_sync(0xffffffffu, vo, r);
-            const uint32_t pos = r * ROWB + (Q8 ? q8_piece<DP>(r, cc) : static_cast<uint32_t>(cc ^ (r & 7))) * 16u;
-            const int n = ka >= 0 && cc < pieces ? 16 : 0;
-            cp_async16(kdst + pos, n ? p.k.base + ka + cc * 16 : p.k.base, n);
-            cp_async16(vdst + pos, n ? p.v.base + va + cc * 16 : p.v.base, n);
+            for (int r0 = 0; r0 < RW; r0 += 16) {
+                const int id = __shfl_sync(0xffffffffu, pg_ok ? pg_id : -1, r0), off = __shfl_sync(0xffffffffu, pg_off, r0);
+                const int have = id >= 0 && cc < pieces ? pw.len - (pw.lo + pw.j * TK + warp * RW + r0) - rr : 0;
+                const int col = cc < pieces ? cc * 16 : 0;
+                const char *ka = p.k.base + (p.k.at(max(id, 0), id >= 0 ? off + rr : rr, pg_head) + col);
+                const char *va = p.v.base + (p.v.at(max(id, 0), id >= 0 ? off + rr : rr, pg_head) + col);
+                const int k_step = static_cast<int>(p.k.token), v_step = static_cast<int>(p.v.token);
+#pragma unroll
+                for (int it = 0; it < 16 / RPI; ++it) {
+                    const uint32_t pos = place(r0 + it * RPI + rr);
+                    const int n = it * RPI < have ? 16 : 0;
+                    cp_async16(kdst + pos, ka + static_cast<int64_t>(k_step) * (it * RPI), n);
+                    cp_async16(vdst + pos, va + static_cast<int64_t>(v_step) * (it * RPI), n);
+                }
+            }
+        } else {
+            const int64_t ko = pg_ok ? p.k.at(pg_id, pg_off, pg_head) : -1;
+            const int64_t vo = pg_ok ? p.v.at(pg_id, pg_off, pg_head) : -1;
+#pragma unroll
+            for (int it = 0; it < RW / RPI; ++it) {
+                const int r = it * RPI + rr;
+                const int64_t ka = __shfl_sync(0xffffffffu, ko, r), va = __shfl_sync(0xffffffffu, vo, r);
+                const uint32_t pos = place(r);
+                const int n = ka >= 0 && cc < pieces ? 16 : 0;
+                cp_async16(kdst + pos, n ? p.k.base + ka + cc * 16 : p.k.base, n);
+                cp_async16(vdst + pos, n ? p.v.base + va + cc * 16 : p.v.base, n);
+            }
         }
         if constexpr (Q8) {
             if (lane < RW) {
                 const uint32_t sdst = smem0 + stage * C::STAGE + 2 * TK * ROWB + (warp * RW + lane) * C::SCB;
                 const char *ks = pg_ok ? p.ks.base + p.ks.at(pg_id, pg_off, pg_head) : p.ks.base;
                 const char *vs = pg_ok ? p.vs.base + p.vs.at(pg_id, pg_off, pg_head) : p.vs.base;
+                if constexpr (DP == 128) {  // four scales, aligned to their size
+                    cp_async8(sdst, ks, pg_ok ? 8 : 0);
+                    cp_async8(sdst + TK * C::SCB, vs, pg_ok ? 8 : 0);
+                } else {
 #pragma unroll
-                for (int i = 0; i < DP / 64; ++i) {
-                    const int n = pg_ok && i * 64 < p.head_dim ? 4 : 0;
-                    cp_async4(sdst + i * 4, ks + (n ? i * 4 : 0), n);
-                    cp_async4(sdst + TK * C::SCB + i * 4, vs + (n ? i * 4 : 0), n);
+                    for (int i = 0; i < DP / 64; ++i) {
+                        const int n = pg_ok && i * 64 < p.head_dim ? 4 : 0;
+                        cp_async4(sdst + i * 4, ks + (n ? i * 4 : 0), n);
+                        cp_async4(sdst + TK * C::SCB + i * 4, vs + (n ? i * 4 : 0), n);
+                    }
                 }
             }
         }
@@ -419,30 +505,162 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
 
     // ---- prologue: S - 1 units in flight, the page ids of the next ----
     look_up();
-    long long issued = u0;
 #pragma unroll
     for (int s = 0; s < S - 1; ++s) {
-        if (issued < u1) {
+        if (pw.v < v1) {
             issue(s);
-            ++issued;
             advance(pw);
-            if (issued < u1) look_up();
+            if (pw.v < v1) look_up();
         }
         cp_async_commit();
     }
 
+    // ---- an item's end ----
+    auto heads_of = [&](int h) { return min(p.group - (h % p.head_blocks) * C::ROWS, C::ROWS); };  // query heads of the block
+    auto store = [&](int b, int h, int r, int col, const float4 &v, float M, float L) {
+        const int head = (h / p.head_blocks) * p.group + (h % p.head_blocks) * C::ROWS + r;
+        const float inv = L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;  // no key: zeros; a NaN sum stays NaN
+        if (col < p.head_dim)
+            *reinterpret_cast<uint2 *>(p.out + b * p.o_batch + static_cast<int64_t>(head) * p.o_head + col * 2) =
+                make_uint2(pack2<T>(v.x * inv, v.y * inv), pack2<T>(v.z * inv, v.w * inv));
+        if (p.lse && col == 0)
+            p.lse[static_cast<int64_t>(b) * p.kv_heads * p.group + head] = L == 0.f ? -INFINITY : M * 0.6931471805599453f + logf(L);
+    };
+    // The item of the walk, v the place of its first unit.
+    auto piece_of = [&](const AttnWalk &w, long long v) {
+        AttnPiece i;
+        i.b = w.b;
+        i.h = w.h;
+        i.first = cta_of(v);
+        i.n = cta_of(v + w.n - 1) - i.first + 1;
+        i.per_group = i.n;
+        if (i.n > 16 && i.n * heads_of(w.h) > kAttnFlat) {
+            i.per_group = 16;
+            while (i.per_group * i.per_group < i.n) i.per_group += 4;
+        }
+        return i;
+    };
+    // The counter of this CTA's group.  An item's first group counts at its first CTA, the others at
+    // theirs in a field of their own, where no other item has a group that is not its first; a second
+    // level counts in a third field.
+    auto counter_of = [&](const AttnPiece &i) {
+        const int at = static_cast<int>(cta) - i.first;
+        return p.counters + (at < i.per_group ? i.first : static_cast<int>(gridDim.x) + i.first + at / i.per_group * i.per_group);
+    };
+    // Joins `count` pieces i0, i0 + step, ... of the item, to the output or over piece i0.  The ring is
+    // free by now: EB float4 of o per thread and piece come through it, as many pieces at once as it
+    // holds, so that a join costs one trip to L2 and not one per few pieces.
+    auto join = [&](const AttnPiece &item, int i0, int step, int count, bool final) {
+        constexpr int EB = 4, BLOCK = EB * NTH;             // float4 of o at a time
+        constexpr int HELD = BLOCK * 16 + 2 * C::ROWS * 4;  // bytes of a piece in the ring: o, m, l
+        constexpr int AT_ONCE = S * C::STAGE / HELD;
+        static_assert(AT_ONCE >= 2, "a join makes progress");
+        const float *base = p.partials + static_cast<size_t>(2 * item.first) * C::SLOT;
+        auto at = [&](int i) { return base + static_cast<size_t>(i == 0 ? 1 : 2 * i) * C::SLOT; };
+        const int all = heads_of(item.h) * (DP / 4);
+        for (int e0 = 0; e0 < all; e0 += BLOCK) {
+            const int block = min(BLOCK, all - e0);
+            float M[EB], L[EB];
+            float4 acc[EB];
+#pragma unroll
+            for (int x = 0; x < EB; ++x) {
+                M[x] = -INFINITY;
+                L[x] = 0.f;
+                acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            for (int c0 = 0; c0 < count; c0 += AT_ONCE) {
+                const int n = min(AT_ONCE, count - c0);
+                for (int i = 0; i < n; ++i) {
+                    const float *src = at(i0 + (c0 + i) * step);
+                    const uint32_t dst = smem0 + i * HELD;
+#pragma unroll
+                    for (int x = 0; x < EB; ++x)
+                        if (x * NTH + tid < block) cp_async16(dst + (x * NTH + tid) * 16, src + (e0 + x * NTH + tid) * 4, 16);
+                    for (int x = tid; x < C::ROWS / 2; x += NTH) cp_async16(dst + BLOCK * 16 + x * 16, src + C::ROWS * DP + x * 4, 16);
+                }
+                cp_async_commit();
+                cp_async_wait<0>();
+                cta_sync();
+#pragma unroll
+                for (int x = 0; x < EB; ++x) {
+                    const int e = x * NTH + tid, r = (e0 + e) / (DP / 4);
+                    if (e >= block) break;
+                    auto held = [&](int i) { return reinterpret_cast<const float *>(smem + i * HELD); };
+                    float top = M[x];
+#pragma unroll 4
+                    for (int i = 0; i < n; ++i) top = fmaxf(top, held(i)[BLOCK * 4 + r]);
+                    const float f = M[x] == top ? 1.f : pow2(M[x] - top);
+                    M[x] = top;
+                    L[x] *= f;
+                    acc[x].x *= f;
+                    acc[x].y *= f;
+                    acc[x].z *= f;
+                    acc[x].w *= f;
+#pragma unroll 4
+                    for (int i = 0; i < n; ++i) {
+                        const float mi = held(i)[BLOCK * 4 + r];
+                        const float w = mi == top ? 1.f : pow2(mi - top);  // (both -inf: zeros either way)
+                        const float4 v = *reinterpret_cast<const float4 *>(held(i) + e * 4);
+                        L[x] += held(i)[BLOCK * 4 + C::ROWS + r] * w;
+                        acc[x].x += v.x * w;
+                        acc[x].y += v.y * w;
+                        acc[x].z += v.z * w;
+                        acc[x].w += v.w * w;
+                    }
+                }
+                cta_sync();
+            }
+#pragma unroll
+            for (int x = 0; x < EB; ++x) {
+                const int e = e0 + x * NTH + tid, r = e / (DP / 4), col = (e % (DP / 4)) * 4;
+                if (e >= e0 + block) break;
+                if (final) {
+                    store(item.b, item.h, r, col, acc[x], M[x], L[x]);
+                } else {  // (the piece's own m and l are still read for the next block: they change at the end)
+                    *reinterpret_cast<float4 *>(const_cast<float *>(at(i0)) + e * 4) = acc[x];
+                    if (col == 0) {
+                        st_m[r / C::HEADS][r % C::HEADS] = M[x];
+                        st_l[r / C::HEADS][r % C::HEADS] = L[x];
+                    }
+                }
+            }
+        }
+        if (!final) {
+            cta_sync();
+            for (int r = tid; r < heads_of(item.h); r += NTH) {
+                const_cast<float *>(at(i0))[C::ROWS * DP + r] = st_m[r / C::HEADS][r % C::HEADS];
+                const_cast<float *>(at(i0))[C::ROWS * (DP + 1) + r] = st_l[r / C::HEADS][r % C::HEADS];
+            }
+            cta_sync();
+        }
+    };
+
     int stage = 0;
     bool fresh = true;
-    for (long long u = u0; u < u1; ++u) {
+    // Pieces that this CTA shares with others: of the item that its share begins inside, and of the one
+    // that it ends inside.  Whether they are complete is asked at the end, when the answer has come.
+    AttnPiece begun{}, left_open{};
+    unsigned begun_ticket = 0, left_ticket = 0;  // thread 0's
+    bool has_begun = false, has_left = false;
+    while (cw.v < v1) {
+        if (fresh) {  // (while the unit is on its way)
+            const long long v = cw.v - cw.j;
+            if (v < v0) {
+                has_begun = true;
+                begun = piece_of(cw, v);
+            } else if (v + cw.n > v1) {
+                has_left = true;
+                left_open = piece_of(cw, v);
+            }
+        }
         cp_async_wait<S - 2>();
         group_sync();
         {
             const int st = stage == 0 ? S - 1 : stage - 1;  // consumed in the previous round
-            if (issued < u1) {
+            if (pw.v < v1) {
                 issue(st);
-                ++issued;
                 advance(pw);
-                if (issued < u1) look_up();
+                if (pw.v < v1) look_up();
             }
             cp_async_commit();
         }
@@ -551,7 +769,7 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
                         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
                         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
                         y = fmaxf(y, m[nt][i]);
-                        a[i] = y == m[nt][i] ? 1.f : exp2f(m[nt][i] - y);
+                        a[i] = y == m[nt][i] ? 1.f : pow2(m[nt][i] - y);
                         m[nt][i] = y;
                         l[nt][i] *= a[i];
                     }
@@ -570,10 +788,10 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
                 const float e0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], e1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
 #pragma unroll
                 for (int i = 0; i < KT; ++i) {
-                    s[i][nt][0] = exp2f(s[i][nt][0] - e0);
-                    s[i][nt][1] = exp2f(s[i][nt][1] - e1);
-                    s[i][nt][2] = exp2f(s[i][nt][2] - e0);
-                    s[i][nt][3] = exp2f(s[i][nt][3] - e1);
+                    s[i][nt][0] = pow2(s[i][nt][0] - e0);
+                    s[i][nt][1] = pow2(s[i][nt][1] - e1);
+                    s[i][nt][2] = pow2(s[i][nt][2] - e0);
+                    s[i][nt][3] = pow2(s[i][nt][3] - e1);
                     l[nt][0] += s[i][nt][0] + s[i][nt][2];
                     l[nt][1] += s[i][nt][1] + s[i][nt][3];
                 }
@@ -631,6 +849,12 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
                 }
                 const float up = __uint_as_float(static_cast<uint32_t>(127 + 30 - static_cast<int>(kAttnSlack) - v_exp) << 23);
 #pragma unroll
+                for (int i = 0; i < KT; ++i)
+#pragma unroll
+                    for (int nt = 0; nt < NH; ++nt)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) s[i][nt][y] *= up;
+#pragma unroll
                 for (int i = 0; i < KT; ++i) {
                     const uint32_t r = k0 + i * 16 + 2 * c;  // this thread's keys in the values: r, r+1, r+8, r+9
 #pragma unroll
@@ -642,7 +866,7 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
                             w[t] = lds32(vt + rt * ROWB + q8_piece<DP>(rt, gr * 2 + (g >> 2)) * 16 + (g & 3) * 4) ^ 0x80808080u;
                         }
                         const float2 y0 = unpack2<__half>(xs[i][0][gr >> 1]), y1 = unpack2<__half>(xs[i][1][gr >> 1]);
-                        const float f0 = (gr & 1 ? y0.y : y0.x) * up, f1 = (gr & 1 ? y1.y : y1.x) * up;
+                        const float f0 = gr & 1 ? y0.y : y0.x, f1 = gr & 1 ? y1.y : y1.x;
                         uint32_t hi[NH][2], lo[NH][2];
 #pragma unroll
                         for (int nt = 0; nt < NH; ++nt)
@@ -661,10 +885,10 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
                         for (int t = 0; t < 2; ++t) {  // rows g and g + 8 of the tile: values 4 g + 2 t and + 1 of the group
                             uint32_t a[4];
 #pragma unroll
-                            for (int y = 0; y < 4; ++y) {
-                                const uint32_t j = 2 * t + (y & 1), pair = (y >> 1) * 2;
-                                a[y] = __byte_perm(w[pair], w[pair + 1], j | ((4 + j) << 8));
-                                a[y] = widen_u8((a[y] & 0x00ff00ffu) | 0x64006400u);
+                            for (int y = 0; y < 2; ++y) {  // bytes 2 t and 2 t + 1 of two neighbouring keys, interleaved
+                                const uint32_t x = __byte_perm(w[2 * y], w[2 * y + 1], t ? 0x7362 : 0x5140);
+                                a[2 * y] = widen_u8(__byte_perm(x, 0x64646464u, 0x4140));
+                                a[2 * y + 1] = widen_u8(__byte_perm(x, 0x64646464u, 0x4342));
                             }
 #pragma unroll
                             for (int nt = 0; nt < NH; ++nt) {
@@ -677,8 +901,7 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
             }
         }
 
-        const bool item_done = cw.j == cw.n - 1;
-        if (item_done || u == u1 - 1) {
+        if (cw.j == cw.n - 1 || cw.v == v1 - 1) {
             // ---- the CTA's piece of the item: join the warps through the stage just read ----
             const float back = Q8 ? __uint_as_float(static_cast<uint32_t>(127 - 30 + static_cast<int>(kAttnSlack) + v_exp) << 23) : 1.f;
 #pragma unroll
@@ -689,9 +912,10 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
                     l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], 8);
                     l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], 16);
                 }
+            const bool begun_here = cw.v - cw.j >= v0, whole = begun_here && cw.v - cw.j + cw.n <= v1;
             cta_sync();  // every warp has read the stage
             float *ob = reinterpret_cast<float *>(smem + stage * C::STAGE);
-            const int valid = min(p.group - (cw.h % p.head_blocks) * C::ROWS, C::ROWS);  // query heads of this block
+            const int valid = heads_of(cw.h);
 #pragma unroll
             for (int nt = 0; nt < NH; ++nt)
 #pragma unroll
@@ -720,19 +944,7 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
                 }
             cta_sync();
 
-            const long long first_unit = u - cw.j, end_unit = first_unit + cw.n;
-            const bool whole = first_unit >= u0 && end_unit <= u1;
-            const int head0 = (cw.h / p.head_blocks) * p.group + (cw.h % p.head_blocks) * C::ROWS;
-            auto store = [&](int r, int col, const float4 &v, float M, float L) {
-                const float inv = L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;  // no key: zeros; a NaN sum stays NaN
-                if (col < p.head_dim)
-                    *reinterpret_cast<uint2 *>(p.out + cw.b * p.o_batch + static_cast<int64_t>(head0 + r) * p.o_head + col * 2) =
-                        make_uint2(pack2<T>(v.x * inv, v.y * inv), pack2<T>(v.z * inv, v.w * inv));
-                if (p.lse && col == 0)
-                    p.lse[static_cast<int64_t>(cw.b) * p.kv_heads * p.group + head0 + r] =
-                        L == 0.f ? -INFINITY : M * 0.6931471805599453f + logf(L);
-            };
-            float *slot = p.partials + static_cast<size_t>(2 * cta + (first_unit >= u0 ? 1 : 0)) * C::SLOT;
+            float *slot = p.partials + static_cast<size_t>(2 * cta + (begun_here ? 1 : 0)) * C::SLOT;
             for (int e = tid; e < valid * (DP / 4); e += NTH) {
                 const int r = e / (DP / 4), col = (e % (DP / 4)) * 4, rw = r / C::HEADS, rr = r % C::HEADS;
                 float M = st_m[rw][rr];
@@ -743,7 +955,7 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
 #pragma unroll
                 for (int w = 0; w < C::WK; ++w) {
                     const float mw = st_m[w * WH + rw][rr];
-                    const float f = mw == M ? 1.f : exp2f(mw - M);  // (both -inf: zeros either way)
+                    const float f = mw == M ? 1.f : pow2(mw - M);  // (both -inf: zeros either way)
                     const float4 v = *reinterpret_cast<const float4 *>(ob + ((w * WH + rw) * C::HEADS + rr) * DP + (col ^ (((rr >> 1) & 3) << 3)));
                     L += st_l[w * WH + rw][rr] * f;
                     acc.x += v.x * f;
@@ -752,7 +964,7 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
                     acc.w += v.w * f;
                 }
                 if (whole) {
-                    store(r, col, acc, M, L);
+                    store(cw.b, cw.h, r, col, acc, M, L);
                 } else {
                     *reinterpret_cast<float4 *>(slot + r * DP + col) = acc;
                     if (col == 0) {
@@ -761,96 +973,42 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
                     }
                 }
             }
-            cta_sync();  // the stage and the statistics may be written again
-            if (!whole) {
-                // ---- the item's pieces: the last CTA to arrive joins them.  More than kAttnFlat pieces
-                // join in two levels of at most kAttnJoin (the grid has at most its square of CTAs) ----
-                const long long first_cta = ((first_unit + 1) * P - 1) / U, last_cta = (end_unit * P - 1) / U;
-                const int n = static_cast<int>(last_cta - first_cta) + 1;
-                // piece 0 lies in its CTA's second slot, the others in their first
-                auto piece = [&](int i) { return p.partials + static_cast<size_t>(2 * (first_cta + i) + (i == 0 ? 1 : 0)) * C::SLOT; };
-                float *weights = ob;  // [pieces][ROWS]
-                // Counts an arrival; true in all threads of the last of `all` to arrive.
-                auto arrive = [&](unsigned *counter, int all) {
-                    if (tid == 0) {
-                        __threadfence();
-                        const bool last = atomicAdd(counter, 1u) == static_cast<unsigned>(all - 1);
-                        if (last) {
-                            *counter = 0;
-                            __threadfence();
-                        }
-                        sh_last = last;
-                    }
-                    cta_sync();
-                    return sh_last != 0;
-                };
-                // Joins `count` pieces i0, i0 + step, ...; to the output or over piece i0.
-                auto join = [&](int i0, int step, int count, bool final) {
-                    for (int r = warp; r < valid; r += NW) {
-                        float M = -INFINITY, L = 0.f;
-                        const float mi = lane < count ? __ldcg(piece(i0 + lane * step) + C::ROWS * DP + r) : -INFINITY;
-                        const float li = lane < count ? __ldcg(piece(i0 + lane * step) + C::ROWS * (DP + 1) + r) : 0.f;
-                        M = mi;
-#pragma unroll
-                        for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-                        const float f = mi == M ? 1.f : exp2f(mi - M);
-                        L = li * f;
-#pragma unroll
-                        for (int x = 16; x > 0; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
-                        if (lane < count) weights[lane * C::ROWS + r] = f;
-                        if (lane == 0) {
-                            st_m[r / C::HEADS][r % C::HEADS] = M;
-                            st_l[r / C::HEADS][r % C::HEADS] = L;
-                        }
-                    }
-                    cta_sync();
-                    for (int e = tid; e < valid * (DP / 4); e += NTH) {
-                        const int r = e / (DP / 4), col = (e % (DP / 4)) * 4;
-                        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                        for (int i = 0; i < count; ++i) {
-                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(piece(i0 + i * step) + r * DP + col));
-                            const float f = weights[i * C::ROWS + r];
-                            acc.x += v.x * f;
-                            acc.y += v.y * f;
-                            acc.z += v.z * f;
-                            acc.w += v.w * f;
-                        }
-                        const float M = st_m[r / C::HEADS][r % C::HEADS], L = st_l[r / C::HEADS][r % C::HEADS];
-                        if (final) {
-                            store(r, col, acc, M, L);
-                        } else {
-                            float *to = piece(i0);
-                            *reinterpret_cast<float4 *>(to + r * DP + col) = acc;
-                            if (col == 0) {
-                                to[C::ROWS * DP + r] = M;
-                                to[C::ROWS * (DP + 1) + r] = L;
-                            }
-                        }
-                    }
-                    cta_sync();
-                };
-                unsigned *count_item = p.counters + first_cta;
-                if (n <= kAttnFlat) {
-                    if (arrive(count_item, n)) join(0, 1, n, true);
-                } else {
-                    const int per_group = max((n + kAttnJoin - 1) / kAttnJoin, 16), groups = (n + per_group - 1) / per_group;
-                    const int mine = static_cast<int>(cta - first_cta) / per_group, i0 = mine * per_group, in = min(per_group, n - i0);
-                    // an item's first group counts beside the item's own counter, the others at their first
-                    // CTA, where no other item has a group that is not its first
-                    unsigned *count_group = p.counters + (mine == 0 ? gridDim.x + first_cta : 2 * gridDim.x + first_cta + i0);
-                    if (arrive(count_group, in)) {
-                        join(i0, 1, in, false);
-                        if (arrive(count_item, groups)) join(0, per_group, groups, true);
-                    }
-                }
+            cta_sync();  // the stage and the statistics may be written again; a piece is whole in the workspace
+            if (!whole && tid == 0) {
+                if (begun_here) left_ticket = add_acq_rel(counter_of(left_open));
+                else begun_ticket = add_acq_rel(counter_of(begun));
             }
             fresh = true;
         }
         advance(cw);
         if (++stage == S) stage = 0;
     }
-    cp_async_wait<0>();
+#pragma unroll 1
+    for (int x = 0; x < 2; ++x) {
+        if (!(x == 0 ? has_begun : has_left)) continue;
+        const AttnPiece item = x == 0 ? begun : left_open;
+        unsigned t = x == 0 ? begun_ticket : left_ticket;
+        unsigned *counter = counter_of(item);
+        int i0 = (static_cast<int>(cta) - item.first) / item.per_group * item.per_group, step = 1, count = min(item.per_group, item.n - i0);
+#pragma unroll 1
+        while (true) {
+            if (tid == 0) {
+                sh_last = t == static_cast<unsigned>(count - 1);
+                if (sh_last) *counter = 0;
+            }
+            cta_sync();
+            if (!sh_last) break;
+            const bool final = step > 1 || item.per_group == item.n;
+            join(item, i0, step, count, final);
+            if (final) break;
+            counter = p.counters + 2 * gridDim.x + item.first;
+            if (tid == 0) t = add_acq_rel(counter);
+            i0 = 0;
+            step = item.per_group;
+            count = (item.n + item.per_group - 1) / item.per_group;
+        }
+        cta_sync();  // sh_last is written again
+    }
 }
 
 }  // namespace sdt

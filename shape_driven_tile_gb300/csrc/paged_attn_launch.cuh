@@ -36,7 +36,7 @@ static cudaError_t launch_variant(PagedAttnArgs a, const PagedAttnLaunch &l) {
     if (e != cudaSuccess) return e;
     const int64_t keys = (l.max_keys + C::TK - 1) / C::TK;
     const int64_t units = std::max<int64_t>(keys, 1) * a.batch * a.kv_heads * a.head_blocks;  // no mix of lengths has more
-    const int64_t slots = std::min<int64_t>(static_cast<int64_t>(l.sm_count) * ctas, kAttnJoin * kAttnJoin);
+    const int64_t slots = static_cast<int64_t>(l.sm_count) * ctas;
     return launch_kernel(paged_attn_kernel<T, DP, NH, WH, NW, Q8>, dim3(static_cast<unsigned>(std::min(units, slots))),
                          dim3(C::THREADS), C::smem(a.q_rows), l.stream, 1, a);
 }

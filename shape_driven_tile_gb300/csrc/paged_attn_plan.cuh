@@ -21,8 +21,8 @@ struct PagedAttnLaunch {
     cudaStream_t stream;
 };
 
-// CTAs of nw warps per SM, at most: more of one warp would pass the join's 1024 on 152 SMs.
-inline int paged_attn_ctas(int nw) { return nw == 1 ? 6 : 2; }
+// CTAs of nw warps per SM, at most.
+inline int paged_attn_ctas(int nw) { return nw == 1 ? 8 : 3; }
 
 // `group` query heads per key head; keys are read once for up to 64 of them.  `items`:
 // requests x key heads.

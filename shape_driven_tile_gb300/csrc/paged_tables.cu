@@ -13,6 +13,8 @@
 // another launch or CTA, keeps them in shared memory and finds the request of a token or of
 // a fresh page by bisection.  A slot on a fresh page takes its page from `free`, not from
 // the table entry that another CTA may be writing.
+#include <atomic>
+
 #include "launch.cuh"
 #include "paged.cuh"
 #include "ptx.cuh"
@@ -160,8 +162,13 @@ extern "C" int paged_tables(int64_t batch, int64_t page_size, int64_t max_pages,
                  static_cast<int>(batch), static_cast<int>(max_pages), static_cast<int>(num_free),
                  FastDiv::of(static_cast<uint32_t>(page_size))};
     const size_t smem = 2 * sizeof(int) * static_cast<size_t>(batch);
-    cudaError_t e = cudaFuncSetAttribute(paged_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         2 * static_cast<int>(sizeof(int)) * kTablesMaxBatch);
+    static std::atomic<bool> ready[kMaxDevices];  // the attribute call takes longer than the launch: once a device
+    cudaError_t e = cudaSuccess;
+    if (!ready[dev.device].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(paged_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 2 * static_cast<int>(sizeof(int)) * kTablesMaxBatch);
+        if (e == cudaSuccess) ready[dev.device].store(true, std::memory_order_release);
+    }
     if (e == cudaSuccess) {
         const int64_t want = (num_slots + kTablesThreads * kTablesPerThread - 1) / (kTablesThreads * kTablesPerThread);
         const int64_t grid = want < 1 ? 1 : want > dev.sm_count ? dev.sm_count : want;

@@ -8,7 +8,6 @@ the current stream, without a synchronisation, so a step can be captured in a CU
 from __future__ import annotations
 
 import ctypes
-import math
 
 import torch
 
@@ -18,14 +17,30 @@ GROUP = 32  # values per fp16 scale of a q8 cache
 DTYPE_CODES = {torch.float16: 0, torch.bfloat16: 1, torch.int8: 2}
 
 
+# A decode step calls these once a layer, so a call's own time counts: the library's functions
+# are looked up once, the current stream is asked for as the raw handle, and a tensor that is
+# as it should be passes one comparison.
+_current_stream = torch._C._cuda_getCurrentRawStream
+_functions = {}
+
+
+def _fn(name):
+    f = _functions.get(name)
+    if f is None:
+        f = _functions[name] = getattr(lib(), name)
+    return f
+
+
 def _stream(stream, device):
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        return _current_stream(device)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def _tensor(t, name, dtype, ndim, device=None):
     """A CUDA tensor on the current device (or on `device`, already known to be it)."""
+    if type(t) is torch.Tensor and t.dtype is dtype and t.dim() == ndim and t.get_device() == device:
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
@@ -42,6 +57,9 @@ def _tensor(t, name, dtype, ndim, device=None):
 
 
 def _vector(t, name, dtype, n, device):
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == device and t.dim() == 1 and t.is_contiguous()
+            and (n is None or len(t) == n)):
+        return
     _tensor(t, name, dtype, 1, device)
     if n is not None and t.shape[0] != n:
         raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
@@ -94,7 +112,7 @@ class PagedCache:
 def _cache(cache):
     if not isinstance(cache, PagedCache):
         raise TypeError("cache must be a PagedCache")
-    if cache.device_index != torch.cuda.current_device():
+    if cache.device_index != torch._C._cuda_getDevice():
         raise ValueError(f"the cache is on cuda:{cache.device_index}, but the current device is "
                          f"cuda:{torch.cuda.current_device()}")
     return cache.device_index
@@ -121,23 +139,17 @@ def paged_tables(lens, new_tokens, free_pages, table, *, page_size: int, slots, 
     _vector(slots, "slots", torch.int64, None, dev)
     if table.shape[0] != batch or (table.stride(1) != 1 and table.shape[1] > 1):
         raise ValueError(f"table must be [{batch}, max_pages] with contiguous rows")
-    own = batch * 2 + 2  # one allocation for the outputs that the caller did not bring
-    buf = None if None not in (kv_lens, starts, used) else torch.empty(own, dtype=torch.int32, device=lens.device)
-    if kv_lens is None:
-        kv_lens = buf[:batch]
-    else:
-        _vector(kv_lens, "kv_lens", torch.int32, batch, dev)
-    if starts is None:
-        starts = buf[batch:2 * batch + 1]
-    else:
-        _vector(starts, "starts", torch.int32, batch + 1, dev)
-    if used is None:
-        used = buf[2 * batch + 1:]
-    else:
-        _vector(used, "used", torch.int32, 1, dev)
+    if kv_lens is None or starts is None or used is None:  # one allocation serves them all
+        mine = torch.empty(2 * batch + 2, dtype=torch.int32, device=lens.device).split((batch, batch + 1, 1))
+        kv_lens = mine[0] if kv_lens is None else kv_lens
+        starts = mine[1] if starts is None else starts
+        used = mine[2] if used is None else used
+    _vector(kv_lens, "kv_lens", torch.int32, batch, dev)
+    _vector(starts, "starts", torch.int32, batch + 1, dev)
+    _vector(used, "used", torch.int32, 1, dev)
     if batch == 0:
         raise SdtError(-3, "paged_tables: batch must be at least 1")
-    check(lib().paged_tables(batch, page_size, table.shape[1], lens.data_ptr(), new_tokens.data_ptr(),
+    check(_fn("paged_tables")(batch, page_size, table.shape[1], lens.data_ptr(), new_tokens.data_ptr(),
                              free_pages.data_ptr(), free_pages.shape[0], table.data_ptr(),
                              table.stride(0) if batch > 1 else table.shape[1], kv_lens.data_ptr(), starts.data_ptr(),
                              slots.data_ptr(), slots.shape[0], used.data_ptr(), _stream(stream, dev)))
@@ -161,7 +173,7 @@ def paged_append(k, v, slots, cache: PagedCache, *, stream=None) -> PagedCache:
     if k.stride(2) != 1 or v.stride(2) != 1:
         raise ValueError("k and v must be contiguous in their last dimension")
     _vector(slots, "slots", torch.int64, tokens, dev)
-    check(lib().paged_append(tokens, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1),
+    check(_fn("paged_append")(tokens, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1),
                              DTYPE_CODES[dtype], slots.data_ptr(), cache._ref, _stream(stream, dev)))
     return cache
 
@@ -174,7 +186,7 @@ def paged_attn_workspace(q_heads: int, kv_heads: int, head_dim: int, device=None
     ws = torch.empty(nbytes + 256, dtype=torch.uint8, device=device or "cuda")
     off = (-ws.data_ptr()) % 256
     ws = ws[off:off + nbytes]
-    check(lib().sdt_splitk_workspace_init(ws.data_ptr(), nbytes, _stream(None, None)))
+    check(lib().sdt_splitk_workspace_init(ws.data_ptr(), nbytes, _stream(None, ws.get_device())))
     return ws
 
 
@@ -200,13 +212,14 @@ def paged_attn_m1(q, cache: PagedCache, table, lens, out=None, *, workspace, sca
     if q.stride(2) != 1:
         raise ValueError("q must be contiguous in its last dimension")
     if out is None:
-        out = torch.empty((batch, q_heads, head_dim), dtype=dtype, device=q.device)
+        out = torch.empty_like(q) if q.is_contiguous() else torch.empty(q.shape, dtype=dtype, device=q.device)
     else:
         _tensor(out, "out", dtype, 3, dev)
         if out.shape != q.shape or out.stride(2) != 1:
             raise ValueError(f"out must be {tuple(q.shape)}, contiguous in its last dimension")
     _tensor(table, "table", torch.int32, 2, dev)
-    if table.shape[0] != batch or (table.stride(1) != 1 and table.shape[1] > 1):
+    rows, wide = table.shape
+    if rows != batch or (wide > 1 and table.stride(1) != 1):
         raise ValueError(f"table must be [{batch}, max_pages] with contiguous rows")
     _vector(lens, "lens", torch.int32, batch, dev)
     if lse is not None:
@@ -214,13 +227,13 @@ def paged_attn_m1(q, cache: PagedCache, table, lens, out=None, *, workspace, sca
         if lse.shape != (batch, q_heads) or not lse.is_contiguous():
             raise ValueError(f"lse must be contiguous {(batch, q_heads)}")
     _vector(workspace, "workspace", torch.uint8, None, dev)
+    # (a dimension of one never steps: its stride may be anything)
     qb, qh, _ = q.stride()
     ob, oh, _ = out.stride()
-    check(lib().paged_attn_m1(batch, q_heads, q.data_ptr(), qb if batch > 1 else 0, qh if q_heads > 1 else 0,
-                              DTYPE_CODES[dtype], cache._ref, table.data_ptr(),
-                              table.stride(0) if batch > 1 else table.shape[1], table.shape[1], lens.data_ptr(), window,
-                              1.0 / math.sqrt(head_dim) if scale is None else scale, out.data_ptr(),
-                              ob if batch > 1 else 0, oh if q_heads > 1 else 0,
-                              None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.shape[0],
-                              _stream(stream, dev)))
+    check(_fn("paged_attn_m1")(batch, q_heads, q.data_ptr(), qb if batch > 1 else 0, qh if q_heads > 1 else 0,
+                               DTYPE_CODES[dtype], cache._ref, table.data_ptr(), table.stride(0) if batch > 1 else wide,
+                               wide, lens.data_ptr(), window, head_dim ** -0.5 if scale is None else scale,
+                               out.data_ptr(), ob if batch > 1 else 0, oh if q_heads > 1 else 0,
+                               None if lse is None else lse.data_ptr(), workspace.data_ptr(), len(workspace),
+                               _stream(stream, dev)))
     return out
