@@ -1,13 +1,21 @@
 // paged_append.cu -- new keys and values into a paged cache: cache[slot[t]] = x[t], as they
 // are or as q8 (int8 and one fp16 scale per 32 values, gemv_m1_q8's weight format).
 //
-// q8 of one group of 32 values: s = fp16(max|x| * fl32(1/127)) (at most 65504),
-// q = rint(x / s) limited to +-127, with an IEEE division; s = 0 gives q = 0, and a NaN is stored as 0.
+// q8 of one group of 32 values: s = fp16(max|x| * fl32(1/127)) (at most 65504), q = x / s
+// rounded to the nearest integer, ties to even, within +-127; s = 0 gives q = 0, and a NaN
+// is stored as 0.  Divisions would take more time than the memory traffic (23.8 us instead of
+// DIVISION for 8191 tokens of 8 heads of 128), and x times fl(1/s) is enough: x has at most 11
+// bits, is at least s/2 where a tie can be, and s has 11, so x/s is a tie exactly or at least
+// 2^-12 away from one, while the product is off by 2^-15 at most.  Adding and taking away
+// 1536 = 1.5 * 2^10 rounds it to a multiple of 2^-13, which puts a tie back where it belongs;
+// adding 1.5 * 2^23 then rounds to the integer, ties to even, in the last bits.
 //
 // What bounds it: HBM for prompts (each value read once and written once), the launch for a
 // decode step's few tokens.  A thread moves 16-byte pieces of 8 values; four neighbouring
 // threads hold one q8 group and find its maximum by two shuffles, so q8 needs no second
 // pass and no shared memory.
+#include <type_traits>
+
 #include "launch.cuh"
 #include "paged.cuh"
 #include "ptx.cuh"
@@ -33,6 +41,18 @@ __device__ __forceinline__ void to_f32(const uint4 &v, float (&f)[8]) {
     const T *p = reinterpret_cast<const T *>(&v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = static_cast<float>(p[i]);
+}
+
+// A 16-bit value's bits (sign bit clear) as a number, and back (exact for values of T).
+template <typename T>
+__device__ __forceinline__ float value_of(uint32_t bits) {
+    if constexpr (std::is_same_v<T, __half>) return __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
+    else return __uint_as_float(bits << 16);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t bits_of(float x) {
+    if constexpr (std::is_same_v<T, __half>) return __half_as_ushort(__float2half_rn(x));
+    else return __float_as_uint(x) >> 16;
 }
 
 template <typename T, bool Q8>
@@ -71,23 +91,36 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
             if (write)
                 *reinterpret_cast<uint4 *>(a.rows[kv].base + a.rows[kv].at(page, off, head[u]) + piece[u] * 16) = val[u];
         } else {
+            // the group's largest |x| by its bits: they order as the values do, NaNs above infinity
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(&val[u]);
+            uint32_t most = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+            most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, 2));
+            most = max(most & 0xffffu, most >> 16);
             float f[8];
             to_f32<T>(val[u], f);
-            float top = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const __half hs = __float2half_rn(fminf(top * (1.0f / 127.0f), 65504.0f));
-            const float sc = __half2float(hs);
-            uint32_t q[2] = {0, 0};
-            if (sc > 0.f) {
+            constexpr uint32_t inf = std::is_same_v<T, __half> ? 0x7c00u : 0x7f80u;
+            if (__any_sync(0xffffffffu, most > inf)) {  // NaNs: they count as 0
+                float top = 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float r = f[i] == f[i] ? fminf(fmaxf(rintf(__fdiv_rn(f[i], sc)), -127.f), 127.f) : 0.f;
-                    q[i >> 2] |= (static_cast<uint32_t>(static_cast<int>(r)) & 0xffu) << (8 * (i & 3));
+                    f[i] = f[i] == f[i] ? f[i] : 0.f;
+                    top = fmaxf(top, fabsf(f[i]));
                 }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                most = bits_of<T>(top);
             }
+            const __half hs = __float2half_rn(fminf(value_of<T>(most) * (1.0f / 127.0f), 65504.0f));
+            const float sc = __half2float(hs), inv = sc > 0.f ? __frcp_rn(sc) : 0.f;
+            uint32_t r[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float y = fminf(fmaxf(f[i] * inv, -127.f), 127.f);
+                r[i] = __float_as_uint(((y + 1536.f) - 1536.f) + 12582912.f);
+            }
+            const uint32_t q[2] = {__byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040), 0x5410),
+                                   __byte_perm(__byte_perm(r[4], r[5], 0x0040), __byte_perm(r[6], r[7], 0x0040), 0x5410)};
             if (write) {
                 *reinterpret_cast<uint2 *>(a.rows[kv].base + a.rows[kv].at(page, off, head[u]) + piece[u] * 8) =
                     make_uint2(q[0], q[1]);

@@ -139,14 +139,18 @@ def paged_tables(lens, new_tokens, free_pages, table, *, page_size: int, slots, 
     _vector(slots, "slots", torch.int64, None, dev)
     if table.shape[0] != batch or (table.stride(1) != 1 and table.shape[1] > 1):
         raise ValueError(f"table must be [{batch}, max_pages] with contiguous rows")
-    if kv_lens is None or starts is None or used is None:  # one allocation serves them all
-        mine = torch.empty(2 * batch + 2, dtype=torch.int32, device=lens.device).split((batch, batch + 1, 1))
-        kv_lens = mine[0] if kv_lens is None else kv_lens
-        starts = mine[1] if starts is None else starts
-        used = mine[2] if used is None else used
-    _vector(kv_lens, "kv_lens", torch.int32, batch, dev)
-    _vector(starts, "starts", torch.int32, batch + 1, dev)
-    _vector(used, "used", torch.int32, 1, dev)
+    if kv_lens is None:
+        kv_lens = torch.empty(batch, dtype=torch.int32, device=lens.device)
+    else:
+        _vector(kv_lens, "kv_lens", torch.int32, batch, dev)
+    if starts is None:
+        starts = torch.empty(batch + 1, dtype=torch.int32, device=lens.device)
+    else:
+        _vector(starts, "starts", torch.int32, batch + 1, dev)
+    if used is None:
+        used = torch.empty(1, dtype=torch.int32, device=lens.device)
+    else:
+        _vector(used, "used", torch.int32, 1, dev)
     if batch == 0:
         raise SdtError(-3, "paged_tables: batch must be at least 1")
     check(_fn("paged_tables")(batch, page_size, table.shape[1], lens.data_ptr(), new_tokens.data_ptr(),
@@ -209,13 +213,16 @@ def paged_attn_m1(q, cache: PagedCache, table, lens, out=None, *, workspace, sca
     batch, q_heads, head_dim = q.shape
     if head_dim != cache.head_dim:
         raise ValueError(f"q has heads of {head_dim}, the cache of {cache.head_dim}")
-    if q.stride(2) != 1:
+    qb, qh, qd = q.stride()
+    if qd != 1:
         raise ValueError("q must be contiguous in its last dimension")
     if out is None:
         out = torch.empty_like(q) if q.is_contiguous() else torch.empty(q.shape, dtype=dtype, device=q.device)
+        ob, oh = q_heads * head_dim, head_dim
     else:
         _tensor(out, "out", dtype, 3, dev)
-        if out.shape != q.shape or out.stride(2) != 1:
+        ob, oh, od = out.stride()
+        if out.shape != q.shape or od != 1:
             raise ValueError(f"out must be {tuple(q.shape)}, contiguous in its last dimension")
     _tensor(table, "table", torch.int32, 2, dev)
     rows, wide = table.shape
@@ -228,8 +235,6 @@ def paged_attn_m1(q, cache: PagedCache, table, lens, out=None, *, workspace, sca
             raise ValueError(f"lse must be contiguous {(batch, q_heads)}")
     _vector(workspace, "workspace", torch.uint8, None, dev)
     # (a dimension of one never steps: its stride may be anything)
-    qb, qh, _ = q.stride()
-    ob, oh, _ = out.stride()
     check(_fn("paged_attn_m1")(batch, q_heads, q.data_ptr(), qb if batch > 1 else 0, qh if q_heads > 1 else 0,
                                DTYPE_CODES[dtype], cache._ref, table.data_ptr(), table.stride(0) if batch > 1 else wide,
                                wide, lens.data_ptr(), window, head_dim ** -0.5 if scale is None else scale,
