@@ -17,10 +17,13 @@ GROUP = 32  # values per fp16 scale of a q8 cache
 DTYPE_CODES = {torch.float16: 0, torch.bfloat16: 1, torch.int8: 2}
 
 
-# A decode step calls these once a layer, so a call's own time counts: the library's functions
-# are looked up once, the current stream is asked for as the raw handle, and a tensor that is
-# as it should be passes one comparison.
+# A decode step calls these once a layer, so a call's own time counts.  The library's functions
+# are looked up once, the current stream is asked for as the raw handle, and each call first
+# compares everything in one expression; only if something is not plainly as it should be, the
+# _need_* functions go through it again and raise what is wrong.
 _current_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_I32, _I64 = torch.int32, torch.int64
 _functions = {}
 
 
@@ -31,16 +34,12 @@ def _fn(name):
     return f
 
 
-def _stream(stream, device):
-    if stream is None:
-        return _current_stream(device)
+def _handle(stream):
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _tensor(t, name, dtype, ndim, device=None):
-    """A CUDA tensor on the current device (or on `device`, already known to be it)."""
-    if type(t) is torch.Tensor and t.dtype is dtype and t.dim() == ndim and t.get_device() == device:
-        return
+def _need(t, name, dtype, ndim):
+    """A CUDA tensor on the current device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
@@ -49,22 +48,43 @@ def _tensor(t, name, dtype, ndim, device=None):
         raise ValueError(f"{name} must be {ndim}-D")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if device is None:
-        if t.get_device() != torch.cuda.current_device():
-            raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
-    elif t.get_device() != device:
-        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{device}")
+    if t.get_device() != _current_device():
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{_current_device()}")
 
 
-def _vector(t, name, dtype, n, device):
-    if (type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == device and t.dim() == 1 and t.is_contiguous()
-            and (n is None or len(t) == n)):
-        return
-    _tensor(t, name, dtype, 1, device)
+def _need_vector(t, name, dtype, n=None):
+    _need(t, name, dtype, 1)
     if n is not None and t.shape[0] != n:
         raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
-    if t.stride(0) != 1 and t.shape[0] > 1:
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _need_table(table, batch):
+    _need(table, "table", _I32, 2)
+    if table.shape[0] != batch or (table.stride(1) != 1 and table.shape[1] > 1):
+        raise ValueError(f"table must be [{batch}, max_pages] with contiguous rows")
+
+
+def _need_cache(cache):
+    if not isinstance(cache, PagedCache):
+        raise TypeError("cache must be a PagedCache")
+    if cache.device_index != _current_device():
+        raise ValueError(f"the cache is on cuda:{cache.device_index}, but the current device is cuda:{_current_device()}")
+
+
+def _need_values(t, name, cache, shape):
+    """Queries, keys or values [n, heads, head_dim] of a type that goes with the cache."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in cache.value_dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, cache.value_dtypes))}, got {t.dtype}")
+    _need(t, name, t.dtype, 3)
+    for have, want in zip(t.shape, shape):
+        if want is not None and have != want:
+            raise ValueError(f"{name} must be {tuple('any' if w is None else w for w in shape)}, got {tuple(t.shape)}")
+    if t.stride(2) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
 
 
 class PagedCache:
@@ -87,7 +107,7 @@ class PagedCache:
         if q8:
             tensors += [("k_scales", k_scales, torch.float16), ("v_scales", v_scales, torch.float16)]
         for name, t, dtype in tensors:
-            _tensor(t, name, dtype, 4)
+            _need(t, name, dtype, 4)
             want = tuple(k.shape) if t.dtype is k.dtype else (*k.shape[:3], k.shape[3] // GROUP)
             if tuple(t.shape) != want:
                 raise ValueError(f"{name} must be {want}, got {tuple(t.shape)}")
@@ -96,6 +116,7 @@ class PagedCache:
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
         self.num_pages, self.page_size, self.kv_heads, self.head_dim = k.shape
         self.dtype, self.device_index = k.dtype, k.get_device()
+        self.value_dtypes = (torch.float16, torch.bfloat16) if q8 else (k.dtype,)  # of queries and new values
         d = sdt_paged_cache()
         d.num_pages, d.page_size, d.kv_heads, d.head_dim = k.shape
         d.dtype = DTYPE_CODES[k.dtype]
@@ -107,15 +128,6 @@ class PagedCache:
                     setattr(d, f"{short}_{axis}", t.stride(dim) if t.shape[dim] > 1 else 0)
         self.descriptor = d
         self._ref = ctypes.byref(d)
-
-
-def _cache(cache):
-    if not isinstance(cache, PagedCache):
-        raise TypeError("cache must be a PagedCache")
-    if cache.device_index != torch._C._cuda_getDevice():
-        raise ValueError(f"the cache is on cuda:{cache.device_index}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    return cache.device_index
 
 
 def paged_tables(lens, new_tokens, free_pages, table, *, page_size: int, slots, kv_lens=None, starts=None, used=None,
@@ -130,33 +142,43 @@ def paged_tables(lens, new_tokens, free_pages, table, *, page_size: int, slots, 
     sums of new_tokens, and int32 [1], the pages taken; where that exceeds free_pages' length,
     the entries and slots without a page are -1.
     """
-    _tensor(lens, "lens", torch.int32, 1)
-    dev, batch = lens.get_device(), lens.shape[0]
-    _vector(lens, "lens", torch.int32, batch, dev)
-    _vector(new_tokens, "new_tokens", torch.int32, batch, dev)
-    _vector(free_pages, "free_pages", torch.int32, None, dev)
-    _tensor(table, "table", torch.int32, 2, dev)
-    _vector(slots, "slots", torch.int64, None, dev)
-    if table.shape[0] != batch or (table.stride(1) != 1 and table.shape[1] > 1):
-        raise ValueError(f"table must be [{batch}, max_pages] with contiguous rows")
+    try:
+        batch, dev = len(lens), _current_device()
+        rows, wide = table.shape
+        step, along = table.stride()
+        good = (rows == batch and (along == 1 or wide <= 1)
+                and lens.dtype is _I32 and new_tokens.dtype is _I32 and free_pages.dtype is _I32
+                and table.dtype is _I32 and slots.dtype is _I64
+                and lens.get_device() == dev and new_tokens.get_device() == dev and free_pages.get_device() == dev
+                and table.get_device() == dev and slots.get_device() == dev
+                and lens.dim() == 1 and new_tokens.shape == lens.shape and free_pages.dim() == 1 and slots.dim() == 1
+                and lens.is_contiguous() and new_tokens.is_contiguous() and free_pages.is_contiguous()
+                and slots.is_contiguous())
+    except (AttributeError, TypeError, ValueError, RuntimeError):
+        good = False
+    if not good:
+        _need_vector(lens, "lens", _I32)
+        batch = len(lens)
+        _need_vector(new_tokens, "new_tokens", _I32, batch)
+        _need_vector(free_pages, "free_pages", _I32)
+        _need_table(table, batch)
+        _need_vector(slots, "slots", _I64)
     if kv_lens is None:
-        kv_lens = torch.empty(batch, dtype=torch.int32, device=lens.device)
+        kv_lens = torch.empty_like(lens)
     else:
-        _vector(kv_lens, "kv_lens", torch.int32, batch, dev)
+        _need_vector(kv_lens, "kv_lens", _I32, batch)
     if starts is None:
-        starts = torch.empty(batch + 1, dtype=torch.int32, device=lens.device)
+        starts = torch.empty(batch + 1, dtype=_I32, device=lens.device)
     else:
-        _vector(starts, "starts", torch.int32, batch + 1, dev)
+        _need_vector(starts, "starts", _I32, batch + 1)
     if used is None:
-        used = torch.empty(1, dtype=torch.int32, device=lens.device)
+        used = torch.empty(1, dtype=_I32, device=lens.device)
     else:
-        _vector(used, "used", torch.int32, 1, dev)
-    if batch == 0:
-        raise SdtError(-3, "paged_tables: batch must be at least 1")
-    check(_fn("paged_tables")(batch, page_size, table.shape[1], lens.data_ptr(), new_tokens.data_ptr(),
-                             free_pages.data_ptr(), free_pages.shape[0], table.data_ptr(),
-                             table.stride(0) if batch > 1 else table.shape[1], kv_lens.data_ptr(), starts.data_ptr(),
-                             slots.data_ptr(), slots.shape[0], used.data_ptr(), _stream(stream, dev)))
+        _need_vector(used, "used", _I32, 1)
+    check(_fn("paged_tables")(batch, page_size, wide, lens.data_ptr(), new_tokens.data_ptr(), free_pages.data_ptr(),
+                              len(free_pages), table.data_ptr(), step if batch > 1 else wide, kv_lens.data_ptr(),
+                              starts.data_ptr(), slots.data_ptr(), len(slots), used.data_ptr(),
+                              _current_stream(dev) if stream is None else _handle(stream)))
     return kv_lens, starts, slots, used
 
 
@@ -164,21 +186,26 @@ def paged_append(k, v, slots, cache: PagedCache, *, stream=None) -> PagedCache:
     """Writes k and v [tokens, kv_heads, head_dim] (float16 or bfloat16; a 16-bit cache's own
     type) into the cache at slots (int64 [tokens], page * page_size + offset; negative: left
     out), as q8 if the cache is.  k and v may be slices of wider rows."""
-    dev = _cache(cache)
-    dtype = cache.dtype if cache.dtype is not torch.int8 else k.dtype if isinstance(k, torch.Tensor) else None
-    if dtype not in (torch.float16, torch.bfloat16):
-        raise TypeError("k must be a float16 or bfloat16 tensor")
-    _tensor(k, "k", dtype, 3, dev)
-    _tensor(v, "v", dtype, 3, dev)
-    tokens = k.shape[0]
-    want = (tokens, cache.kv_heads, cache.head_dim)
-    if k.shape != want or v.shape != want:
-        raise ValueError(f"k and v must be {want}, got {tuple(k.shape)} and {tuple(v.shape)}")
-    if k.stride(2) != 1 or v.stride(2) != 1:
-        raise ValueError("k and v must be contiguous in their last dimension")
-    _vector(slots, "slots", torch.int64, tokens, dev)
-    check(_fn("paged_append")(tokens, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1),
-                             DTYPE_CODES[dtype], slots.data_ptr(), cache._ref, _stream(stream, dev)))
+    try:
+        dev, dtype, tokens = cache.device_index, k.dtype, len(k)
+        want = (tokens, cache.kv_heads, cache.head_dim)
+        kt, kh, kd = k.stride()
+        vt, vh, vd = v.stride()
+        good = (dev == _current_device() and dtype in cache.value_dtypes and v.dtype is dtype and slots.dtype is _I64
+                and k.get_device() == dev and v.get_device() == dev and slots.get_device() == dev
+                and k.shape == want and v.shape == want and slots.shape == want[:1] and kd == 1 and vd == 1
+                and slots.is_contiguous())
+    except (AttributeError, TypeError, ValueError, RuntimeError):
+        good = False
+    if not good:
+        _need_cache(cache)
+        _need_values(k, "k", cache, (None, cache.kv_heads, cache.head_dim))
+        _need_values(v, "v", cache, k.shape)
+        if v.dtype is not k.dtype:
+            raise TypeError("k and v must have one type")
+        _need_vector(slots, "slots", _I64, len(k))
+    check(_fn("paged_append")(tokens, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, DTYPE_CODES[dtype], slots.data_ptr(),
+                              cache._ref, _current_stream(dev) if stream is None else _handle(stream)))
     return cache
 
 
@@ -190,7 +217,7 @@ def paged_attn_workspace(q_heads: int, kv_heads: int, head_dim: int, device=None
     ws = torch.empty(nbytes + 256, dtype=torch.uint8, device=device or "cuda")
     off = (-ws.data_ptr()) % 256
     ws = ws[off:off + nbytes]
-    check(lib().sdt_splitk_workspace_init(ws.data_ptr(), nbytes, _stream(None, ws.get_device())))
+    check(lib().sdt_splitk_workspace_init(ws.data_ptr(), nbytes, _current_stream(ws.get_device())))
     return ws
 
 
@@ -205,40 +232,43 @@ def paged_attn_m1(q, cache: PagedCache, table, lens, out=None, *, workspace, sca
     zeros.  scale: None is 1 / sqrt(head_dim).  lse: float32 [batch, q_heads], if given
     receives log(sum(exp(scores))).  workspace: paged_attn_workspace().
     """
-    dev = _cache(cache)
-    dtype = cache.dtype if cache.dtype is not torch.int8 else q.dtype if isinstance(q, torch.Tensor) else None
-    if dtype not in (torch.float16, torch.bfloat16):
-        raise TypeError("q must be a float16 or bfloat16 tensor")
-    _tensor(q, "q", dtype, 3, dev)
-    batch, q_heads, head_dim = q.shape
-    if head_dim != cache.head_dim:
-        raise ValueError(f"q has heads of {head_dim}, the cache of {cache.head_dim}")
-    qb, qh, qd = q.stride()
-    if qd != 1:
-        raise ValueError("q must be contiguous in its last dimension")
+    try:
+        dev, dtype = cache.device_index, q.dtype
+        batch, q_heads, head_dim = q.shape
+        rows, wide = table.shape
+        qb, qh, qd = q.stride()
+        step, along = table.stride()
+        good = (dev == _current_device() and dtype in cache.value_dtypes and head_dim == cache.head_dim and qd == 1
+                and rows == batch and (along == 1 or wide <= 1)
+                and table.dtype is _I32 and lens.dtype is _I32 and workspace.dtype is torch.uint8
+                and q.get_device() == dev and table.get_device() == dev and lens.get_device() == dev
+                and workspace.get_device() == dev and lens.dim() == 1 and len(lens) == batch and workspace.dim() == 1
+                and lens.is_contiguous() and workspace.is_contiguous())
+    except (AttributeError, TypeError, ValueError, RuntimeError):
+        good = False
+    if not good:
+        _need_cache(cache)
+        _need_values(q, "q", cache, (None, None, cache.head_dim))
+        _need_table(table, len(q))
+        _need_vector(lens, "lens", _I32, len(q))
+        _need_vector(workspace, "workspace", torch.uint8)
     if out is None:
         out = torch.empty_like(q) if q.is_contiguous() else torch.empty(q.shape, dtype=dtype, device=q.device)
         ob, oh = q_heads * head_dim, head_dim
     else:
-        _tensor(out, "out", dtype, 3, dev)
+        _need(out, "out", dtype, 3)
         ob, oh, od = out.stride()
         if out.shape != q.shape or od != 1:
             raise ValueError(f"out must be {tuple(q.shape)}, contiguous in its last dimension")
-    _tensor(table, "table", torch.int32, 2, dev)
-    rows, wide = table.shape
-    if rows != batch or (wide > 1 and table.stride(1) != 1):
-        raise ValueError(f"table must be [{batch}, max_pages] with contiguous rows")
-    _vector(lens, "lens", torch.int32, batch, dev)
     if lse is not None:
-        _tensor(lse, "lse", torch.float32, 2, dev)
+        _need(lse, "lse", torch.float32, 2)
         if lse.shape != (batch, q_heads) or not lse.is_contiguous():
             raise ValueError(f"lse must be contiguous {(batch, q_heads)}")
-    _vector(workspace, "workspace", torch.uint8, None, dev)
     # (a dimension of one never steps: its stride may be anything)
     check(_fn("paged_attn_m1")(batch, q_heads, q.data_ptr(), qb if batch > 1 else 0, qh if q_heads > 1 else 0,
-                               DTYPE_CODES[dtype], cache._ref, table.data_ptr(), table.stride(0) if batch > 1 else wide,
-                               wide, lens.data_ptr(), window, head_dim ** -0.5 if scale is None else scale,
-                               out.data_ptr(), ob if batch > 1 else 0, oh if q_heads > 1 else 0,
+                               DTYPE_CODES[dtype], cache._ref, table.data_ptr(), step if batch > 1 else wide, wide,
+                               lens.data_ptr(), window, head_dim ** -0.5 if scale is None else scale, out.data_ptr(),
+                               ob if batch > 1 else 0, oh if q_heads > 1 else 0,
                                None if lse is None else lse.data_ptr(), workspace.data_ptr(), len(workspace),
-                               _stream(stream, dev)))
+                               _current_stream(dev) if stream is None else _handle(stream)))
     return out
