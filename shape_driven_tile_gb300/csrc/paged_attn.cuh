@@ -187,12 +187,13 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
     return v;
 }
 
-// Position of 16-byte piece c of row r in a q8 tile: pairs of pieces (32 values, one group)
-// move together, so that both access patterns below spread over the banks: 8-byte reads of
-// rows r .. r+3 and 4-byte reads of rows r, r+2, r+4, r+6.
-template <int DP>
-__device__ __forceinline__ uint32_t q8_piece(uint32_t r, uint32_t c) {
-    return DP >= 128 ? c ^ (((r & 3) ^ ((r >> 2) & 1)) << 1) : c ^ (((r >> 1) & 1) << 1);
+// 16-byte piece c of row r of a tile lies at piece c ^ swizzle(r) of its row, which spreads the
+// reads over the banks: 8 rows at one piece (16 bits); in q8, whose pieces move in pairs (32
+// values, one group), 8-byte reads of rows r .. r + 3 and 4-byte reads of rows r, r + 2, r + 4,
+// r + 6.  swizzle(a + b) = swizzle(a) ^ swizzle(b) where a and b share no bit.
+template <int DP, bool Q8>
+__host__ __device__ constexpr uint32_t swizzle(uint32_t r) {
+    return !Q8 ? r & 7 : DP >= 128 ? ((r & 3) ^ ((r >> 2) & 1)) << 1 : ((r >> 1) & 1) << 1;
 }
 
 // Where in the work a reader stands: the unit that begins with key `key` of the keys [lo, len) of
@@ -373,9 +374,10 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
             pg_ok = false;
         }
         constexpr int CPR = ROWB / 16, RPI = 32 / CPR;  // pieces per row, rows per instruction
-        const uint32_t kdst = smem0 + stage * C::STAGE + warp * RW * ROWB, vdst = kdst + TK * ROWB;
         const int cc = lane % CPR, rr = lane / CPR;
-        auto place = [&](int r) { return r * ROWB + (Q8 ? q8_piece<DP>(r, cc) : static_cast<uint32_t>(cc ^ (r & 7))) * 16u; };
+        const uint32_t dst = smem0 + stage * C::STAGE + (warp * RW + rr) * ROWB + ((cc ^ swizzle<DP, Q8>(rr)) << 4);
+        // (r, a multiple of RPI known at compile time, shares no bit with rr; rows start at multiples of ROWB)
+        auto place = [&](int r) { return (dst ^ (swizzle<DP, Q8>(r) << 4)) + r * ROWB; };
         if (p.whole_pages) {
             // 16 rows at a time lie in one page, token after token: one address and steps from it.  (A row
             // past the range has zeros copied, but its address is still one of the page, or of page 0.)
@@ -389,10 +391,10 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
                 const int k_step = static_cast<int>(p.k.token), v_step = static_cast<int>(p.v.token);
 #pragma unroll
                 for (int it = 0; it < 16 / RPI; ++it) {
-                    const uint32_t pos = place(r0 + it * RPI + rr);
+                    const uint32_t to = place(r0 + it * RPI);
                     const int n = it * RPI < have ? 16 : 0;
-                    cp_async16(kdst + pos, ka + static_cast<int64_t>(k_step) * (it * RPI), n);
-                    cp_async16(vdst + pos, va + static_cast<int64_t>(v_step) * (it * RPI), n);
+                    cp_async16(to, ka + static_cast<int64_t>(k_step) * (it * RPI), n);
+                    cp_async16(to + TK * ROWB, va + static_cast<int64_t>(v_step) * (it * RPI), n);
                 }
             }
         } else {
@@ -402,10 +404,10 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
             for (int it = 0; it < RW / RPI; ++it) {
                 const int r = it * RPI + rr;
                 const int64_t ka = __shfl_sync(0xffffffffu, ko, r), va = __shfl_sync(0xffffffffu, vo, r);
-                const uint32_t pos = place(r);
+                const uint32_t to = place(it * RPI);
                 const int n = ka >= 0 && cc < pieces ? 16 : 0;
-                cp_async16(kdst + pos, n ? p.k.base + ka + cc * 16 : p.k.base, n);
-                cp_async16(vdst + pos, n ? p.v.base + va + cc * 16 : p.v.base, n);
+                cp_async16(to, n ? p.k.base + ka + cc * 16 : p.k.base, n);
+                cp_async16(to + TK * ROWB, n ? p.v.base + va + cc * 16 : p.v.base, n);
             }
         }
         if constexpr (Q8) {
@@ -703,7 +705,7 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
                     }
             } else {
                 const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-                const uint32_t row = kt + (k0 + g) * ROWB + q8_piece<DP>(g, c >> 1) * 16 + (c & 1) * 8;
+                const uint32_t row = kt + (k0 + g) * ROWB + ((c >> 1) ^ swizzle<DP, true>(g)) * 16 + (c & 1) * 8;
                 const uint32_t row_sc = kst + (k0 + g) * C::SCB;
 #pragma unroll
                 for (int i = 0; i < KT; ++i) {
@@ -829,8 +831,8 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
                 }
             } else {
                 // this thread's keys in the values: 2c, 2c + 1 and 8 further on
-                const uint32_t v_row[2] = {vt + (k0 + 2 * c) * ROWB + q8_piece<DP>(2 * c, g >> 2) * 16 + (g & 3) * 4,
-                                           vt + (k0 + 2 * c + 1) * ROWB + q8_piece<DP>(2 * c + 1, g >> 2) * 16 + (g & 3) * 4};
+                const uint32_t v_row[2] = {vt + (k0 + 2 * c) * ROWB + ((g >> 2) ^ swizzle<DP, true>(2 * c)) * 16 + (g & 3) * 4,
+                                           vt + (k0 + 2 * c + 1) * ROWB + ((g >> 2) ^ swizzle<DP, true>(2 * c + 1)) * 16 + (g & 3) * 4};
                 // the exponents of this block's value scales: o is kept so that weight times scale fits fp16
                 uint32_t xs[KT][2][DP / 64], top = 0;
 #pragma unroll
