@@ -463,7 +463,7 @@ int sdt_tune_table_lookup(int64_t M, int64_t N, int64_t K);
  * elements with one fp16 scale per 32 (element e of a head is q[e] * scale[e / 32], as in
  * gemv_m1_q8); head_dim a multiple of 64 up to 256; the scales have strides of their own,
  * head_dim / 32 contiguous, base and strides multiples of 4 bytes (8 with head_dim 128).
- * num_pages * page_size < 2^31; element offsets may exceed 32 bits.
+ * num_pages * page_size < 2^31; strides up to 16 GiB, offsets of any size.
  */
 #define SDT_DTYPE_Q8 2
 typedef struct sdt_paged_cache {

@@ -34,23 +34,27 @@ struct FastDiv {
     }
 };
 
-// One tensor of the cache ([page][token][head][d], any order in memory with d contiguous):
-// base and strides in bytes.
+// One tensor of the cache ([page][token][head][d], any order in memory with d contiguous).
+// Strides are held in units of UNIT bytes as 32 bits, so that an address is three wide
+// multiply-adds and a shifted add; offsets are 64 bits.
+template <int UNIT>
 struct PagedRows {
     char *base;
-    int64_t page, token, head;
-    __device__ __forceinline__ int64_t at(int64_t p, int64_t t, int64_t h) const {
-        return p * page + t * token + h * head;
+    uint32_t page, token, head;
+    __device__ __forceinline__ char *at(uint32_t p, uint32_t t, uint32_t h) const {
+        return base + (static_cast<uint64_t>(p) * page + static_cast<uint64_t>(t) * token + static_cast<uint64_t>(h) * head) * UNIT;
     }
 };
+using KvRows = PagedRows<16>;    // keys and values
+using ScaleRows = PagedRows<4>;  // q8 scales
 
 __device__ __forceinline__ void paged_status(int *status, int code) { atomicCAS(status, 0, code); }
 
 // Checks a cache descriptor; SDT_OK or a negative status with the last error set.
 int check_cache(const sdt_paged_cache *c);
-// The cache's tensors in bytes (after check_cache).
-PagedRows rows_k(const sdt_paged_cache &c), rows_v(const sdt_paged_cache &c);
-PagedRows rows_ks(const sdt_paged_cache &c), rows_vs(const sdt_paged_cache &c);
+// The cache's tensors (after check_cache).
+KvRows rows_k(const sdt_paged_cache &c), rows_v(const sdt_paged_cache &c);
+ScaleRows rows_ks(const sdt_paged_cache &c), rows_vs(const sdt_paged_cache &c);
 
 inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 

@@ -28,7 +28,8 @@ constexpr int kAppendUnroll = 4;  // 16-byte loads in flight per thread
 struct AppendArgs {
     const char *x[2];          // keys, values
     int64_t x_token[2], x_head[2];  // bytes
-    PagedRows rows[2], scales[2];
+    KvRows rows[2];
+    ScaleRows scales[2];
     const int64_t *slots;
     int64_t num_slots_cache;   // pages * page size
     int tokens;
@@ -89,7 +90,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
         const uint32_t page = a.page.div(s), off = s - page * a.page.d;
         if constexpr (!Q8) {
             if (write)
-                *reinterpret_cast<uint4 *>(a.rows[kv].base + a.rows[kv].at(page, off, head[u]) + piece[u] * 16) = val[u];
+                *reinterpret_cast<uint4 *>(a.rows[kv].at(page, off, head[u]) + piece[u] * 16) = val[u];
         } else {
             // the group's largest |x| by its bits: they order as the values do, NaNs above infinity
             const uint32_t *w = reinterpret_cast<const uint32_t *>(&val[u]);
@@ -122,10 +123,10 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
             const uint32_t q[2] = {__byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040), 0x5410),
                                    __byte_perm(__byte_perm(r[4], r[5], 0x0040), __byte_perm(r[6], r[7], 0x0040), 0x5410)};
             if (write) {
-                *reinterpret_cast<uint2 *>(a.rows[kv].base + a.rows[kv].at(page, off, head[u]) + piece[u] * 8) =
+                *reinterpret_cast<uint2 *>(a.rows[kv].at(page, off, head[u]) + piece[u] * 8) =
                     make_uint2(q[0], q[1]);
                 if ((piece[u] & 3) == 0)
-                    *reinterpret_cast<__half *>(a.scales[kv].base + a.scales[kv].at(page, off, head[u]) + (piece[u] >> 2) * 2) = hs;
+                    *reinterpret_cast<__half *>(a.scales[kv].at(page, off, head[u]) + (piece[u] >> 2) * 2) = hs;
             }
         }
     }
@@ -136,9 +137,10 @@ static bool stride_ok(int64_t s, int64_t mult) { return s >= 0 && s % mult == 0;
 static int check_rows(const char *what, const void *p, int64_t sp, int64_t st, int64_t sh, int64_t bytes_el, int64_t align) {
     if (!p) return fail(SDT_ERR_NULL, "paged cache: %s is NULL", what);
     if (!aligned(p, align)) return fail(SDT_ERR_ALIGN, "paged cache: %s must be %lld-byte aligned", what, (long long)align);
-    const int64_t mult = align / bytes_el;
-    if (!stride_ok(sp, mult) || !stride_ok(st, mult) || !stride_ok(sh, mult))
-        return fail(SDT_ERR_ARG, "paged cache: strides of %s must be non-negative multiples of %lld elements", what, (long long)mult);
+    const int64_t mult = align / bytes_el, most = int64_t(UINT32_MAX) * 4 / bytes_el;  // strides fit 32 bits in units of 4 bytes
+    for (int64_t s : {sp, st, sh})
+        if (!stride_ok(s, mult) || s > most)
+            return fail(SDT_ERR_ARG, "paged cache: strides of %s must be multiples of %lld elements, 0 to 16 GiB", what, (long long)mult);
     return SDT_OK;
 }
 
@@ -162,13 +164,16 @@ int check_cache(const sdt_paged_cache *c) {
     return rc;
 }
 
-static PagedRows rows_of(void *p, int64_t sp, int64_t st, int64_t sh, int el) {
-    return {static_cast<char *>(p), sp * el, st * el, sh * el};
+template <int UNIT>
+static PagedRows<UNIT> rows_of(void *p, int64_t sp, int64_t st, int64_t sh, int el) {
+    auto u = [&](int64_t s) { return static_cast<uint32_t>(s * el / UNIT); };
+    return {static_cast<char *>(p), u(sp), u(st), u(sh)};
 }
-PagedRows rows_k(const sdt_paged_cache &c) { return rows_of(c.k, c.k_page, c.k_token, c.k_head, c.dtype == SDT_DTYPE_Q8 ? 1 : 2); }
-PagedRows rows_v(const sdt_paged_cache &c) { return rows_of(c.v, c.v_page, c.v_token, c.v_head, c.dtype == SDT_DTYPE_Q8 ? 1 : 2); }
-PagedRows rows_ks(const sdt_paged_cache &c) { return rows_of(c.k_scales, c.ks_page, c.ks_token, c.ks_head, 2); }
-PagedRows rows_vs(const sdt_paged_cache &c) { return rows_of(c.v_scales, c.vs_page, c.vs_token, c.vs_head, 2); }
+static int width(const sdt_paged_cache &c) { return c.dtype == SDT_DTYPE_Q8 ? 1 : 2; }
+KvRows rows_k(const sdt_paged_cache &c) { return rows_of<16>(c.k, c.k_page, c.k_token, c.k_head, width(c)); }
+KvRows rows_v(const sdt_paged_cache &c) { return rows_of<16>(c.v, c.v_page, c.v_token, c.v_head, width(c)); }
+ScaleRows rows_ks(const sdt_paged_cache &c) { return rows_of<4>(c.k_scales, c.ks_page, c.ks_token, c.ks_head, 2); }
+ScaleRows rows_vs(const sdt_paged_cache &c) { return rows_of<4>(c.v_scales, c.vs_page, c.vs_token, c.vs_head, 2); }
 
 }  // namespace sdt
 

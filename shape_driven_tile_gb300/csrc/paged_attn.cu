@@ -87,7 +87,7 @@ int paged_attn_m1(int64_t batch, int64_t q_heads, const void *q, int64_t q_batch
     a.max_pages = static_cast<int>(max_pages);
     a.num_pages = static_cast<int>(cache->num_pages);
     a.window = window < INT32_MAX ? static_cast<int>(window) : 0;  // longer than any row: no window
-    a.whole_pages = cache->page_size % 16 == 0 && a.window == 0 && a.k.token < (1 << 26) && a.v.token < (1 << 26);
+    a.whole_pages = cache->page_size % 16 == 0 && a.window == 0 && a.k.token < (1 << 22) && a.v.token < (1 << 22);
     a.page = FastDiv::of(static_cast<uint32_t>(cache->page_size));
     a.scale_log2 = scale * 1.4426950408889634f;
     a.counters = static_cast<unsigned *>(workspace);

@@ -53,7 +53,8 @@ struct PagedAttnArgs {
     char *out;
     float *lse;                // [batch][q_heads], or null
     int64_t q_batch, q_head, o_batch, o_head;
-    PagedRows k, v, ks, vs;
+    KvRows k, v;
+    ScaleRows ks, vs;
     const int *table;
     int64_t table_stride;
     const int *lens;
@@ -342,6 +343,7 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
     };
     AttnWalk pw;  // the loads' place
     pw.b = sh_b;
+    const int *pw_pages = p.table + pw.b * p.table_stride;  // its request's pages
     range_of(pw.b, pw.lo, pw.len);
     {
         const int n = units_in(pw.lo, pw.len) + C::COST, item = static_cast<int>(div_small(sh_rest, n));
@@ -357,13 +359,18 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
     // ---- loads: lane r < RW describes row warp * RW + r of the unit ----
     int pg_id = -1, pg_off = 0;
     bool pg_ok = false;
+    auto load_next = [&] {  // the loads' place moves on
+        const int b = pw.b;
+        advance(pw);
+        if (pw.b != b) pw_pages += p.table_stride;
+    };
     auto look_up = [&] {
         const int key = pw.key + warp * RW + lane;
         pg_ok = lane < RW && key < pw.len;
         if (pg_ok) {
             const int pi = static_cast<int>(p.page.div(key));
             pg_off = key - pi * static_cast<int>(p.page.d);
-            pg_id = __ldg(p.table + pw.b * p.table_stride + pi);
+            pg_id = __ldg(pw_pages + pi);
         }
     };
     const int pieces = p.head_dim * (Q8 ? 1 : 2) / 16;  // 16-byte pieces of a row that exist
@@ -386,9 +393,9 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
                 const int id = __shfl_sync(0xffffffffu, pg_ok ? pg_id : -1, r0), off = __shfl_sync(0xffffffffu, pg_off, r0);
                 const int have = id >= 0 && cc < pieces ? pw.len - (pw.key + warp * RW + r0) - rr : 0;
                 const int col = cc < pieces ? cc * 16 : 0;
-                const char *ka = p.k.base + (p.k.at(max(id, 0), id >= 0 ? off + rr : rr, pw.h) + col);
-                const char *va = p.v.base + (p.v.at(max(id, 0), id >= 0 ? off + rr : rr, pw.h) + col);
-                const int k_step = static_cast<int>(p.k.token), v_step = static_cast<int>(p.v.token);
+                const char *ka = p.k.at(max(id, 0), id >= 0 ? off + rr : rr, pw.h) + col;
+                const char *va = p.v.at(max(id, 0), id >= 0 ? off + rr : rr, pw.h) + col;
+                const int k_step = static_cast<int>(p.k.token) * 16, v_step = static_cast<int>(p.v.token) * 16;
 #pragma unroll
                 for (int it = 0; it < 16 / RPI; ++it) {
                     const uint32_t to = place(r0 + it * RPI);
@@ -398,8 +405,8 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
                 }
             }
         } else {
-            const int64_t ko = pg_ok ? p.k.at(pg_id, pg_off, pw.h) : -1;
-            const int64_t vo = pg_ok ? p.v.at(pg_id, pg_off, pw.h) : -1;
+            const int64_t ko = pg_ok ? p.k.at(pg_id, pg_off, pw.h) - p.k.base : -1;
+            const int64_t vo = pg_ok ? p.v.at(pg_id, pg_off, pw.h) - p.v.base : -1;
 #pragma unroll
             for (int it = 0; it < RW / RPI; ++it) {
                 const int r = it * RPI + rr;
@@ -413,8 +420,8 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
         if constexpr (Q8) {
             if (lane < RW) {
                 const uint32_t sdst = smem0 + stage * C::STAGE + 2 * TK * ROWB + (warp * RW + lane) * C::SCB;
-                const char *ks = pg_ok ? p.ks.base + p.ks.at(pg_id, pg_off, pw.h) : p.ks.base;
-                const char *vs = pg_ok ? p.vs.base + p.vs.at(pg_id, pg_off, pw.h) : p.vs.base;
+                const char *ks = pg_ok ? p.ks.at(pg_id, pg_off, pw.h) : p.ks.base;
+                const char *vs = pg_ok ? p.vs.at(pg_id, pg_off, pw.h) : p.vs.base;
                 if constexpr (DP == 128) {  // four scales, aligned to their size
                     cp_async8(sdst, ks, pg_ok ? 8 : 0);
                     cp_async8(sdst + TK * C::SCB, vs, pg_ok ? 8 : 0);
@@ -513,7 +520,7 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
     for (int s = 0; s < S - 1; ++s) {
         if (pw.at < places) {
             issue(s);
-            advance(pw);
+            load_next();
             if (pw.at < places) look_up();
         }
         cp_async_commit();
@@ -666,7 +673,7 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
             const int st = stage == 0 ? S - 1 : stage - 1;  // consumed in the previous round
             if (pw.at < places) {
                 issue(st);
-                advance(pw);
+                load_next();
                 if (pw.at < places) look_up();
             }
             cp_async_commit();
