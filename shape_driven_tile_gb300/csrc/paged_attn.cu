@@ -20,7 +20,7 @@ size_t sdt_paged_attn_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t
     if (current_device(&dev)) return 0;
     size_t most = 0;  // of the variants that the sizes may take with any batch
     for (int64_t items : {int64_t(1), INT64_MAX}) {
-        const PagedAttnVariant v = paged_attn_variant(q_heads / kv_heads, items, dev.sm_count);
+        const PagedAttnVariant v = paged_attn_variant(q_heads / kv_heads, items, head_dim, false, dev.sm_count);
         const size_t slot = static_cast<size_t>(8 * v.nh * v.wh) * (paged_attn_width(head_dim) + 2) * sizeof(float);
         most = std::max(most, 2 * static_cast<size_t>(dev.sm_count) * paged_attn_ctas(v.nw) * slot);  // two pieces a CTA
     }
@@ -61,7 +61,7 @@ int paged_attn_m1(int64_t batch, int64_t q_heads, const void *q, int64_t q_batch
     if (rc) return rc;
 
     const int64_t cap = max_pages * cache->page_size;
-    PagedAttnLaunch l{paged_attn_variant(q_heads / kvh, batch * kvh, dev.sm_count), q8, dev.device, dev.sm_count,
+    PagedAttnLaunch l{paged_attn_variant(q_heads / kvh, batch * kvh, cache->head_dim, q8, dev.sm_count), q8, dev.device, dev.sm_count,
                       window > 0 && window < cap ? window : cap, reinterpret_cast<cudaStream_t>(stream)};
     PagedAttnArgs a{};
     a.q = static_cast<const char *>(q);

@@ -86,13 +86,14 @@ struct AttnCfg {
     static constexpr int ROWS = HEADS * WH;               // query heads of a CTA
     static constexpr int SLOT = ROWS * (DP + 2);          // floats of a partial
     static constexpr int QROW = DP * 2;                   // bytes of a query row in shared memory
-    // Three stages where two CTAs (or more of one warp) still share an SM, else two; wide heads
-    // have the SM to themselves.  q8 is bound by its arithmetic first: two stages and three CTAs.
+    // The warps of an SM hide each other's latency, so stages beyond two are worth less than another CTA
+    // where one fits: one-warp CTAs and q8 take two.  Four warps of 16-bit heads of 128 have three
+    // stages, two CTAs an SM; wider heads have the SM to themselves.
     static constexpr bool fits(int s, int bytes) { return s * (STAGE + ROWS * QROW) + 2048 <= bytes; }
     // An item costs about this many units besides its own (queries, join of the warps, output).  Four
     // warps have larger units and few items: counting it would only leave CTAs without a unit.
     static constexpr int COST = NW == 1 ? 1 : 0;
-    static constexpr int S = Q8 && DP <= 128 ? 2 : fits(3, 113 * 1024) || (!fits(2, 113 * 1024) && fits(3, 227 * 1024)) ? 3 : 2;
+    static constexpr int S = NW == 1 || DP == 64 || (Q8 && DP == 128) ? 2 : fits(3, 113 * 1024) || (!fits(2, 113 * 1024) && fits(3, 227 * 1024)) ? 3 : 2;
     static constexpr int smem(int q_rows) { return S * (STAGE + q_rows * QROW); }
     static_assert(fits(S, 227 * 1024), "shared memory of an SM");
     static_assert(STAGE >= NW * HEADS * DP * 4, "the stage must hold every warp's o");

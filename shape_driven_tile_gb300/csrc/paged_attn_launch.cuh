@@ -46,8 +46,10 @@ static cudaError_t launch_of(const PagedAttnArgs &a, const PagedAttnLaunch &l) {
     const PagedAttnVariant v = l.variant;
     if (v.wh == 4) return launch_variant<T, DP, 2, 4, 4, Q8>(a, l);
     if (v.wh == 2) return launch_variant<T, DP, 2, 2, 4, Q8>(a, l);
-    if (v.nh == 2) return v.nw == 1 ? launch_variant<T, DP, 2, 1, 1, Q8>(a, l) : launch_variant<T, DP, 2, 1, 4, Q8>(a, l);
-    return v.nw == 1 ? launch_variant<T, DP, 1, 1, 1, Q8>(a, l) : launch_variant<T, DP, 1, 1, 4, Q8>(a, l);
+    if (v.nh == 2) return launch_variant<T, DP, 2, 1, 4, Q8>(a, l);
+    if constexpr (!(Q8 && DP == 128))
+        if (v.nw == 1) return launch_variant<T, DP, 1, 1, 1, Q8>(a, l);
+    return launch_variant<T, DP, 1, 1, 4, Q8>(a, l);
 }
 
 template <typename T, int DP>
