@@ -479,6 +479,7 @@ typedef struct sdt_paged_cache {
 
 /*
  * paged_tables -- block tables and slot maps of a step, from the requests' lengths.
+ * (The calls with many arguments take them in a struct, which they read before they return.)
  * Request b of `batch` (1 .. 16384) holds lens[b] tokens and adds new_tokens[b] (0 or
  * more).  Its row table + b * table_stride holds its ceil(lens[b] / page_size) pages; the
  * call appends the pages that the new tokens need, taken in request order from the front
@@ -492,10 +493,13 @@ typedef struct sdt_paged_cache {
  * Negative lengths count as 0, lengths past max_pages * page_size as that; the sum of
  * new_tokens must be below 2^31.
  */
-int paged_tables(int64_t batch, int64_t page_size, int64_t max_pages, const int32_t *lens,
-                 const int32_t *new_tokens, const int32_t *free_pages, int64_t num_free, int32_t *table,
-                 int64_t table_stride, int32_t *kv_lens, int32_t *starts, int64_t *slots, int64_t num_slots,
-                 int32_t *used, sdt_stream_t stream);
+typedef struct sdt_paged_step {
+    const int32_t *lens, *new_tokens, *free_pages;
+    int32_t *table, *kv_lens, *starts, *used;
+    int64_t *slots;
+    int64_t batch, page_size, max_pages, table_stride, num_free, num_slots;
+} sdt_paged_step;
+int paged_tables(const sdt_paged_step *step, sdt_stream_t stream);
 
 /*
  * paged_append -- the keys and values of `tokens` tokens into the cache at their slots
@@ -530,10 +534,20 @@ int paged_append(int64_t tokens, const void *k, int64_t k_token, int64_t k_head,
  * shared with those), then the pieces of requests that are split over CTAs.  Calls that
  * share a workspace must not overlap on the GPU.
  */
-int paged_attn_m1(int64_t batch, int64_t q_heads, const void *q, int64_t q_batch, int64_t q_head, int dtype,
-                  const sdt_paged_cache *cache, const int32_t *table, int64_t table_stride, int64_t max_pages,
-                  const int32_t *lens, int64_t window, float scale, void *out, int64_t out_batch, int64_t out_head,
-                  float *lse, void *workspace, size_t workspace_bytes, sdt_stream_t stream);
+typedef struct sdt_paged_attn {
+    const void *q;
+    void *out;
+    float *lse;                /* NULL: not wanted */
+    const int32_t *table, *lens;
+    const sdt_paged_cache *cache;
+    void *workspace;
+    int64_t batch, q_heads;
+    int64_t q_batch, q_head, out_batch, out_head; /* strides in elements */
+    int64_t table_stride, max_pages, window, workspace_bytes;
+    float scale;
+    int dtype;
+} sdt_paged_attn;
+int paged_attn_m1(const sdt_paged_attn *call, sdt_stream_t stream);
 /* Workspace bytes of paged_attn_m1 on the current device, for any batch and lengths (0 on error). */
 size_t sdt_paged_attn_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t head_dim);
 

@@ -9,6 +9,18 @@ using namespace sdt;
 static constexpr size_t kCounterBytes = size_t(1) << 20;  // the counter region of the split-K workspaces
 static constexpr int64_t kMaxTokens = INT32_MAX - 1024;   // a row's tokens; key indices run past them by a unit at most
 
+// Workspace bytes of any call with `group` query heads per key head: of the variants that it may
+// take, whatever the batch.
+static size_t workspace_for(int64_t group, int64_t head_dim, int sm_count) {
+    size_t most = 0;
+    for (int64_t items : {int64_t(1), INT64_MAX}) {
+        const PagedAttnVariant v = paged_attn_variant(group, items, head_dim, false, sm_count);
+        const size_t slot = static_cast<size_t>(8 * v.nh * v.wh) * (paged_attn_width(head_dim) + 2) * sizeof(float);
+        most = std::max(most, 2 * static_cast<size_t>(sm_count) * paged_attn_ctas(v.nw) * slot);  // two pieces a CTA
+    }
+    return kCounterBytes + most;
+}
+
 extern "C" {
 
 size_t sdt_paged_attn_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
@@ -17,21 +29,14 @@ size_t sdt_paged_attn_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t
         fail(SDT_ERR_SHAPE, "sdt_paged_attn_workspace_bytes: bad sizes");
         return 0;
     }
-    if (current_device(&dev)) return 0;
-    size_t most = 0;  // of the variants that the sizes may take with any batch
-    for (int64_t items : {int64_t(1), INT64_MAX}) {
-        const PagedAttnVariant v = paged_attn_variant(q_heads / kv_heads, items, head_dim, false, dev.sm_count);
-        const size_t slot = static_cast<size_t>(8 * v.nh * v.wh) * (paged_attn_width(head_dim) + 2) * sizeof(float);
-        most = std::max(most, 2 * static_cast<size_t>(dev.sm_count) * paged_attn_ctas(v.nw) * slot);  // two pieces a CTA
-    }
-    return kCounterBytes + most;
+    return current_device(&dev) ? 0 : workspace_for(q_heads / kv_heads, head_dim, dev.sm_count);
 }
 
-int paged_attn_m1(int64_t batch, int64_t q_heads, const void *q, int64_t q_batch, int64_t q_head, int dtype,
-                  const sdt_paged_cache *cache, const int32_t *table, int64_t table_stride, int64_t max_pages,
-                  const int32_t *lens, int64_t window, float scale, void *out, int64_t out_batch, int64_t out_head,
-                  float *lse, void *workspace, size_t workspace_bytes, sdt_stream_t stream) {
+int paged_attn_m1(const sdt_paged_attn *call, sdt_stream_t stream) {
     clear_error();
+    if (!call) return fail(SDT_ERR_NULL, "paged_attn_m1: NULL arguments");
+    const auto &[q, out, lse, table, lens, cache, workspace, batch, q_heads, q_batch, q_head, out_batch, out_head, table_stride,
+                 max_pages, window, workspace_bytes, scale, dtype] = *call;
     int rc = check_cache(cache);
     if (rc) return rc;
     if (dtype != SDT_DTYPE_F16 && dtype != SDT_DTYPE_BF16) return fail(SDT_ERR_ARG, "paged_attn_m1: dtype must be fp16 or bf16 (got %d)", dtype);
@@ -54,8 +59,9 @@ int paged_attn_m1(int64_t batch, int64_t q_heads, const void *q, int64_t q_batch
     DeviceInfo dev;
     rc = current_device(&dev);
     if (rc) return rc;
-    const size_t need = sdt_paged_attn_workspace_bytes(q_heads, kvh, cache->head_dim);
-    if (workspace_bytes < need) return fail(SDT_ERR_ARG, "paged_attn_m1: workspace of %zu bytes, %zu needed", workspace_bytes, need);
+    const size_t need = workspace_for(q_heads / kvh, cache->head_dim, dev.sm_count);
+    if (workspace_bytes < 0 || static_cast<size_t>(workspace_bytes) < need)
+        return fail(SDT_ERR_ARG, "paged_attn_m1: workspace of %lld bytes, %zu needed", (long long)workspace_bytes, need);
     int *status = nullptr;
     rc = status_word(&status);
     if (rc) return rc;

@@ -231,7 +231,8 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
     using C = AttnCfg<DP, NH, WH, NW, Q8>;
     constexpr int TK = C::TK, KS = C::KS, RW = C::RW, ROWB = C::ROWB, S = C::S, NTH = C::THREADS;
     constexpr int MT = DP / 16;       // 16-wide row tiles of o
-    constexpr int SUB = KS < 32 ? KS : 32;  // keys between two looks at the running maximum
+    // keys between two looks at the running maximum: 32, but 16 where the registers would not do
+    constexpr int SUB = KS < 32 || (DP == 256 && NH == 2) ? 16 : 32;
     using PT = std::conditional_t<Q8, __half, T>;            // operand type of both products
     constexpr bool LOW = !Q8 || std::is_same_v<T, __half>;   // weights in two parts
     extern __shared__ __align__(1024) uint8_t smem[];

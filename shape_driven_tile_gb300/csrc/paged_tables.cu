@@ -138,11 +138,11 @@ __global__ void __launch_bounds__(kTablesThreads) paged_tables_kernel(const Tabl
 
 using namespace sdt;
 
-extern "C" int paged_tables(int64_t batch, int64_t page_size, int64_t max_pages, const int32_t *lens,
-                            const int32_t *new_tokens, const int32_t *free_pages, int64_t num_free, int32_t *table,
-                            int64_t table_stride, int32_t *kv_lens, int32_t *starts, int64_t *slots, int64_t num_slots,
-                            int32_t *used, sdt_stream_t stream) {
+extern "C" int paged_tables(const sdt_paged_step *step, sdt_stream_t stream) {
     clear_error();
+    if (!step) return fail(SDT_ERR_NULL, "paged_tables: NULL arguments");
+    const auto &[lens, new_tokens, free_pages, table, kv_lens, starts, used, slots, batch, page_size, max_pages, table_stride,
+                 num_free, num_slots] = *step;
     if (batch < 1 || batch > kTablesMaxBatch)
         return fail(SDT_ERR_SHAPE, "paged_tables: batch must be in 1 .. %d (got %lld)", kTablesMaxBatch, (long long)batch);
     if (page_size < 1 || max_pages < 0 || num_free < 0 || num_slots < 0 || max_pages > INT32_MAX || num_free > INT32_MAX ||

@@ -8,6 +8,7 @@ the current stream, without a synchronisation, so a step can be captured in a CU
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -24,6 +25,9 @@ DTYPE_CODES = {torch.float16: 0, torch.bfloat16: 1, torch.int8: 2}
 _current_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 _I32, _I64 = torch.int32, torch.int64
+# sdt_paged_step and sdt_paged_attn (include/sdt.h): packing them takes a fraction of what ctypes takes
+# for as many arguments
+_STEP, _ATTN = struct.Struct("8P6q"), struct.Struct("7P10qfi")
 _functions = {}
 
 
@@ -127,7 +131,7 @@ class PagedCache:
                     # a dimension of one never steps
                     setattr(d, f"{short}_{axis}", t.stride(dim) if t.shape[dim] > 1 else 0)
         self.descriptor = d
-        self._ref = ctypes.byref(d)
+        self._ref, self._address = ctypes.byref(d), ctypes.addressof(d)
 
 
 def paged_tables(lens, new_tokens, free_pages, table, *, page_size: int, slots, kv_lens=None, starts=None, used=None,
@@ -175,10 +179,11 @@ def paged_tables(lens, new_tokens, free_pages, table, *, page_size: int, slots, 
         used = torch.empty(1, dtype=_I32, device=lens.device)
     else:
         _need_vector(used, "used", _I32, 1)
-    check(_fn("paged_tables")(batch, page_size, wide, lens.data_ptr(), new_tokens.data_ptr(), free_pages.data_ptr(),
-                              len(free_pages), table.data_ptr(), step if batch > 1 else wide, kv_lens.data_ptr(),
-                              starts.data_ptr(), slots.data_ptr(), len(slots), used.data_ptr(),
-                              _current_stream(dev) if stream is None else _handle(stream)))
+    check(_fn("paged_tables")(
+        _STEP.pack(lens.data_ptr(), new_tokens.data_ptr(), free_pages.data_ptr(), table.data_ptr(), kv_lens.data_ptr(),
+                   starts.data_ptr(), used.data_ptr(), slots.data_ptr(), batch, page_size, wide,
+                   step if batch > 1 else wide, len(free_pages), len(slots)),
+        _current_stream(dev) if stream is None else _handle(stream)))
     return kv_lens, starts, slots, used
 
 
@@ -265,10 +270,10 @@ def paged_attn_m1(q, cache: PagedCache, table, lens, out=None, *, workspace, sca
         if lse.shape != (batch, q_heads) or not lse.is_contiguous():
             raise ValueError(f"lse must be contiguous {(batch, q_heads)}")
     # (a dimension of one never steps: its stride may be anything)
-    check(_fn("paged_attn_m1")(batch, q_heads, q.data_ptr(), qb if batch > 1 else 0, qh if q_heads > 1 else 0,
-                               DTYPE_CODES[dtype], cache._ref, table.data_ptr(), step if batch > 1 else wide, wide,
-                               lens.data_ptr(), window, head_dim ** -0.5 if scale is None else scale, out.data_ptr(),
-                               ob if batch > 1 else 0, oh if q_heads > 1 else 0,
-                               None if lse is None else lse.data_ptr(), workspace.data_ptr(), len(workspace),
-                               _current_stream(dev) if stream is None else _handle(stream)))
+    check(_fn("paged_attn_m1")(
+        _ATTN.pack(q.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), table.data_ptr(), lens.data_ptr(),
+                   cache._address, workspace.data_ptr(), batch, q_heads, qb if batch > 1 else 0, qh if q_heads > 1 else 0,
+                   ob if batch > 1 else 0, oh if q_heads > 1 else 0, step if batch > 1 else wide, wide, window,
+                   len(workspace), head_dim ** -0.5 if scale is None else scale, DTYPE_CODES[dtype]),
+        _current_stream(dev) if stream is None else _handle(stream)))
     return out

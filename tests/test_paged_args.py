@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import shape_driven_tile_gb300 as sdt
-from shape_driven_tile_gb300 import _lib
+from shape_driven_tile_gb300 import _lib, paged
 
 A = 0x10000  # an address that is aligned to everything; never followed
 NULL, ALIGN, SHAPE, ARG = -1, -2, -3, -10
@@ -23,11 +23,11 @@ def cache(**kw):
 
 
 def attn(c, **kw):
-    a = dict(batch=4, q_heads=8, q=A, q_batch=512, q_head=64, dtype=1, cache=ctypes.byref(c), table=A, table_stride=10,
-             max_pages=10, lens=A, window=0, scale=1.0, out=A, out_batch=512, out_head=64, lse=None, workspace=A,
-             workspace_bytes=1 << 30, stream=None)
+    a = dict(q=A, out=A, lse=0, table=A, lens=A, cache=ctypes.addressof(c), workspace=A, batch=4, q_heads=8, q_batch=512,
+             q_head=64, out_batch=512, out_head=64, table_stride=10, max_pages=10, window=0, workspace_bytes=1 << 30,
+             scale=1.0, dtype=1)
     assert not set(kw) - set(a)
-    return sdt.lib().paged_attn_m1(*{**a, **kw}.values())
+    return sdt.lib().paged_attn_m1(paged._ATTN.pack(*(0 if v is None else v for v in {**a, **kw}.values())), None)
 
 
 def append(c, **kw):
@@ -38,10 +38,10 @@ def append(c, **kw):
 
 
 def tables(**kw):
-    a = dict(batch=4, page_size=16, max_pages=10, lens=A, new_tokens=A, free_pages=A, num_free=5, table=A, table_stride=10,
-             kv_lens=A, starts=A, slots=A, num_slots=4, used=A, stream=None)
+    a = dict(lens=A, new_tokens=A, free_pages=A, table=A, kv_lens=A, starts=A, used=A, slots=A, batch=4, page_size=16,
+             max_pages=10, table_stride=10, num_free=5, num_slots=4)
     assert not set(kw) - set(a)
-    return sdt.lib().paged_tables(*{**a, **kw}.values())
+    return sdt.lib().paged_tables(paged._STEP.pack(*(0 if v is None else v for v in {**a, **kw}.values())), None)
 
 
 BAD_CACHES = [
@@ -64,6 +64,11 @@ def test_caches(change, status):
 
 def test_no_cache():
     assert sdt.lib().paged_append(4, A, 128, 64, A, 128, 64, 1, A, None, None) == NULL
+    assert attn(cache(), cache=None) == NULL
+
+
+def test_no_arguments():
+    assert sdt.lib().paged_attn_m1(None, None) == NULL and sdt.lib().paged_tables(None, None) == NULL
 
 
 @pytest.mark.parametrize("change,status", [

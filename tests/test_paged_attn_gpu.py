@@ -252,3 +252,26 @@ def test_graph_replay_follows_the_lengths(cuda_device):
         torch.cuda.synchronize()
         want, _, tol, _ = _paged.attention(q, cache, table, step)
         _paged.assert_within(out, want, tol)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("D,heads,q8", [(64, 8, False), (128, 8, False), (256, 4, False), (64, 8, True), (128, 8, True), (256, 4, True),
+                                        (40, 8, False), (192, 4, True)])
+def test_many_items(cuda_device, D, heads, q8, dtype):
+    """Enough requests and heads for CTAs of one warp (and, in q8 of 128, of four all the same)."""
+    lens = [(i * 29) % 70 for i in range(256)]
+    lens[100], lens[255] = 1500, 600
+    run(cuda_device, lens, 2 * heads, heads, D, 16, dtype, q8, layout="head", seed=D)
+
+
+def test_many_items_of_odd_pages_in_a_window(cuda_device):
+    lens = [(i * 31) % 150 for i in range(240)]
+    run(cuda_device, lens, 16, 8, 64, 12, BF16, window=77)
+    run(cuda_device, lens, 56, 8, 80, 12, F16, window=77)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("group", [32, 64])
+def test_many_pieces_join_in_two_levels(cuda_device, group, q8):
+    """One long request of one key head: its pieces are more than one CTA joins at once."""
+    run(cuda_device, [30007, 5], group, 1, 128, 16, BF16, q8, seed=group)
