@@ -3,8 +3,8 @@
 //
 // q8 of one group of 32 values: s = fp16(max|x| * fl32(1/127)) (at most 65504), q = x / s
 // rounded to the nearest integer, ties to even, within +-127; s = 0 gives q = 0, and a NaN
-// is stored as 0.  Divisions would take more time than the memory traffic (23.8 us instead of
-// DIVISION for 8191 tokens of 8 heads of 128), and x times fl(1/s) is enough: x has at most 11
+// is stored as 0.  Divisions would take more time than the memory traffic (15.0 us without, 23.8 with them,
+// 23.8 for 8191 tokens of 8 heads of 128), and x times fl(1/s) is enough: x has at most 11
 // bits, is at least s/2 where a tie can be, and s has 11, so x/s is a tie exactly or at least
 // 2^-12 away from one, while the product is off by 2^-15 at most.  Adding and taking away
 // 1536 = 1.5 * 2^10 rounds it to a multiple of 2^-13, which puts a tie back where it belongs;
