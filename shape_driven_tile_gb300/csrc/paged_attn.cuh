@@ -90,9 +90,8 @@ struct AttnCfg {
     // where one fits: one-warp CTAs and q8 take two.  Four warps of 16-bit heads of 128 have three
     // stages, two CTAs an SM; wider heads have the SM to themselves.
     static constexpr bool fits(int s, int bytes) { return s * (STAGE + ROWS * QROW) + 2048 <= bytes; }
-    // An item costs about this many units besides its own (queries, join of the warps, output).  Four
-    // warps have larger units and few items: counting it would only leave CTAs without a unit.
-    static constexpr int COST = NW == 1 ? 1 : 0;
+    // What an item costs besides its units (queries, join of the warps, output), in units.
+    static constexpr int COST = NW == 1 || Q8 ? 1 : 2;
     static constexpr int S = NW == 1 || DP == 64 || (Q8 && DP == 128) ? 2 : fits(3, 113 * 1024) || (!fits(2, 113 * 1024) && fits(3, 227 * 1024)) ? 3 : 2;
     static constexpr int smem(int q_rows) { return S * (STAGE + q_rows * QROW); }
     static_assert(fits(S, 227 * 1024), "shared memory of an SM");
@@ -200,7 +199,7 @@ __host__ __device__ constexpr uint32_t swizzle(uint32_t r) {
 
 // Where in the work a reader stands: the unit that begins with key `key` of the keys [lo, len) of
 // one item (request b, key head h, block hb of its query heads), and the unit's place, where an
-// item takes COST places and then one for each unit, counted from the CTA's first.
+// item takes `cost` places and then one for each unit, counted from the CTA's first.
 struct AttnWalk {
     int b, h, hb, key, lo, len, at;
 };
@@ -273,14 +272,13 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
     // a thread's requests are consecutive: one scan over the threads' sums finds everything
     const int per = (p.batch + NTH - 1) / NTH;
     const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
-    long long mine = 0, real = 0;  // places and units of this thread's requests, one head
+    long long mine = 0;  // units of this thread's requests, one head
 #pragma unroll 4
     for (int b = b0; b < b1; ++b) {
         int lo, len;
         if (range_of(b, lo, len) && blockIdx.x == 0) paged_status(p.status, kSiteLength);
-        real += units_in(lo, len);
+        mine += units_in(lo, len);
     }
-    mine = real + static_cast<long long>(b1 - b0) * C::COST;
     long long inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -289,15 +287,18 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
     }
     if (lane == 31) sh_sum[warp] = inc;
     cta_sync();
-    long long V = 0;
+    long long U = 0;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
         if (w < warp) inc += sh_sum[w];
-        V += sh_sum[w];
+        U += sh_sum[w];
     }
     const long long H = static_cast<long long>(p.kv_heads) * p.head_blocks;
-    const long long U = (V - static_cast<long long>(p.batch) * C::COST) * H;  // units
-    V *= H;                                                                   // places
+    // An item's own cost counts where CTAs have several units; where they have one or two it would only
+    // leave some without any.
+    const int cost = U * H >= 4ll * gridDim.x ? C::COST : 0;
+    const long long V = (U + static_cast<long long>(p.batch) * cost) * H;  // places
+    U *= H;                                                                // units
     // CTAs with work: one for a unit while there are few, then two units each, which halves the pieces to
     // join (one request of 4096 tokens and 8 key heads: 11.3 instead of 12.6 us)
     const long long P = U <= 128 ? min(U, static_cast<long long>(gridDim.x)) : min(max(U / 2, 128ll), static_cast<long long>(gridDim.x));
@@ -313,13 +314,13 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
         else if (V * (i + 1) < (v + 1) * P) ++i;
         return i;
     };
-    if (v0 < inc * H && v0 >= (inc - mine) * H) {  // place v0 is in one of this thread's requests
-        long long at = (inc - mine) * H;
+    long long at = (inc - mine + static_cast<long long>(b0) * cost) * H;
+    if (v0 >= at && v0 < (inc + static_cast<long long>(b1) * cost) * H) {  // place v0 is in one of this thread's requests
         int b = b0;
         for (; b < b1; ++b) {
             int lo, len;
             range_of(b, lo, len);
-            const long long n = static_cast<long long>(units_in(lo, len) + C::COST) * H;
+            const long long n = static_cast<long long>(units_in(lo, len) + cost) * H;
             if (v0 < at + n) break;
             at += n;
         }
@@ -332,7 +333,7 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
         ++w.at;
         w.key += TK;
         if (w.key >= w.len) {
-            w.at += C::COST;
+            w.at += cost;
             if (++w.hb == p.head_blocks) {
                 w.hb = 0;
                 if (++w.h == p.kv_heads) {
@@ -348,12 +349,12 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
     const int *pw_pages = p.table + pw.b * p.table_stride;  // its request's pages
     range_of(pw.b, pw.lo, pw.len);
     {
-        const int n = units_in(pw.lo, pw.len) + C::COST, item = static_cast<int>(div_small(sh_rest, n));
-        const int at = static_cast<int>(sh_rest - static_cast<long long>(item) * n), j = max(at - C::COST, 0);
+        const int n = units_in(pw.lo, pw.len) + cost, item = static_cast<int>(div_small(sh_rest, n));
+        const int at = static_cast<int>(sh_rest - static_cast<long long>(item) * n), j = max(at - cost, 0);
         pw.h = item / p.head_blocks;
         pw.hb = item - pw.h * p.head_blocks;
         pw.key = pw.lo + j * TK;
-        pw.at = j + C::COST - at;
+        pw.at = j + cost - at;
     }
     if (pw.at >= places) return;  // a share without units
     AttnWalk cw = pw;             // the products' place
