@@ -177,6 +177,12 @@ __device__ __forceinline__ float pow2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// 1 / x within 2^-23, for normal x
+__device__ __forceinline__ float reciprocal(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t v;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
@@ -533,7 +539,7 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
     auto heads_of = [&](int hb) { return min(p.group - hb * C::ROWS, C::ROWS); };  // query heads of the block
     auto store = [&](int b, int h, int hb, int r, int col, const float4 &v, float M, float L) {
         const int head = h * p.group + hb * C::ROWS + r;
-        const float inv = L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;  // no key: zeros; a NaN sum stays NaN
+        const float inv = L > 0.f ? reciprocal(L) : L == 0.f ? 0.f : L;  // no key: zeros; a NaN sum stays NaN
         if (col < p.head_dim)
             *reinterpret_cast<uint2 *>(p.out + b * p.o_batch + static_cast<int64_t>(head) * p.o_head + col * 2) =
                 make_uint2(pack2<T>(v.x * inv, v.y * inv), pack2<T>(v.z * inv, v.w * inv));
