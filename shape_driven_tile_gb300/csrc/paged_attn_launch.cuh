@@ -43,10 +43,16 @@ static cudaError_t launch_variant(PagedAttnArgs a, const PagedAttnLaunch &l) {
 
 template <typename T, int DP, bool Q8>
 static cudaError_t launch_of(const PagedAttnArgs &a, const PagedAttnLaunch &l) {
-    const PagedAttnVariant v = l.variant;
-    if (v.wh == 4) return launch_variant<T, DP, 2, 4, 4, Q8>(a, l);
-    if (v.wh == 2) return launch_variant<T, DP, 2, 2, 4, Q8>(a, l);
-    if (v.nh == 2) return launch_variant<T, DP, 2, 1, 4, Q8>(a, l);
+    const PagedAttnVariant v = l.variant;  // (every variant that paged_attn_variant names for this width)
+    if constexpr (DP == 256) {
+        if constexpr (!Q8)
+            if (v.nh == 2) return launch_variant<T, DP, 2, 4, 4, Q8>(a, l);
+        if (v.wh == 4) return launch_variant<T, DP, 1, 4, 4, Q8>(a, l);
+        if (v.wh == 2) return launch_variant<T, DP, 1, 2, 4, Q8>(a, l);
+    } else if (v.nh == 2) {
+        if (v.wh == 4) return launch_variant<T, DP, 2, 4, 4, Q8>(a, l);
+        return v.wh == 2 ? launch_variant<T, DP, 2, 2, 4, Q8>(a, l) : launch_variant<T, DP, 2, 1, 4, Q8>(a, l);
+    }
     if constexpr (!(Q8 && DP == 128))
         if (v.nw == 1) return launch_variant<T, DP, 1, 1, 1, Q8>(a, l);
     return launch_variant<T, DP, 1, 1, 4, Q8>(a, l);
