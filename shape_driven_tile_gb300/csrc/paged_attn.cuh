@@ -570,53 +570,16 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
     };
     // Joins `count` pieces i0, i0 + step, ... of the item, to the output or over piece i0.  The ring is
     // free by now: EB float4 of o per thread and piece come through it, as many pieces at once as it
-    // holds, so that a join costs one trip to L2 and not one per few pieces.
-    auto join = [&](const AttnPiece &item, int i0, int step, int count, bool final) {
-        constexpr int EB = 4, BLOCK = EB * NTH;             // float4 of o at a time
+    // holds, so that a join costs a trip to L2 or two and not one per few pieces.  (EB is as small as the
+    // rows allow: few warps run here, and instructions that do nothing cost as much as others.)
+    auto join_wide = [&](auto eb, const AttnPiece &item, int i0, int step, int count, bool final) {
+        constexpr int EB = decltype(eb)::value, BLOCK = EB * NTH;  // float4 of o at a time
         constexpr int HELD = BLOCK * 16 + 2 * C::ROWS * 4;  // bytes of a piece in the ring: o, m, l
         constexpr int AT_ONCE = S * C::STAGE / HELD;
         static_assert(AT_ONCE >= 2, "a join makes progress");
         const float *base = p.partials + static_cast<size_t>(2 * item.first) * C::SLOT;
         auto at = [&](int i) { return base + static_cast<size_t>(i == 0 ? 1 : 2 * i) * C::SLOT; };
         const int all = heads_of(item.hb) * (DP / 4);
-        if (all * 2 <= NTH && final) {
-            // few float4: groups of threads take every so many-th piece, straight from L2, and meet at the end
-            const int groups = NTH / all, mine = tid / all, e = tid - mine * all, r = e / (DP / 4);
-            float M = -INFINITY, L = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (mine < groups)
-#pragma unroll 4
-                for (int i = mine; i < count; i += groups) {
-                    const float *src = at(i0 + i * step);
-                    const float mi = __ldcg(src + C::ROWS * DP + r), li = __ldcg(src + C::ROWS * (DP + 1) + r);
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + e * 4));
-                    const float top = fmaxf(M, mi);
-                    const float f = M == top ? 1.f : pow2(M - top), w = mi == top ? 1.f : pow2(mi - top);  // (both -inf: zeros either way)
-                    M = top;
-                    L = L * f + li * w;
-                    acc = make_float4(acc.x * f + v.x * w, acc.y * f + v.y * w, acc.z * f + v.z * w, acc.w * f + v.w * w);
-                }
-            float4 *o4 = reinterpret_cast<float4 *>(smem);
-            float2 *ml = reinterpret_cast<float2 *>(smem + NTH * 16);
-            o4[tid] = acc;
-            ml[tid] = make_float2(M, L);
-            cta_sync();
-            if (mine == 0) {
-#pragma unroll 1
-                for (int i = 1; i < groups; ++i) {
-                    const float2 y = ml[i * all + e];
-                    const float4 v = o4[i * all + e];
-                    const float top = fmaxf(M, y.x);
-                    const float f = M == top ? 1.f : pow2(M - top), w = y.x == top ? 1.f : pow2(y.x - top);
-                    M = top;
-                    L = L * f + y.y * w;
-                    acc = make_float4(acc.x * f + v.x * w, acc.y * f + v.y * w, acc.z * f + v.z * w, acc.w * f + v.w * w);
-                }
-                store(item.b, item.h, item.hb, r, (e % (DP / 4)) * 4, acc, M, L);
-            }
-            cta_sync();
-            return;
-        }
         for (int e0 = 0; e0 < all; e0 += BLOCK) {
             const int block = min(BLOCK, all - e0);
             float M[EB], L[EB];
@@ -691,6 +654,54 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
                 const_cast<float *>(at(i0))[C::ROWS * (DP + 1) + r] = st_l[r / C::HEADS][r % C::HEADS];
             }
             cta_sync();
+        }
+    };
+
+    auto join = [&](const AttnPiece &item, int i0, int step, int count, bool final) {
+        const int all = heads_of(item.hb) * (DP / 4);
+        if (all * 2 <= NTH && final) {
+            // few float4: groups of threads take every so many-th piece, straight from L2, and meet at the end
+            const int groups = NTH / all, mine = tid / all, e = tid - mine * all, r = e / (DP / 4);
+            float M = -INFINITY, L = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (mine < groups)
+#pragma unroll 4
+                for (int i = mine; i < count; i += groups) {
+                    const int y = i0 + i * step;
+                    const float *src = p.partials + static_cast<size_t>(2 * item.first + (y == 0 ? 1 : 2 * y)) * C::SLOT;
+                    const float mi = __ldcg(src + C::ROWS * DP + r), li = __ldcg(src + C::ROWS * (DP + 1) + r);
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + e * 4));
+                    const float top = fmaxf(M, mi);
+                    const float f = M == top ? 1.f : pow2(M - top), w = mi == top ? 1.f : pow2(mi - top);  // (both -inf: zeros either way)
+                    M = top;
+                    L = L * f + li * w;
+                    acc = make_float4(acc.x * f + v.x * w, acc.y * f + v.y * w, acc.z * f + v.z * w, acc.w * f + v.w * w);
+                }
+            float4 *o4 = reinterpret_cast<float4 *>(smem);
+            float2 *ml = reinterpret_cast<float2 *>(smem + NTH * 16);
+            o4[tid] = acc;
+            ml[tid] = make_float2(M, L);
+            cta_sync();
+            if (mine == 0) {
+#pragma unroll 1
+                for (int i = 1; i < groups; ++i) {
+                    const float2 y = ml[i * all + e];
+                    const float4 v = o4[i * all + e];
+                    const float top = fmaxf(M, y.x);
+                    const float f = M == top ? 1.f : pow2(M - top), w = y.x == top ? 1.f : pow2(y.x - top);
+                    M = top;
+                    L = L * f + y.y * w;
+                    acc = make_float4(acc.x * f + v.x * w, acc.y * f + v.y * w, acc.z * f + v.z * w, acc.w * f + v.w * w);
+                }
+                store(item.b, item.h, item.hb, r, (e % (DP / 4)) * 4, acc, M, L);
+            }
+            cta_sync();
+        } else if (all <= NTH) {
+            join_wide(std::integral_constant<int, 1>{}, item, i0, step, count, final);
+        } else if (all <= 2 * NTH) {
+            join_wide(std::integral_constant<int, 2>{}, item, i0, step, count, final);
+        } else {
+            join_wide(std::integral_constant<int, 4>{}, item, i0, step, count, final);
         }
     };
 
