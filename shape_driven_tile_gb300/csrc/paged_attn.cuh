@@ -8,12 +8,20 @@
 //
 // What bounds it: HBM.  A cached token costs 4 G flops per key and value element pair of 4
 // bytes (2 in q8), which the matrix instructions do at a fraction of their rate; the design
-// keeps enough bytes in flight and few instructions per byte.
+// keeps enough bytes in flight and few instructions per byte.  GB300, against the measured
+// copy rate of 6782 GB/s: 64 requests of 1000 to 32768 tokens, 8 key heads of 128 in fp16 (2.42
+// GB), 351 us, 6.9 TB/s; one request of 131071 tokens (537 MB) 84.4 us, 6.4 TB/s; 16 ragged
+// requests (62 MB) 16.9 us, of which 2.3 us pass before the first keys arrive and 3.5 us join the
+// split items.  q8 is bound by its arithmetic: 520 instructions per 16 keys and warp to widen,
+// scale and multiply 4 KB (48 requests of 500 to 16000 tokens, 476 MB, 96.4 us, 4.9 TB/s).  Few
+// tokens cost a chain of trips to memory, lengths -> pages -> keys -> output: 3.7 us for 17.
 //
 // Work: a unit is TK consecutive keys of one (request, key head, block of query heads).
 // The units of all requests, in that order, are dealt out evenly over one resident grid, so
 // a batch of any mix of lengths keeps every SM streaming to the end; a CTA computes its
-// share from `lens` by itself.  A share may begin and end inside a (request, head) item:
+// share from `lens` by itself.  An item's own cost counts as a unit or two: equal units alone
+// gave CTAs with many short items up to 1.6 times the mean time (25 requests of 30 to 6667 tokens,
+// 32 heads of 80: 94 us, with it 64 us).  A share may begin and end inside a (request, head) item:
 // such pieces go to the workspace as (m, l, o) in fp32 and the last CTA to arrive at the
 // item joins them in the order of the keys, so results do not depend on the order of
 // arrival.
@@ -45,7 +53,7 @@
 
 namespace sdt {
 
-constexpr float kAttnSlack = 8.f;  // log2 of the largest weight
+constexpr float kAttnSlack = 8.f;  // log2 of the largest weight: far from fp16's 65504, and rarely passed
 constexpr int kAttnFlat = 256;     // most pieces x query heads that are joined in one level
 
 struct PagedAttnArgs {
@@ -74,7 +82,8 @@ struct AttnCfg {
     static constexpr int THREADS = NW * 32;
     static constexpr int ROWB = DP * (Q8 ? 1 : 2);        // bytes of a cached row in shared memory
     // Keys per warp of a unit: about 8 KB of keys and values, and room for the warp's o (8 NH x DP
-    // fp32), which passes through the stage at an item's end.
+    // fp32), which passes through the stage at an item's end.  Smaller units cost more instructions a key
+    // (q8 of 128, 48 requests of 4096: 16 keys a warp 96.4 us, 32 keys 75.8).
     static constexpr int KW = Q8 ? (DP == 256 && NH == 1 ? 16 : 32) : (DP == 64 ? 32 : 16);
     static constexpr int TK = KW * NW;                    // keys of a unit
     static constexpr int WK = NW / WH;                    // groups of warps with keys of their own
@@ -87,12 +96,15 @@ struct AttnCfg {
     static constexpr int SLOT = ROWS * (DP + 2);          // floats of a partial
     static constexpr int QROW = DP * 2;                   // bytes of a query row in shared memory
     // The warps of an SM hide each other's latency, so stages beyond two are worth less than another CTA
-    // where one fits: one-warp CTAs and q8 take two.  Four warps of 16-bit heads of 128 have three
-    // stages, two CTAs an SM; wider heads have the SM to themselves.
+    // where one fits: one-warp CTAs, heads of 64 and q8 of 128 take two (that: 109 us with three CTAs an SM,
+    // 126 with three stages and two CTAs).  Four warps of 16-bit heads of 128 have three stages, two CTAs
+    // an SM (one request of 8192 tokens 16.0 us; two stages, three CTAs and their pieces 21.0; 2.42 GB of
+    // cache the same within 2 %); wider heads have the SM to themselves.
     static constexpr bool fits(int s, int bytes) { return s * (STAGE + ROWS * QROW) + 2048 <= bytes; }
-    // What an item costs besides its units (queries, join of the warps, output), in units.
-    static constexpr int COST = NW == 1 || Q8 ? 1 : 2;
     static constexpr int S = NW == 1 || DP == 64 || (Q8 && DP == 128) ? 2 : fits(3, 113 * 1024) || (!fits(2, 113 * 1024) && fits(3, 227 * 1024)) ? 3 : 2;
+    // What an item costs besides its units (queries, join of the warps, output), in units: measured 1.5 to
+    // 2.3 us an item against 0.9 to 1.4 us a unit, and 3 us a unit in q8 of 128.
+    static constexpr int COST = NW == 1 || Q8 ? 1 : 2;
     static constexpr int smem(int q_rows) { return S * (STAGE + q_rows * QROW); }
     static_assert(fits(S, 227 * 1024), "shared memory of an SM");
     static_assert(STAGE >= NW * HEADS * DP * 4, "the stage must hold every warp's o");
