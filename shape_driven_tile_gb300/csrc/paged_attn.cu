@@ -1,11 +1,91 @@
 // paged_attn.cu -- paged_attn_m1: argument checks and dispatch of the paged attention kernel.
 #include <algorithm>
 
+#include "launch.cuh"
 #include "paged_attn.cuh"
 #include "paged_attn_plan.cuh"
 
+namespace sdt {
+
+// Joins the pieces of split items: a CTA takes 64 columns of one row, 16 groups of 16 threads every
+// sixteenth piece, and meets at the end in the order of the groups.
+constexpr int kJoinGroups = 16, kJoinWide = 16, kJoinThreads = kJoinGroups * kJoinWide;
+constexpr int kJoinPieces = 1024;  // no grid of four-warp CTAs is larger
+
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) paged_attn_join_kernel(const PagedAttnArgs p, int width, int rows) {
+    __shared__ float weight[kJoinPieces];
+    __shared__ float red[2][kJoinThreads / 32];
+    __shared__ float4 meet[kJoinThreads];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, item = blockIdx.y;
+    const int parts = width / 64, r = blockIdx.x / parts, part = blockIdx.x % parts;
+    const int hb = item % p.head_blocks, h = item / p.head_blocks % p.kv_heads, b = item / p.head_blocks / p.kv_heads;
+    const int2 split = p.split[item];
+    const int n = min(split.y, kJoinPieces);
+    if (n == 0 || hb * rows + r >= p.group) return;
+    const int slot = rows * (width + 2);  // floats
+    // piece 0 lies in its CTA's second slot, the others in their first
+    auto at = [&](int i) { return p.partials + static_cast<size_t>(2 * (split.x + i) + (i == 0 ? 1 : 0)) * slot; };
+    float M = -INFINITY, L = 0.f;
+    for (int i = tid; i < n; i += kJoinThreads) {
+        weight[i] = at(i)[rows * width + r];
+        M = fmaxf(M, weight[i]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (lane == 0) red[0][warp] = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w) M = fmaxf(M, red[0][w]);
+    for (int i = tid; i < n; i += kJoinThreads) {
+        const float w = weight[i] == M ? 1.f : pow2(weight[i] - M);  // (both -inf: zeros either way)
+        L += at(i)[rows * (width + 1) + r] * w;
+        weight[i] = w;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (lane == 0) red[1][warp] = L;
+    __syncthreads();
+    L = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w) L += red[1][w];
+    const int group = tid / kJoinWide, col = part * 64 + (tid % kJoinWide) * 4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int i = group; i < n; i += kJoinGroups) {
+        const float4 v = *reinterpret_cast<const float4 *>(at(i) + r * width + col);
+        const float w = weight[i];
+        acc = make_float4(acc.x + v.x * w, acc.y + v.y * w, acc.z + v.z * w, acc.w + v.w * w);
+    }
+    meet[tid] = acc;
+    __syncthreads();
+    if (group > 0) return;
+    for (int g = 1; g < kJoinGroups; ++g) {
+        const float4 v = meet[g * kJoinWide + tid];
+        acc = make_float4(acc.x + v.x, acc.y + v.y, acc.z + v.z, acc.w + v.w);
+    }
+    const int head = h * p.group + hb * rows + r;
+    const float inv = L > 0.f ? reciprocal(L) : L == 0.f ? 0.f : L;  // no key: zeros; a NaN sum stays NaN
+    if (col < p.head_dim)
+        *reinterpret_cast<uint2 *>(p.out + b * p.o_batch + head * p.o_head + col * 2) =
+            make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
+    if (p.lse && col == 0)
+        p.lse[static_cast<int64_t>(b) * p.kv_heads * p.group + head] = L == 0.f ? -INFINITY : M * 0.6931471805599453f + logf(L);
+}
+
+cudaError_t launch_paged_attn_join(const PagedAttnArgs &a, bool f16, int width, int rows, int items, cudaStream_t stream) {
+    const dim3 grid(static_cast<unsigned>(std::min(a.group, rows) * (width / 64)), static_cast<unsigned>(items));
+    return launch_kernel(f16 ? paged_attn_join_kernel<__half> : paged_attn_join_kernel<__nv_bfloat16>, grid, dim3(kJoinThreads), 0,
+                         stream, 1, a, width, rows);
+}
+
+}  // namespace sdt
+
 using namespace sdt;
 
+static constexpr size_t kSplitBytes = size_t(kAttnSplitItems) * sizeof(int2);
 static constexpr size_t kCounterBytes = size_t(1) << 20;  // the counter region of the split-K workspaces
 static constexpr int64_t kMaxTokens = INT32_MAX - 1024;   // a row's tokens; key indices run past them by a unit at most
 
@@ -18,7 +98,7 @@ static size_t workspace_for(int64_t group, int64_t head_dim, int sm_count) {
         const size_t slot = static_cast<size_t>(8 * v.nh * v.wh) * (paged_attn_width(head_dim) + 2) * sizeof(float);
         most = std::max(most, 2 * static_cast<size_t>(sm_count) * paged_attn_ctas(v.nw) * slot);  // two pieces a CTA
     }
-    return kCounterBytes + most;
+    return kCounterBytes + kSplitBytes + most;
 }
 
 extern "C" {
@@ -97,7 +177,8 @@ int paged_attn_m1(const sdt_paged_attn *call, sdt_stream_t stream) {
     a.page = FastDiv::of(static_cast<uint32_t>(cache->page_size));
     a.scale_log2 = scale * 1.4426950408889634f;
     a.counters = static_cast<unsigned *>(workspace);
-    a.partials = reinterpret_cast<float *>(static_cast<char *>(workspace) + kCounterBytes);
+    a.split = reinterpret_cast<int2 *>(static_cast<char *>(workspace) + kCounterBytes);
+    a.partials = reinterpret_cast<float *>(static_cast<char *>(workspace) + kCounterBytes + kSplitBytes);
     a.status = status;
     const int dp = paged_attn_width(a.head_dim);
     cudaError_t e;

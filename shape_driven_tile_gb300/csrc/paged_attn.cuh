@@ -74,6 +74,9 @@ struct PagedAttnArgs {
     int q_rows;                // query rows that a CTA keeps in shared memory: min(group, 8 NH WH)
     float *partials;           // 2 slots per CTA: [rows][DP] o, [rows] m, [rows] l
     unsigned *counters;        // 3 per CTA, zero between calls
+    int2 *split;               // null: the last CTA to arrive joins an item's pieces; else [items]: the first
+                               // CTA with a piece of an item writes (that CTA, pieces), 0 pieces if it is whole,
+                               // and a kernel of its own joins them
     int *status;
 };
 
@@ -274,7 +277,7 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
     {
         const int64_t line = static_cast<int64_t>(blockIdx.x) * NTH + tid;
         const int64_t bytes = ((p.batch - 1) * p.table_stride + p.max_pages) * 4;
-        if (line * 128 < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(p.table) + line * 128));
+        if (p.max_pages > 0 && line * 128 < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(p.table) + line * 128));
     }
     griddep_wait();
 
@@ -1058,7 +1061,10 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
                 }
             }
             cta_sync();  // the stage and the statistics may be written again; a piece is whole in the workspace
-            if (!whole && tid == 0) {
+            if (p.split) {
+                if (begun_here && tid == 0)
+                    p.split[(cw.b * p.kv_heads + cw.h) * p.head_blocks + cw.hb] = whole ? make_int2(0, 0) : make_int2(left_open.first, left_open.n);
+            } else if (!whole && tid == 0) {
                 if (begun_here) left_ticket = add_acq_rel(counter_of(left_open));
                 else begun_ticket = add_acq_rel(counter_of(begun));
             }
@@ -1069,7 +1075,7 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
     }
 #pragma unroll 1
     for (int x = 0; x < 2; ++x) {
-        if (!(x == 0 ? has_begun : has_left)) continue;
+        if (p.split || !(x == 0 ? has_begun : has_left)) continue;
         const AttnPiece item = x == 0 ? begun : left_open;
         unsigned t = x == 0 ? begun_ticket : left_ticket;
         unsigned *counter = counter_of(item);

@@ -52,6 +52,15 @@ inline PagedAttnVariant paged_attn_variant(int64_t group, int64_t items, int64_t
     return {1, 1, many && !(q8 && width == 128) ? 1 : 4};
 }
 
+// Whether an item's pieces are joined by a kernel of their own: where a piece is large (`values`: of o)
+// and one CTA would join eight or more.  `keys`: units of the longest request, `slots`: CTAs.
+// JOINCOST
+constexpr int kAttnSplitItems = 256;  // items that the workspace has room for then
+inline bool paged_attn_splits(int values, int64_t items, int64_t keys, int64_t slots) {
+    return values >= 4096 && items * 8 <= slots && items <= kAttnSplitItems && keys >= 8;
+}
+cudaError_t launch_paged_attn_join(const PagedAttnArgs &a, bool f16, int width, int rows, int items, cudaStream_t stream);
+
 template <typename T, int DP>
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, const PagedAttnLaunch &l);
 

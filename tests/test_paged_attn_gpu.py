@@ -271,7 +271,24 @@ def test_many_items_of_odd_pages_in_a_window(cuda_device):
 
 
 @pytest.mark.parametrize("q8", [False, True])
-@pytest.mark.parametrize("group", [32, 64])
-def test_many_pieces_join_in_two_levels(cuda_device, group, q8):
-    """One long request of one key head: its pieces are more than one CTA joins at once."""
-    run(cuda_device, [30007, 5], group, 1, 128, 16, BF16, q8, seed=group)
+@pytest.mark.parametrize("group,D", [(8, 128), (16, 128), (32, 128), (64, 128), (40, 64), (64, 64), (12, 256), (30, 256), (64, 256), (70, 256)])
+def test_many_pieces_of_an_item(cuda_device, group, D, q8):
+    """Few long requests of one key head: more pieces than one CTA joins at once, or pieces so large that a
+    kernel of its own joins them."""
+    run(cuda_device, [30007, 5, 0, 2049], group, 1, D, 16, BF16, q8, seed=group)
+
+
+def test_steps_that_split_otherwise_share_a_workspace(cuda_device):
+    """One workspace for calls that join in the kernel, in a second kernel, and not at all."""
+    dev = cuda_device
+    ws = sdt.paged_attn_workspace(64, 1, 256)
+    for D, group, lens in ((256, 64, [9000]), (128, 8, [9000]), (128, 64, [20, 1]), (256, 64, [700, 800, 10]), (256, 64, [9000])):
+        table, pool = _paged.tables(lens, 16, 3)
+        cache = _paged.make_cache(pool, 16, 1, D, F16, "token", 0)
+        _paged.fill(cache, table, lens, 4, F16)
+        q = torch.randn(len(lens), group, D, generator=torch.Generator().manual_seed(5)).to(F16)
+        got = sdt.paged_attn_m1(q.to(dev), sdt.PagedCache(*[t.to(dev) for t in cache[:2]]), table.to(dev),
+                                torch.tensor(lens, dtype=torch.int32, device=dev), workspace=ws)
+        want, _, tol, _ = _paged.attention(q, cache, table, lens)
+        _paged.assert_within(got, want, tol)
+        assert not ws[: 1 << 20].any()
