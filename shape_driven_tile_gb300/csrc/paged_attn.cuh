@@ -24,7 +24,7 @@
 // 32 heads of 80: 94 us, with it 64 us).  A share may begin and end inside a (request, head) item:
 // such pieces go to the workspace as (m, l, o) in fp32 and the last CTA to arrive at the
 // item joins them in the order of the keys, so results do not depend on the order of
-// arrival.
+// arrival.  (Large pieces of few items are joined by a second kernel, see paged_attn_splits.)
 //
 // CTA: NW warps, four or one.  WH warps work on the same keys for 8 NH query heads each,
 // NW / WH such groups on neighbouring keys; each group has its own ring of S stages in
