@@ -531,8 +531,8 @@ int paged_append(int64_t tokens, const void *k, int64_t k_token, int64_t k_head,
  * Workspace: device memory owned by the caller, 256-byte aligned, at least
  * sdt_paged_attn_workspace_bytes() bytes: the 1 MiB counter region of the split-K
  * workspaces (zero before the first call, left zero by every completed call; it may be
- * shared with those), then the pieces of requests that are split over CTAs.  Calls that
- * share a workspace must not overlap on the GPU.
+ * shared with those), then a list of the requests that are split over CTAs and their
+ * pieces.  Calls that share a workspace must not overlap on the GPU.
  */
 typedef struct sdt_paged_attn {
     const void *q;

@@ -8,7 +8,9 @@
 namespace sdt {
 
 // Joins the pieces of split items: a CTA takes 64 columns of one row, 16 groups of 16 threads every
-// sixteenth piece, and meets at the end in the order of the groups.
+// sixteenth piece, and meets at the end in the order of the groups.  The pieces lie in L2 and one CTA's
+// loads in flight bound the join, so it is spread over rows and columns: 32 query heads on one key head,
+// 32768 tokens, 15.2 us for both kernels (36.0 joined by one CTA an item).
 constexpr int kJoinGroups = 16, kJoinWide = 16, kJoinThreads = kJoinGroups * kJoinWide;
 constexpr int kJoinPieces = 1024;  // no grid of four-warp CTAs is larger
 

@@ -54,10 +54,12 @@ inline PagedAttnVariant paged_attn_variant(int64_t group, int64_t items, int64_t
 
 // Whether an item's pieces are joined by a kernel of their own: where a piece is large (`values`: of o)
 // and one CTA would join eight or more.  `keys`: units of the longest request, `slots`: CTAs.
-// The second launch costs 2 us on the host and as much on the GPU; one CTA joins 50 GB/s.  4 requests
-// of 4096 tokens, 4 key heads for 64 queries: 13.9 us (19.5 joined by the last CTA to arrive); one key
-// head for 64 queries of 256 and 32768 tokens 28.7 (81.7).  Pieces of half the size gain 0 to 2 us on the
-// GPU, which the host's do not leave.
+// 4 requests of 4096 tokens, 4 key heads for 64 queries of 128: 13.9 us on the GPU (19.5 joined by the
+// last CTA to arrive); one key head for 64 queries of 256 and 32768 tokens 28.7 (81.7).  The second launch
+// costs 2 to 3 us of host time.  Pieces of 1024 values, which most calls of few requests have, are left
+// to the last CTA for that: split they take 10.6 us (14.4; 1 query head, 32768 tokens), 7.3 (10.0; 8 to a
+// key head, 2048), 83.6 (84.8; 64 to 8, 131071), but also 27.2 (26.7; 4 requests of 8192, 32 to 8) and
+// 7.0 (6.5; 32 to 8, 512), where the host's time is most of the call.
 constexpr int kAttnSplitItems = 256;  // items that the workspace has room for then
 inline bool paged_attn_splits(int values, int64_t items, int64_t keys, int64_t slots) {
     return values >= 2048 && items * 8 <= slots && items <= kAttnSplitItems && keys >= 8;
