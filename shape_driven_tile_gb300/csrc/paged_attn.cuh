@@ -54,6 +54,7 @@
 namespace sdt {
 
 constexpr float kAttnSlack = 8.f;  // log2 of the largest weight: far from fp16's 65504, and rarely passed
+constexpr int kAttnSplitValues = 2048;  // least values of a piece's o that a second kernel joins
 constexpr int kAttnFlat = 256;     // most pieces x query heads that are joined in one level
 
 struct PagedAttnArgs {
@@ -98,6 +99,8 @@ struct AttnCfg {
     static constexpr int ROWS = HEADS * WH;               // query heads of a CTA
     static constexpr int SLOT = ROWS * (DP + 2);          // floats of a partial
     static constexpr int QROW = DP * 2;                   // bytes of a query row in shared memory
+    // Whether a call may have its pieces joined by the second kernel (paged_attn_splits).
+    static constexpr bool SPLITS = ROWS * DP >= kAttnSplitValues;
     // The warps of an SM hide each other's latency, so stages beyond two are worth less than another CTA
     // where one fits: one-warp CTAs, heads of 64 and q8 of 128 take two (that: 109 us with three CTAs an SM,
     // 126 with three stages and two CTAs).  Four warps of 16-bit heads of 128 have three stages, two CTAs
@@ -586,7 +589,9 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
     // Joins `count` pieces i0, i0 + step, ... of the item, to the output or over piece i0.  The ring is
     // free by now: EB float4 of o per thread and piece come through it, as many pieces at once as it
     // holds, so that a join costs a trip to L2 or two and not one per few pieces.  (EB is as small as the
-    // rows allow: few warps run here, and instructions that do nothing cost as much as others.)
+    // rows allow: few warps run here, and instructions that do nothing cost as much as others.  CTAs of one
+    // warp have the largest alone: with all three, 256 requests of 1 to 500 tokens, 16 heads of 64, took 23.9
+    // us for 23.0, and of 500 to 4000 tokens 294 for 291.)
     auto join_wide = [&](auto eb, const AttnPiece &item, int i0, int step, int count, bool final) {
         constexpr int EB = decltype(eb)::value, BLOCK = EB * NTH;  // float4 of o at a time
         constexpr int HELD = BLOCK * 16 + 2 * C::ROWS * 4;  // bytes of a piece in the ring: o, m, l
@@ -711,9 +716,9 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
                 store(item.b, item.h, item.hb, r, (e % (DP / 4)) * 4, acc, M, L);
             }
             cta_sync();
-        } else if (all <= NTH) {
+        } else if (NW > 1 && all <= NTH) {
             join_wide(std::integral_constant<int, 1>{}, item, i0, step, count, final);
-        } else if (all <= 2 * NTH) {
+        } else if (NW > 1 && all <= 2 * NTH) {
             join_wide(std::integral_constant<int, 2>{}, item, i0, step, count, final);
         } else {
             join_wide(std::integral_constant<int, 4>{}, item, i0, step, count, final);
@@ -1061,7 +1066,7 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
                 }
             }
             cta_sync();  // the stage and the statistics may be written again; a piece is whole in the workspace
-            if (p.split) {
+            if (C::SPLITS && p.split) {
                 if (begun_here && tid == 0)
                     p.split[(cw.b * p.kv_heads + cw.h) * p.head_blocks + cw.hb] = whole ? make_int2(0, 0) : make_int2(left_open.first, left_open.n);
             } else if (!whole && tid == 0) {
@@ -1075,7 +1080,7 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
     }
 #pragma unroll 1
     for (int x = 0; x < 2; ++x) {
-        if (p.split || !(x == 0 ? has_begun : has_left)) continue;
+        if ((C::SPLITS && p.split) || !(x == 0 ? has_begun : has_left)) continue;
         const AttnPiece item = x == 0 ? begun : left_open;
         unsigned t = x == 0 ? begun_ticket : left_ticket;
         unsigned *counter = counter_of(item);

@@ -38,7 +38,7 @@ static cudaError_t launch_variant(PagedAttnArgs a, const PagedAttnLaunch &l) {
     const int64_t units = std::max<int64_t>(keys, 1) * a.batch * a.kv_heads * a.head_blocks;  // no mix of lengths has more
     const int64_t slots = static_cast<int64_t>(l.sm_count) * ctas;
     const int64_t items = static_cast<int64_t>(a.batch) * a.kv_heads * a.head_blocks;
-    if (!paged_attn_splits(C::ROWS * DP, items, keys, slots)) a.split = nullptr;
+    if (!C::SPLITS || !paged_attn_splits(items, keys, slots)) a.split = nullptr;
     e = launch_kernel(paged_attn_kernel<T, DP, NH, WH, NW, Q8>, dim3(static_cast<unsigned>(std::min(units, slots))),
                       dim3(C::THREADS), C::smem(a.q_rows), l.stream, 1, a);
     if (e == cudaSuccess && a.split)

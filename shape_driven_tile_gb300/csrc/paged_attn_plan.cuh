@@ -52,7 +52,7 @@ inline PagedAttnVariant paged_attn_variant(int64_t group, int64_t items, int64_t
     return {1, 1, many && !(q8 && width == 128) ? 1 : 4};
 }
 
-// Whether an item's pieces are joined by a kernel of their own: where a piece is large (`values`: of o)
+// Whether an item's pieces are joined by a kernel of their own: where a piece is large (kAttnSplitValues)
 // and one CTA would join eight or more.  `keys`: units of the longest request, `slots`: CTAs.
 // 4 requests of 4096 tokens, 4 key heads for 64 queries of 128: 13.9 us on the GPU (19.5 joined by the
 // last CTA to arrive); one key head for 64 queries of 256 and 32768 tokens 28.7 (81.7).  The second launch
@@ -61,8 +61,8 @@ inline PagedAttnVariant paged_attn_variant(int64_t group, int64_t items, int64_t
 // key head, 2048), 83.6 (84.8; 64 to 8, 131071), but also 27.2 (26.7; 4 requests of 8192, 32 to 8) and
 // 7.0 (6.5; 32 to 8, 512), where the host's time is most of the call.
 constexpr int kAttnSplitItems = 256;  // items that the workspace has room for then
-inline bool paged_attn_splits(int values, int64_t items, int64_t keys, int64_t slots) {
-    return values >= 2048 && items * 8 <= slots && items <= kAttnSplitItems && keys >= 8;
+inline bool paged_attn_splits(int64_t items, int64_t keys, int64_t slots) {
+    return items * 8 <= slots && items <= kAttnSplitItems && keys >= 8;
 }
 cudaError_t launch_paged_attn_join(const PagedAttnArgs &a, bool f16, int width, int rows, int items, cudaStream_t stream);
 
