@@ -10,10 +10,10 @@
 // bytes (2 in q8), which the matrix instructions do at a fraction of their rate; the design
 // keeps enough bytes in flight and few instructions per byte.  GB300, against the measured
 // copy rate of 6782 GB/s: 64 requests of 1000 to 32768 tokens, 8 key heads of 128 in fp16 (2.42
-// GB), 351 us, 6.9 TB/s; one request of 131071 tokens (537 MB) 84.4 us, 6.4 TB/s; 16 ragged
+// GB), 350 to 363 us on different machines, 6.7 to 6.9 TB/s; one request of 131071 tokens (537 MB) 84.9 us, 6.3 TB/s; 16 ragged
 // requests (62 MB) 16.9 us, of which 2.3 us pass before the first keys arrive and 3.5 us join the
 // split items.  q8 is bound by its arithmetic: 520 instructions per 16 keys and warp to widen,
-// scale and multiply 4 KB (48 requests of 500 to 16000 tokens, 476 MB, 96.4 us, 4.9 TB/s).  Few
+// scale and multiply 4 KB (48 requests of 500 to 16000 tokens, 476 MB, 99.5 us, 4.8 TB/s).  Few
 // tokens cost a chain of trips to memory, lengths -> pages -> keys -> output: 3.7 us for 17.
 //
 // Work: a unit is TK consecutive keys of one (request, key head, block of query heads).
