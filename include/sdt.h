@@ -492,6 +492,8 @@ typedef struct sdt_paged_cache {
  * no slot.  The same call on the same inputs writes the same values.
  * Negative lengths count as 0, lengths past max_pages * page_size as that; the sum of
  * new_tokens must be below 2^31.
+ * No output may overlap an input or another output (SDT_ERR_ARG): lengths are not updated
+ * in place.
  */
 typedef struct sdt_paged_step {
     const int32_t *lens, *new_tokens, *free_pages;

@@ -135,6 +135,21 @@ __global__ void __launch_bounds__(kTablesThreads) paged_tables_kernel(const Tabl
     }
 }
 
+// A buffer of the call: `rows` stretches of `len` bytes, `step` bytes apart.
+struct Buffer {
+    const char *name, *p;
+    int64_t rows, len, step;
+};
+
+// Whether a byte of x lies in y; x is one stretch.
+static bool lies_in(const Buffer &x, const Buffer &y) {
+    if (!x.len || !y.len || !y.rows) return false;
+    if (x.p + x.len <= y.p || x.p >= y.p + (y.rows - 1) * y.step + y.len) return false;
+    if (x.p < y.p) return true;
+    const int64_t off = x.p - y.p, row = off / y.step;  // x begins in row `row` of y or behind it, before the next
+    return off - row * y.step < y.len || off + x.len > (row + 1) * y.step;
+}
+
 }  // namespace sdt
 
 using namespace sdt;
@@ -156,6 +171,22 @@ extern "C" int paged_tables(const sdt_paged_step *step, sdt_stream_t stream) {
     if (!aligned(lens, 4) || !aligned(new_tokens, 4) || !aligned(free_pages, 4) || !aligned(table, 4) || !aligned(kv_lens, 4) ||
         !aligned(starts, 4) || !aligned(used, 4) || !aligned(slots, 8))
         return fail(SDT_ERR_ALIGN, "paged_tables: pointers must be aligned to their elements");
+    // Every CTA reads the inputs at its own time, and CTA 0 writes sums before the others have read: no output
+    // may lie over an input or over another output.
+    const int64_t vec = 4 * batch;
+    const Buffer all[] = {{"lens", reinterpret_cast<const char *>(lens), 1, vec, vec},
+                          {"new_tokens", reinterpret_cast<const char *>(new_tokens), 1, vec, vec},
+                          {"free_pages", reinterpret_cast<const char *>(free_pages), 1, 4 * num_free, 4 * num_free},
+                          {"kv_lens", reinterpret_cast<const char *>(kv_lens), 1, vec, vec},
+                          {"starts", reinterpret_cast<const char *>(starts), 1, vec + 4, vec + 4},
+                          {"used", reinterpret_cast<const char *>(used), 1, 4, 4},
+                          {"slots", reinterpret_cast<const char *>(slots), 1, 8 * num_slots, 8 * num_slots},
+                          {"table", reinterpret_cast<const char *>(table), batch, 4 * max_pages, 4 * table_stride}};
+    constexpr int kInputs = 3, kBuffers = sizeof(all) / sizeof(all[0]);
+    for (int i = kInputs; i < kBuffers; ++i)
+        for (int j = 0; j < i; ++j)
+            if (lies_in(all[j], all[i]))
+                return fail(SDT_ERR_ARG, "paged_tables: %s and %s overlap", all[j].name, all[i].name);
     DeviceInfo dev;
     int rc = current_device(&dev);
     if (rc) return rc;

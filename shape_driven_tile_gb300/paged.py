@@ -144,7 +144,7 @@ def paged_tables(lens, new_tokens, free_pages, table, *, page_size: int, slots, 
     ``page * page_size + offset`` of the new tokens, request after request, then -1.
     Returns (kv_lens, starts, slots, used): int32 lens + new_tokens, int32 [batch + 1] prefix
     sums of new_tokens, and int32 [1], the pages taken; where that exceeds free_pages' length,
-    the entries and slots without a page are -1.
+    the entries and slots without a page are -1.  No output may overlap an input or another output.
     """
     try:
         batch, dev = len(lens), _current_device()
