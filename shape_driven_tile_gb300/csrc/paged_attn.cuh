@@ -43,7 +43,10 @@
 // a score passes it by kAttnSlack, so most units rescale nothing; weights are then at most
 // 2^kAttnSlack.  They enter the second product as the sum of two 16-bit values (the rounded
 // weight and the rounded rest): one rounding to 8 bits would cost as much accuracy as the
-// output's own, and the matrix unit has the time.
+// output's own, and the matrix unit has the time.  fp16 ends at 2^-24, where the tokens of a
+// long context beside one that outweighs them all would be rounded to few bits or to zero (131071
+// tokens 16.3 below: their sum 28 % short where one warp had them all).  The reference therefore stays
+// 2^kAttnLower below the largest score: weights reach 2^15 and keep 2^-32 of the largest one.
 #pragma once
 
 #include <type_traits>
@@ -53,7 +56,8 @@
 
 namespace sdt {
 
-constexpr float kAttnSlack = 8.f;  // log2 of the largest weight: far from fp16's 65504, and rarely passed
+constexpr float kAttnSlack = 8.f;  // log2 by which a score may pass the largest before it: rarely passed
+constexpr float kAttnLower = 7.f;  // log2 of an fp16 cache's weights at the largest score: with the slack 2^15 of fp16's 65504
 constexpr int kAttnSplitValues = 2048;  // least values of a piece's o that a second kernel joins
 constexpr int kAttnFlat = 256;     // most pieces x query heads that are joined in one level
 
@@ -257,6 +261,7 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
     // keys between two looks at the running maximum: 32, but 16 where the registers would not do
     constexpr int SUB = KS < 32 || (DP == 256 && NH == 2) ? 16 : 32;
     using PT = std::conditional_t<Q8, __half, T>;            // operand type of both products
+    constexpr float LOWER = !Q8 && std::is_same_v<T, __half> ? kAttnLower : 0.f;  // (q8: see v_exp)
     constexpr bool LOW = !Q8 || std::is_same_v<T, __half>;   // weights in two parts
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ float st_m[NW][C::HEADS], st_l[NW][C::HEADS];
@@ -848,9 +853,9 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
                     x[nt][0] = fmaxf(x[nt][0], fmaxf(s[i][nt][0], s[i][nt][2]));
                     x[nt][1] = fmaxf(x[nt][1], fmaxf(s[i][nt][1], s[i][nt][3]));
                 }
-                past = past || x[nt][0] > m[nt][0] + kAttnSlack || x[nt][1] > m[nt][1] + kAttnSlack;
+                past = past || x[nt][0] > m[nt][0] + (kAttnSlack + LOWER) || x[nt][1] > m[nt][1] + (kAttnSlack + LOWER);
             }
-            if (__any_sync(0xffffffffu, past)) {  // the reference moves to the largest score so far
+            if (__any_sync(0xffffffffu, past)) {  // the reference moves to LOWER below the largest score so far
 #pragma unroll
                 for (int nt = 0; nt < NH; ++nt) {
                     float a[2];
@@ -860,7 +865,7 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
                         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
                         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
                         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
-                        y = fmaxf(y, m[nt][i]);
+                        y = fmaxf(y - LOWER, m[nt][i]);
                         a[i] = y == m[nt][i] ? 1.f : pow2(m[nt][i] - y);
                         m[nt][i] = y;
                         l[nt][i] *= a[i];
