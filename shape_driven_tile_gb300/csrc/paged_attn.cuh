@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
     // keys between two looks at the running maximum: 32, but 16 where the registers would not do
     constexpr int SUB = KS < 32 || (DP == 256 && NH == 2) ? 16 : 32;
     using PT = std::conditional_t<Q8, __half, T>;            // operand type of both products
-    constexpr float LOWER = !Q8 && std::is_same_v<T, __half> ? kAttnLower : 0.f;  // (q8: see v_exp)
+    constexpr float LOWER = !Q8 && std::is_same_v<T, __half> ? kAttnLower : 0.f;  // (q8: see v_top)
     constexpr bool LOW = !Q8 || std::is_same_v<T, __half>;   // weights in two parts
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ float st_m[NW][C::HEADS], st_l[NW][C::HEADS];
@@ -491,7 +491,13 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
     float o[MT][NH][4];
     float m[NH][2], l[NH][2];  // running reference and this thread's part of the sum, heads 2c, 2c + 1
     float q_unit[NH][2];       // q8: what one unit of a head's staged query stands for
-    int v_exp = 0;             // q8: o holds sum w v 2^(30 - kAttnSlack - v_exp), every value scale so far < 2^(v_exp - 15)
+    // q8: the largest value scale so far of each group of 32 columns, its fp16 exponent field in place, two
+    // groups a word.  With e that field's number (scales < 2^(e - 14)) o holds sum w v 2^(21 - e), so that a
+    // weight (at most 2^kAttnSlack) times a scale stays below 2^15 and keeps 2^-31 of the group's largest.
+    uint32_t v_top[Q8 ? DP / 64 : 1];
+    static_assert(kAttnSlack + 7 == 15, "2^kAttnSlack 2^(e - 14) 2^(21 - e) must lie in fp16's range");
+    auto v_top_of = [&](int gr) { return gr & 1 ? v_top[gr >> 1] >> 16 : v_top[gr >> 1] & 0xffffu; };  // e << 10
+    auto v_up = [&](int gr) { return __uint_as_float(((127u + 21u) << 23) - (v_top_of(gr) << 13)); };     // 2^(21 - e)
     auto load_q = [&](int stage) {
 #pragma unroll
         for (int nt = 0; nt < NH; ++nt) {
@@ -543,7 +549,10 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
 #pragma unroll
             for (int t = 0; t < MT; ++t) o[t][nt][0] = o[t][nt][1] = o[t][nt][2] = o[t][nt][3] = 0.f;
         }
-        v_exp = 0;
+        if constexpr (Q8) {
+#pragma unroll
+            for (int x = 0; x < DP / 64; ++x) v_top[x] = 0;
+        }
     };
 
     // ---- prologue: S - 1 units in flight, the page ids of the next ----
@@ -923,36 +932,36 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
                 // this thread's keys in the values: 2c, 2c + 1 and 8 further on
                 const uint32_t v_row[2] = {vt + (k0 + 2 * c) * ROWB + ((g >> 2) ^ swizzle<DP, true>(2 * c)) * 16 + (g & 3) * 4,
                                            vt + (k0 + 2 * c + 1) * ROWB + ((g >> 2) ^ swizzle<DP, true>(2 * c + 1)) * 16 + (g & 3) * 4};
-                // the exponents of this block's value scales: o is kept so that weight times scale fits fp16
-                uint32_t xs[KT][2][DP / 64], top = 0;
+                // this block's value scales, and whether one has a larger exponent than its group's so far
+                uint32_t xs[KT][2][DP / 64], top[DP / 64];
+                bool grows = false;
 #pragma unroll
-                for (int i = 0; i < KT; ++i)
+                for (int x = 0; x < DP / 64; ++x) {
+                    top[x] = v_top[x];
 #pragma unroll
-                    for (int y = 0; y < 2; ++y)
+                    for (int i = 0; i < KT; ++i)
 #pragma unroll
-                        for (int x = 0; x < DP / 64; ++x) {
+                        for (int y = 0; y < 2; ++y) {
                             xs[i][y][x] = lds32(vst + (k0 + g) * C::SCB + (i * 16 + 8 * y) * C::SCB + x * 4);
-                            top = __vmaxu2(top, xs[i][y][x] & 0x7fff7fffu);
+                            top[x] = __vmaxu2(top[x], xs[i][y][x] & 0x7c007c00u);
                         }
-                int ex = static_cast<int>(max(top & 0xffffu, top >> 16) >> 10) + 1;  // scales < 2^(ex - 15)
-                if (__any_sync(0xffffffffu, ex > v_exp)) {
-                    ex = max(__reduce_max_sync(0xffffffffu, ex), v_exp);
-                    const float f = __uint_as_float(static_cast<uint32_t>(127 + v_exp - ex) << 23);
-                    v_exp = ex;
-#pragma unroll
-                    for (int t = 0; t < MT; ++t)
-#pragma unroll
-                        for (int nt = 0; nt < NH; ++nt)
-#pragma unroll
-                            for (int y = 0; y < 4; ++y) o[t][nt][y] *= f;
+                    grows = grows || top[x] != v_top[x];
                 }
-                const float up = __uint_as_float(static_cast<uint32_t>(127 + 30 - static_cast<int>(kAttnSlack) - v_exp) << 23);
+                if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
-                for (int i = 0; i < KT; ++i)
+                    for (int gr = 0; gr < DP / 32; ++gr) {
+                        const uint32_t was = v_top_of(gr), mine = gr & 1 ? top[gr >> 1] >> 16 : top[gr >> 1] & 0xffffu;
+                        const uint32_t now = __reduce_max_sync(0xffffffffu, mine);
+                        const float f = __uint_as_float((127u << 23) - ((now - was) << 13));
 #pragma unroll
-                    for (int nt = 0; nt < NH; ++nt)
+                        for (int t = 2 * gr; t < 2 * gr + 2; ++t)  // (a group's columns are two tiles of o)
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) s[i][nt][y] *= up;
+                            for (int nt = 0; nt < NH; ++nt)
+#pragma unroll
+                                for (int y = 0; y < 4; ++y) o[t][nt][y] *= f;
+                        v_top[gr >> 1] = gr & 1 ? (v_top[gr >> 1] & 0xffffu) | now << 16 : (v_top[gr >> 1] & 0xffff0000u) | now;
+                    }
+                }
 #pragma unroll
                 for (int i = 0; i < KT; ++i) {
 #pragma unroll
@@ -963,7 +972,7 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
                             w[t] = lds32((v_row[t & 1] ^ (gr << 5)) + (i * 16 + (t >> 1) * 8) * ROWB) ^ 0x80808080u;
                         }
                         const float2 y0 = unpack2<__half>(xs[i][0][gr >> 1]), y1 = unpack2<__half>(xs[i][1][gr >> 1]);
-                        const float f0 = gr & 1 ? y0.y : y0.x, f1 = gr & 1 ? y1.y : y1.x;
+                        const float f0 = (gr & 1 ? y0.y : y0.x) * v_up(gr), f1 = (gr & 1 ? y1.y : y1.x) * v_up(gr);
                         uint32_t hi[NH][2], lo[NH][2];
 #pragma unroll
                         for (int nt = 0; nt < NH; ++nt)
@@ -1000,7 +1009,6 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
 
         if (cw.key + TK >= cw.len || cw.at == places - 1) {
             // ---- the CTA's piece of the item: join the warps through the stage just read ----
-            const float back = Q8 ? __uint_as_float(static_cast<uint32_t>(127 - 30 + static_cast<int>(kAttnSlack) + v_exp) << 23) : 1.f;
 #pragma unroll
             for (int nt = 0; nt < NH; ++nt)
 #pragma unroll
@@ -1033,10 +1041,12 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
                         }
                     } else {
 #pragma unroll
-                        for (int gr = 0; gr < DP / 32; ++gr)
+                        for (int gr = 0; gr < DP / 32; ++gr) {
+                            const float back = __uint_as_float(((127u - 21u) << 23) + (v_top_of(gr) << 13));  // 2^(e - 21)
                             *reinterpret_cast<float4 *>(row + ((gr * 32 + g * 4) ^ sw)) =
                                 make_float4(o[2 * gr][nt][i] * back, o[2 * gr][nt][2 + i] * back, o[2 * gr + 1][nt][i] * back,
                                             o[2 * gr + 1][nt][2 + i] * back);
+                        }
                     }
                 }
             cta_sync();
