@@ -205,6 +205,14 @@ __device__ __forceinline__ float reciprocal(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// Lengths and page ids come from the kernel before this one in the stream, which may still run when this one
+// starts: an ordinary load, volatile so that it stays behind the wait (not __ldg, whose data nobody may
+// write while the kernel lives).
+__device__ __forceinline__ int load_int(const int *p) {
+    int v;
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t v;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
@@ -292,7 +300,7 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
     // ---- this CTA's share ----
     const int cap = p.max_pages * static_cast<int>(p.page.d);  // < 2^31: checked on the host
     auto range_of = [&](int b, int &lo, int &len) {
-        const int n = __ldg(p.lens + b);
+        const int n = load_int(p.lens + b);
         len = min(max(n, 0), cap);
         lo = p.window > 0 && len > p.window ? len - p.window : 0;
         return n > cap;
@@ -402,7 +410,7 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
         if (pg_ok) {
             const int pi = static_cast<int>(p.page.div(key));
             pg_off = key - pi * static_cast<int>(p.page.d);
-            pg_id = __ldg(pw_pages + pi);
+            pg_id = load_int(pw_pages + pi);
         }
     };
     const int pieces = p.head_dim * (Q8 ? 1 : 2) / 16;  // 16-byte pieces of a row that exist
