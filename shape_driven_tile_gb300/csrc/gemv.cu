@@ -54,6 +54,14 @@ __device__ __forceinline__ uint4 ld_stream_v4(const uint4 *p) {
     return v;
 }
 
+// 16 bytes of activations, kept in program order with the weight loads around it.  The kernel before this one
+// in the stream writes them, and may still run when this one starts: an ordinary load, not one for data that
+// nobody may write while the kernel lives.
+__device__ __forceinline__ uint4 ld_x_v4(const uint4 *p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -136,7 +144,7 @@ __global__ void __launch_bounds__(kGemvThreads)
                 for (int r = 0; r < ROWS; ++r)
                     w[r][u] = (in && n0 + r < N) ? ld_stream_v4(W + size_t(n0 + r) * K8 + c)
                                                  : make_uint4(0, 0, 0, 0);
-                xv[u] = in ? __ldg(x + c) : make_uint4(0, 0, 0, 0);
+                xv[u] = in ? ld_x_v4(x + c) : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -187,8 +195,8 @@ __global__ void __launch_bounds__(kGemvThreads)
             for (int u = 0; u < U; ++u) {
                 const int c = c0 + 32 * u;
                 const bool in = c < K16;
-                const uint4 xa = in ? __ldg(x + 2 * c) : make_uint4(0, 0, 0, 0);
-                const uint4 xb = in ? __ldg(x + 2 * c + 1) : make_uint4(0, 0, 0, 0);
+                const uint4 xa = in ? ld_x_v4(x + 2 * c) : make_uint4(0, 0, 0, 0);
+                const uint4 xb = in ? ld_x_v4(x + 2 * c + 1) : make_uint4(0, 0, 0, 0);
                 // the chunk's 16 activations as 8 packed fp32 pairs, shared by the ROWS rows
                 const uint64_t x0 = bf16x2_to_f32x2(xa.x), x1 = bf16x2_to_f32x2(xa.y);
                 const uint64_t x2 = bf16x2_to_f32x2(xa.z), x3 = bf16x2_to_f32x2(xa.w);
@@ -323,7 +331,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) gemv_stream_kernel(const St
         // already streaming).  x word i holds elements 8i .. 8i+7: chunk 8i / E, pairs from
         // (8i % E) / 2, with E = 16 (q8) or 8 (bf16) elements per chunk.
         for (int i = threadIdx.x; i < (a.K >> 3); i += kStreamConsumers * 32) {
-            const uint4 v = __ldg(a.x + i);
+            const uint4 v = ld_x_v4(a.x + i);
             const int c = Q8 ? (i >> 1) : i;
             const int p0 = Q8 ? (i & 1) * 4 : 0;
             xs2[(p0 + 0) * nchunk + c] = make_uint2(v.x << 16, v.x & 0xFFFF0000u);
@@ -450,13 +458,6 @@ __global__ void __launch_bounds__(kStreamThreads, 1) gemv_stream_kernel(const St
 // has room), and the kernel's own weight loads are marked evict-first in L2 so
 // that its stream does not push those prefetched lines out.
 constexpr int kDpMaxThreads = 256;
-
-// Read-only 16-byte load kept in program order with the weight loads around it.
-__device__ __forceinline__ uint4 ld_nc_v4(const uint4 *p) {
-    uint4 v;
-    asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
-}
 
 __device__ __forceinline__ void ld_stream_v8(const uint8_t *p, uint32_t (&w)[8]) {
     asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -646,7 +647,7 @@ __global__ void __launch_bounds__(kDpMaxThreads, MINB)
     for (int i = 0; i < GT; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint4 v = g[i] < G ? ld_nc_v4(x + size_t(g[i]) * 4 + j) : make_uint4(0, 0, 0, 0);
+            const uint4 v = g[i] < G ? ld_x_v4(x + size_t(g[i]) * 4 + j) : make_uint4(0, 0, 0, 0);
             xw[i][4 * j] = v.x;
             xw[i][4 * j + 1] = v.y;
             xw[i][4 * j + 2] = v.z;
@@ -791,8 +792,8 @@ __global__ void __launch_bounds__(kDpMaxThreads, MINB)
     uint32_t xw[GT][8];
 #pragma unroll
     for (int i = 0; i < GT; ++i) {
-        const uint4 v0 = u[i] < U ? ld_nc_v4(x + size_t(u[i]) * 2) : make_uint4(0, 0, 0, 0);
-        const uint4 v1 = u[i] < U ? ld_nc_v4(x + size_t(u[i]) * 2 + 1) : make_uint4(0, 0, 0, 0);
+        const uint4 v0 = u[i] < U ? ld_x_v4(x + size_t(u[i]) * 2) : make_uint4(0, 0, 0, 0);
+        const uint4 v1 = u[i] < U ? ld_x_v4(x + size_t(u[i]) * 2 + 1) : make_uint4(0, 0, 0, 0);
         xw[i][0] = v0.x; xw[i][1] = v0.y; xw[i][2] = v0.z; xw[i][3] = v0.w;
         xw[i][4] = v1.x; xw[i][5] = v1.y; xw[i][6] = v1.z; xw[i][7] = v1.w;
     }
@@ -1006,7 +1007,7 @@ __global__ void __launch_bounds__((NCW + 1) * 32, 1) gemv_ring_kernel(const Ring
         for (int i = 0; i < GT; ++i)
 #pragma unroll
             for (int j = 0; j < (Q8 ? 4 : 2); ++j) {
-                const uint4 v = g[i] < G ? ld_nc_v4(a.x + size_t(g[i]) * (Q8 ? 4 : 2) + j) : make_uint4(0, 0, 0, 0);
+                const uint4 v = g[i] < G ? ld_x_v4(a.x + size_t(g[i]) * (Q8 ? 4 : 2) + j) : make_uint4(0, 0, 0, 0);
                 xw[i][4 * j] = v.x;
                 xw[i][4 * j + 1] = v.y;
                 xw[i][4 * j + 2] = v.z;
