@@ -526,9 +526,10 @@ int paged_append(int64_t tokens, const void *k, int64_t k_token, int64_t k_head,
  * 8 and 16-byte aligned, out multiples of 4 and 8-byte aligned).  lse, if not NULL, gets
  * log(sum exp(scores)) as fp32 [batch][q_heads].  A request without keys, or whose scores
  * are all -inf, gets zeros and lse -inf.  What lies in the cache outside the named tokens
- * is not read.  A page id outside the cache, or a length past max_pages * page_size, is not
- * followed and is reported by sdt_check_device_status.  Results do not depend on the order
- * in which the CTAs run.
+ * is not read.  A page id outside the cache is not followed and reported by
+ * sdt_check_device_status; the request's out and lse are NaN.  A length past max_pages *
+ * page_size is reported and taken as that.  Results do not depend on the order in which the
+ * CTAs run.
  *
  * Workspace: device memory owned by the caller, 256-byte aligned, at least
  * sdt_paged_attn_workspace_bytes() bytes: the 1 MiB counter region of the split-K

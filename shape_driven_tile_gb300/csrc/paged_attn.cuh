@@ -416,9 +416,10 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
     const int pieces = p.head_dim * (Q8 ? 1 : 2) / 16;  // 16-byte pieces of a row that exist
     bool first_unit_of_cta = true;
     auto issue = [&](int stage) {
-        if (pg_ok && (pg_id < 0 || pg_id >= p.num_pages)) {
+        const uint32_t lost = __ballot_sync(0xffffffffu, pg_ok && static_cast<uint32_t>(pg_id) >= static_cast<uint32_t>(p.num_pages));
+        if (__builtin_expect(lost != 0, 0)) {
             paged_status(p.status, kSitePage);
-            pg_ok = false;
+            if (lost >> lane & 1) pg_ok = false;
         }
         constexpr int CPR = ROWB / 16, RPI = 32 / CPR;  // pieces per row, rows per instruction
         const int cc = lane % CPR, rr = lane / CPR;
@@ -474,6 +475,14 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
                     }
                 }
             }
+        }
+        if (__builtin_expect(lost != 0, 0)) {
+            // a key of a page that does not exist scores NaN, and so does its request: zeros would be a key that
+            // looks like any other.  (After the zeros that were copied to its row.)
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
+            const uint32_t row = smem0 + stage * C::STAGE + (Q8 ? 2 * TK * ROWB + (warp * RW + lane) * C::SCB : (warp * RW + lane) * ROWB);
+            if (lost >> lane & 1) asm volatile("st.shared.b32 [%0], %1;" ::"r"(row), "r"(0x7fff7fffu) : "memory");  // (NaN in fp16 and bf16)
         }
         if (pw.key == pw.lo || first_unit_of_cta) {  // the item's queries
             first_unit_of_cta = false;
