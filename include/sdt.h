@@ -492,8 +492,8 @@ typedef struct sdt_paged_cache {
  * no slot.  The same call on the same inputs writes the same values.
  * Negative lengths count as 0, lengths past max_pages * page_size as that; the sum of
  * new_tokens must be below 2^31.
- * No output may overlap an input or another output (SDT_ERR_ARG): lengths are not updated
- * in place.
+ * No output may overlap an input or another output (SDT_ERR_ARG): lengths are updated in
+ * place by paged_tables_taken only.
  */
 typedef struct sdt_paged_step {
     const int32_t *lens, *new_tokens, *free_pages;
@@ -502,6 +502,16 @@ typedef struct sdt_paged_step {
     int64_t batch, page_size, max_pages, table_stride, num_free, num_slots;
 } sdt_paged_step;
 int paged_tables(const sdt_paged_step *step, sdt_stream_t stream);
+
+/*
+ * paged_tables_taken -- paged_tables for a step that is captured once and replayed: the place
+ * in the free list is on the device.  taken: int32 [2], zeros before the first call; taken[0]
+ * is the number of entries of free_pages that earlier calls have used.  The call takes its
+ * pages from there on (num_free counts the whole list) and adds how many it took, at most up
+ * to num_free; taken[1] is zero between calls.  kv_lens may be lens itself here.  Calls that
+ * share `taken` must not overlap on the GPU.
+ */
+int paged_tables_taken(const sdt_paged_step *step, int32_t *taken, sdt_stream_t stream);
 
 /*
  * paged_append -- the keys and values of `tokens` tokens into the cache at their slots

@@ -83,6 +83,7 @@ SIGNATURES = {
     "sdt_pair_tail_plan": (cint, [i64, i64, i64, cint, cint, cint, cint, cint, ctypes.POINTER(cint),
                                   ctypes.POINTER(cint), ctypes.POINTER(cint), ctypes.POINTER(cint)]),
     "paged_tables": (cint, [vp, vp]),  # a packed sdt_paged_step
+    "paged_tables_taken": (cint, [vp, vp, vp]),
     "paged_append": (cint, [i64, vp, i64, i64, vp, i64, i64, cint, vp, ctypes.POINTER(sdt_paged_cache), vp]),
     "paged_attn_m1": (cint, [vp, vp]),  # a packed sdt_paged_attn
     "sdt_paged_attn_workspace_bytes": (ctypes.c_size_t, [i64, i64, i64]),

@@ -14,6 +14,12 @@
 // another launch or CTA, keeps them in shared memory and finds the request of a token or of
 // a fresh page by bisection.  A slot on a fresh page takes its page from `free`, not from
 // the table entry that another CTA may be writing.
+//
+// With `taken` the place in the free list lives on the device and moves with each call, and the
+// lengths may be updated in place, so that a captured step can be replayed by itself.  What
+// every CTA still reads may then change only when all have read it: the last CTA to arrive
+// (a counter beside the place, zero between calls) writes both: 3.9 us for 256 requests, 8.8
+// for 1021 with 67 new tokens each (2.9 and 6.8 without).
 #include <atomic>
 
 #include "launch.cuh"
@@ -35,6 +41,7 @@ struct TablesArgs {
     int64_t num_slots;
     int batch, max_pages, num_free;
     FastDiv page;
+    int *taken;  // null, or [2]: entries of free_pages used by earlier calls, CTAs that have arrived
 };
 
 // Index of the last of `n` non-decreasing prefix sums that is <= x (sums[0] = 0, x >= 0).
@@ -48,6 +55,7 @@ __device__ __forceinline__ int bisect(const int *sums, int n, int x) {
     return lo;
 }
 
+template <bool TAKEN>
 __global__ void __launch_bounds__(kTablesThreads) paged_tables_kernel(const TablesArgs a) {
     extern __shared__ int sums[];  // [batch] first token, [batch] first fresh page of each request
     int *tok = sums, *pg = sums + a.batch;
@@ -56,8 +64,11 @@ __global__ void __launch_bounds__(kTablesThreads) paged_tables_kernel(const Tabl
     griddep_launch_dependents();
     griddep_wait();
 
+    const int base = TAKEN ? min(max(a.taken[0], 0), a.num_free) : 0;  // of the free list
+    const int num_free = a.num_free - base;
     const int capacity = a.max_pages * static_cast<int>(a.page.d);  // tokens of a table row (< 2^31: checked on the host)
     auto length_of = [&](int b) { return min(max(a.lens[b], 0), capacity); };
+    auto added = [&](int b, int len) { return min(max(a.fresh_tokens[b], 0), INT32_MAX - len); };
     auto held_of = [&](int len) {
         return min(static_cast<int>(a.page.div(static_cast<uint32_t>(len) + a.page.d - 1u)), a.max_pages);
     };
@@ -66,12 +77,12 @@ __global__ void __launch_bounds__(kTablesThreads) paged_tables_kernel(const Tabl
     const int b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
     int my_tok = 0, my_pg = 0;
     for (int b = b0; b < b1; ++b) {
-        const int len = length_of(b), add = min(max(a.fresh_tokens[b], 0), INT32_MAX - len);
+        const int len = length_of(b), add = added(b, len);
         tok[b] = my_tok;
         pg[b] = my_pg;
         my_tok += add;
         my_pg += held_of(len + add) - held_of(len);
-        if (blockIdx.x == 0) a.kv_lens[b] = len + add;
+        if (!TAKEN && blockIdx.x == 0) a.kv_lens[b] = len + add;
     }
     int inc_tok = my_tok, inc_pg = my_pg;
 #pragma unroll
@@ -114,7 +125,7 @@ __global__ void __launch_bounds__(kTablesThreads) paged_tables_kernel(const Tabl
         const int b = bisect(pg, a.batch, static_cast<int>(i));
         const int j = held_of(length_of(b)) + static_cast<int>(i) - pg[b];
         if (j >= 0 && j < a.max_pages)
-            a.table[b * a.table_stride + j] = i < a.num_free ? a.free_pages[i] : -1;
+            a.table[b * a.table_stride + j] = i < num_free ? a.free_pages[base + i] : -1;
     }
     for (int64_t i = first; i < a.num_slots; i += step) {
         int64_t slot = -1;
@@ -127,11 +138,27 @@ __global__ void __launch_bounds__(kTablesThreads) paged_tables_kernel(const Tabl
             if (p < a.max_pages) {
                 const int64_t f = static_cast<int64_t>(pg[b]) + p - held;
                 if (p < held) id = a.table[b * a.table_stride + p];
-                else if (f >= 0 && f < a.num_free) id = a.free_pages[f];
+                else if (f >= 0 && f < num_free) id = a.free_pages[base + f];
             }
             if (id >= 0) slot = static_cast<int64_t>(id) * a.page.d + (pos - static_cast<uint32_t>(p) * a.page.d);
         }
         a.slots[i] = slot;
+    }
+    if constexpr (TAKEN) {
+        __shared__ int last;
+        __syncthreads();  // this CTA has read everything
+        if (tid == 0) {
+            unsigned was;  // (wraps to 0 at the last CTA)
+            asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(was) : "l"(a.taken + 1), "r"(gridDim.x - 1) : "memory");
+            last = was == gridDim.x - 1;
+        }
+        __syncthreads();
+        if (!last) return;
+        for (int b = tid; b < a.batch; b += kTablesThreads) {
+            const int len = length_of(b);
+            a.kv_lens[b] = len + added(b, len);
+        }
+        if (tid == 0) a.taken[0] = base + min(all_pg, num_free);
     }
 }
 
@@ -154,7 +181,7 @@ static bool lies_in(const Buffer &x, const Buffer &y) {
 
 using namespace sdt;
 
-extern "C" int paged_tables(const sdt_paged_step *step, sdt_stream_t stream) {
+static int tables(const sdt_paged_step *step, int32_t *taken, sdt_stream_t stream) {
     clear_error();
     if (!step) return fail(SDT_ERR_NULL, "paged_tables: NULL arguments");
     const auto &[lens, new_tokens, free_pages, table, kv_lens, starts, used, slots, batch, page_size, max_pages, table_stride,
@@ -169,10 +196,10 @@ extern "C" int paged_tables(const sdt_paged_step *step, sdt_stream_t stream) {
         (num_slots && !slots))
         return fail(SDT_ERR_NULL, "paged_tables: NULL pointer");
     if (!aligned(lens, 4) || !aligned(new_tokens, 4) || !aligned(free_pages, 4) || !aligned(table, 4) || !aligned(kv_lens, 4) ||
-        !aligned(starts, 4) || !aligned(used, 4) || !aligned(slots, 8))
+        !aligned(starts, 4) || !aligned(used, 4) || !aligned(slots, 8) || !aligned(taken, 4))
         return fail(SDT_ERR_ALIGN, "paged_tables: pointers must be aligned to their elements");
     // Every CTA reads the inputs at its own time, and CTA 0 writes sums before the others have read: no output
-    // may lie over an input or over another output.
+    // may lie over an input or over another output.  Only with `taken` kv_lens waits for all CTAs.
     const int64_t vec = 4 * batch;
     const Buffer all[] = {{"lens", reinterpret_cast<const char *>(lens), 1, vec, vec},
                           {"new_tokens", reinterpret_cast<const char *>(new_tokens), 1, vec, vec},
@@ -181,32 +208,43 @@ extern "C" int paged_tables(const sdt_paged_step *step, sdt_stream_t stream) {
                           {"starts", reinterpret_cast<const char *>(starts), 1, vec + 4, vec + 4},
                           {"used", reinterpret_cast<const char *>(used), 1, 4, 4},
                           {"slots", reinterpret_cast<const char *>(slots), 1, 8 * num_slots, 8 * num_slots},
+                          {"taken", reinterpret_cast<const char *>(taken), 1, taken ? 8 : 0, 8},
                           {"table", reinterpret_cast<const char *>(table), batch, 4 * max_pages, 4 * table_stride}};
-    constexpr int kInputs = 3, kBuffers = sizeof(all) / sizeof(all[0]);
+    constexpr int kLens = 0, kInputs = 3, kKvLens = 3, kBuffers = sizeof(all) / sizeof(all[0]);
     for (int i = kInputs; i < kBuffers; ++i)
         for (int j = 0; j < i; ++j)
-            if (lies_in(all[j], all[i]))
+            if (lies_in(all[j], all[i]) && !(taken && j == kLens && i == kKvLens && kv_lens == lens))
                 return fail(SDT_ERR_ARG, "paged_tables: %s and %s overlap", all[j].name, all[i].name);
     DeviceInfo dev;
     int rc = current_device(&dev);
     if (rc) return rc;
     TablesArgs a{lens, new_tokens, free_pages, table, table_stride, kv_lens, starts, used, slots, num_slots,
                  static_cast<int>(batch), static_cast<int>(max_pages), static_cast<int>(num_free),
-                 FastDiv::of(static_cast<uint32_t>(page_size))};
+                 FastDiv::of(static_cast<uint32_t>(page_size)), taken};
     const size_t smem = 2 * sizeof(int) * static_cast<size_t>(batch);
-    static std::atomic<bool> ready[kMaxDevices];  // the attribute call takes longer than the launch: once a device
+    auto kern = taken ? paged_tables_kernel<true> : paged_tables_kernel<false>;
+    static std::atomic<bool> ready[kMaxDevices][2];  // the attribute call takes longer than the launch: once a device
     cudaError_t e = cudaSuccess;
-    if (!ready[dev.device].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(paged_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 2 * static_cast<int>(sizeof(int)) * kTablesMaxBatch);
-        if (e == cudaSuccess) ready[dev.device].store(true, std::memory_order_release);
+    if (!ready[dev.device][taken != nullptr].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * static_cast<int>(sizeof(int)) * kTablesMaxBatch);
+        if (e == cudaSuccess) ready[dev.device][taken != nullptr].store(true, std::memory_order_release);
     }
     if (e == cudaSuccess) {
         const int64_t want = (num_slots + kTablesThreads * kTablesPerThread - 1) / (kTablesThreads * kTablesPerThread);
         const int64_t grid = want < 1 ? 1 : want > dev.sm_count ? dev.sm_count : want;
-        e = launch_kernel(paged_tables_kernel, dim3(static_cast<unsigned>(grid)), dim3(kTablesThreads), smem,
+        e = launch_kernel(kern, dim3(static_cast<unsigned>(grid)), dim3(kTablesThreads), smem,
                           reinterpret_cast<cudaStream_t>(stream), 1, a);
     }
     if (e != cudaSuccess) return fail(SDT_ERR_LAUNCH, "paged_tables launch failed: %s", cudaGetErrorString(e));
     return SDT_OK;
+}
+
+extern "C" int paged_tables(const sdt_paged_step *step, sdt_stream_t stream) { return tables(step, nullptr, stream); }
+
+extern "C" int paged_tables_taken(const sdt_paged_step *step, int32_t *taken, sdt_stream_t stream) {
+    if (!taken) {
+        clear_error();
+        return fail(SDT_ERR_NULL, "paged_tables_taken: NULL pointer");
+    }
+    return tables(step, taken, stream);
 }

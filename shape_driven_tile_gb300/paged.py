@@ -135,7 +135,7 @@ class PagedCache:
 
 
 def paged_tables(lens, new_tokens, free_pages, table, *, page_size: int, slots, kv_lens=None, starts=None, used=None,
-                 stream=None):
+                 taken=None, stream=None):
     """Block tables and slot maps of a step, built on the GPU from the requests' lengths.
 
     lens, new_tokens: int32 [batch], the tokens each request holds and adds.  free_pages: int32,
@@ -145,6 +145,9 @@ def paged_tables(lens, new_tokens, free_pages, table, *, page_size: int, slots, 
     Returns (kv_lens, starts, slots, used): int32 lens + new_tokens, int32 [batch + 1] prefix
     sums of new_tokens, and int32 [1], the pages taken; where that exceeds free_pages' length,
     the entries and slots without a page are -1.  No output may overlap an input or another output.
+    taken: int32 [2], zeros at first, for a step that is captured and replayed: taken[0] entries of
+    free_pages have been used by earlier calls, the call takes its pages from there on and moves it;
+    taken[1] belongs to the kernel.  With it kv_lens may be lens, which is then updated in place.
     """
     try:
         batch, dev = len(lens), _current_device()
@@ -179,11 +182,15 @@ def paged_tables(lens, new_tokens, free_pages, table, *, page_size: int, slots, 
         used = torch.empty(1, dtype=_I32, device=lens.device)
     else:
         _need_vector(used, "used", _I32, 1)
-    check(_fn("paged_tables")(
-        _STEP.pack(lens.data_ptr(), new_tokens.data_ptr(), free_pages.data_ptr(), table.data_ptr(), kv_lens.data_ptr(),
-                   starts.data_ptr(), used.data_ptr(), slots.data_ptr(), batch, page_size, wide,
-                   step if batch > 1 else wide, len(free_pages), len(slots)),
-        _current_stream(dev) if stream is None else _handle(stream)))
+    call = _STEP.pack(lens.data_ptr(), new_tokens.data_ptr(), free_pages.data_ptr(), table.data_ptr(), kv_lens.data_ptr(),
+                      starts.data_ptr(), used.data_ptr(), slots.data_ptr(), batch, page_size, wide,
+                      step if batch > 1 else wide, len(free_pages), len(slots))
+    on = _current_stream(dev) if stream is None else _handle(stream)
+    if taken is None:
+        check(_fn("paged_tables")(call, on))
+    else:
+        _need_vector(taken, "taken", _I32, 2)
+        check(_fn("paged_tables_taken")(call, taken.data_ptr(), on))
     return kv_lens, starts, slots, used
 
 

@@ -58,3 +58,30 @@ def test_overlap_with_a_wide_table_counts_its_rows_only():
         for off, over in ((-4, True), (4, True)):
             rc, why = call({**where, "lens": gap + off}, stride=PAGES + BATCH)
             assert (rc == ARG and "overlap" in why) is over
+
+
+TAKEN_AT = 0x40000
+
+
+def call_taken(where, taken):
+    rc = sdt.lib().paged_tables_taken(paged._STEP.pack(*(where[n] for n in SIZES), BATCH, 16, PAGES, PAGES, FREE, SLOTS), taken, None)
+    return rc, sdt.lib().sdt_last_error().decode()
+
+
+def test_the_place_overlaps_nothing():
+    for name, size in SIZES.items():
+        for shift in (0, size - 4, -4):
+            rc, why = call_taken(place(), place()[name] + shift)
+            assert rc == ARG and "overlap" in why
+    assert call_taken(place(), None)[0] == -1 and call_taken(place(), TAKEN_AT + 2)[0] == -2
+
+
+def test_lengths_in_place_with_a_place_in_the_list_are_exactly_the_same_buffer():
+    where = place()
+    where["kv_lens"] = where["lens"] + 4
+    rc, why = call_taken(where, TAKEN_AT)
+    assert rc == ARG and "overlap" in why
+    where["kv_lens"] = where["lens"]
+    where["starts"] = where["lens"]  # the other outputs still may not
+    rc, why = call_taken(where, TAKEN_AT)
+    assert rc == ARG and "overlap" in why
