@@ -191,7 +191,7 @@ extern "C" int paged_append(int64_t tokens, const void *k, int64_t k_token, int6
     const bool q8 = cache->dtype == SDT_DTYPE_Q8;
     if (!q8 && cache->dtype != dtype) return fail(SDT_ERR_ARG, "paged_append: a 16-bit cache takes values of its own type");
     const int64_t per_head = cache->head_dim / 8, per_token = per_head * cache->kv_heads;
-    if (tokens < 0 || tokens * per_token > INT32_MAX - kAppendThreads * kAppendUnroll)
+    if (tokens < 0 || tokens > (INT32_MAX - kAppendThreads * kAppendUnroll) / per_token)
         return fail(SDT_ERR_SHAPE, "paged_append: tokens * kv_heads * head_dim must be in 0 .. 2^34 (got %lld tokens)", (long long)tokens);
     if (tokens == 0) return SDT_OK;
     if (!k || !v || !slots) return fail(SDT_ERR_NULL, "paged_append: NULL pointer");
