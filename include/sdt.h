@@ -517,8 +517,9 @@ int paged_tables_taken(const sdt_paged_step *step, int32_t *taken, sdt_stream_t 
  * paged_append -- the keys and values of `tokens` tokens into the cache at their slots
  * (slot = page * page_size + offset).  k and v: fp16 or bf16 (dtype; a 16-bit cache's own
  * type), head h of token t at t * k_token + h * k_head elements, head_dim contiguous;
- * bases 16-byte aligned, strides multiples of 8.  A negative slot's token is left out.  A
- * slot past the cache is left out too and reported by sdt_check_device_status.  Of two
+ * bases 16-byte aligned, strides multiples of 8 (of a single token or head: anything).  A
+ * negative slot's token is left out; a slot past the cache is left out too and reported by
+ * sdt_check_device_status.  Of two
  * tokens with one slot either may stay.  q8: scale = fp16(max|x| * fl32(1/127)), at most
  * 65504, q = x / scale rounded to the nearest integer (ties to even) within +-127, 0 where
  * the scale is 0 or x is NaN.

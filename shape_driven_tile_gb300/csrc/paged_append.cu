@@ -194,6 +194,8 @@ extern "C" int paged_append(int64_t tokens, const void *k, int64_t k_token, int6
     if (tokens < 0 || tokens > (INT32_MAX - kAppendThreads * kAppendUnroll) / per_token)
         return fail(SDT_ERR_SHAPE, "paged_append: tokens * kv_heads * head_dim must be in 0 .. 2^34 (got %lld tokens)", (long long)tokens);
     if (tokens == 0) return SDT_OK;
+    if (tokens == 1) k_token = v_token = 0;  // a dimension of one never steps: its stride may be anything
+    if (cache->kv_heads == 1) k_head = v_head = 0;
     if (!k || !v || !slots) return fail(SDT_ERR_NULL, "paged_append: NULL pointer");
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8))
         return fail(SDT_ERR_ALIGN, "paged_append: k and v must be 16-byte aligned, slots 8-byte");
