@@ -519,9 +519,11 @@ int paged_tables_taken(const sdt_paged_step *step, int32_t *taken, sdt_stream_t 
  * type), head h of token t at t * k_token + h * k_head elements, head_dim contiguous;
  * bases 16-byte aligned, strides multiples of 8 (of a single token or head: anything).  A
  * negative slot's token is left out; a slot past the cache is left out too and reported by
- * sdt_check_device_status.  Of two
- * tokens with one slot either may stay.  q8: scale = fp16(max|x| * fl32(1/127)), at most
- * 65504, q = x / scale rounded to the nearest integer (ties to even) within +-127, 0 where
+ * sdt_check_device_status.  Slots that
+ * are not negative must differ: tokens with one slot may leave a row mixed from both, in q8
+ * under the scale of either.  k and v must not lie at slots that the call writes.  q8: scale
+ * = fp16(max|x| * fl32(1/127)), at most 65504, q = x / scale rounded to the nearest integer
+ * (ties to even) within +-127, 0 where
  * the scale is 0 or x is NaN.
  */
 int paged_append(int64_t tokens, const void *k, int64_t k_token, int64_t k_head, const void *v, int64_t v_token,

@@ -197,7 +197,8 @@ def paged_tables(lens, new_tokens, free_pages, table, *, page_size: int, slots, 
 def paged_append(k, v, slots, cache: PagedCache, *, stream=None) -> PagedCache:
     """Writes k and v [tokens, kv_heads, head_dim] (float16 or bfloat16; a 16-bit cache's own
     type) into the cache at slots (int64 [tokens], page * page_size + offset; negative: left
-    out), as q8 if the cache is.  k and v may be slices of wider rows."""
+    out), as q8 if the cache is.  k and v may be slices of wider rows.  Slots that are not
+    negative must differ: tokens with one slot may leave a row mixed from both."""
     try:
         dev, dtype, tokens = cache.device_index, k.dtype, len(k)
         want = (tokens, cache.kv_heads, cache.head_dim)
