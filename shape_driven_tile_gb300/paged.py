@@ -12,6 +12,7 @@ import struct
 
 import torch
 
+from . import _streams
 from ._lib import SdtError, check, lib, sdt_paged_cache
 
 GROUP = 32  # values per fp16 scale of a q8 cache
@@ -36,10 +37,6 @@ def _fn(name):
     if f is None:
         f = _functions[name] = getattr(lib(), name)
     return f
-
-
-def _handle(stream):
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def _need(t, name, dtype, ndim):
@@ -171,21 +168,21 @@ def paged_tables(lens, new_tokens, free_pages, table, *, page_size: int, slots, 
         _need_table(table, batch)
         _need_vector(slots, "slots", _I64)
     if kv_lens is None:
-        kv_lens = torch.empty_like(lens)
+        kv_lens = torch.empty_like(lens) if stream is None else _streams.empty(batch, _I32, lens.device, stream)
     else:
         _need_vector(kv_lens, "kv_lens", _I32, batch)
     if starts is None:
-        starts = torch.empty(batch + 1, dtype=_I32, device=lens.device)
+        starts = _streams.empty(batch + 1, _I32, lens.device, stream)
     else:
         _need_vector(starts, "starts", _I32, batch + 1)
     if used is None:
-        used = torch.empty(1, dtype=_I32, device=lens.device)
+        used = _streams.empty(1, _I32, lens.device, stream)
     else:
         _need_vector(used, "used", _I32, 1)
     call = _STEP.pack(lens.data_ptr(), new_tokens.data_ptr(), free_pages.data_ptr(), table.data_ptr(), kv_lens.data_ptr(),
                       starts.data_ptr(), used.data_ptr(), slots.data_ptr(), batch, page_size, wide,
                       step if batch > 1 else wide, len(free_pages), len(slots))
-    on = _current_stream(dev) if stream is None else _handle(stream)
+    on = _current_stream(dev) if stream is None else _streams.handle(stream)
     if taken is None:
         check(_fn("paged_tables")(call, on))
     else:
@@ -218,7 +215,7 @@ def paged_append(k, v, slots, cache: PagedCache, *, stream=None) -> PagedCache:
             raise TypeError("k and v must have one type")
         _need_vector(slots, "slots", _I64, len(k))
     check(_fn("paged_append")(tokens, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, DTYPE_CODES[dtype], slots.data_ptr(),
-                              cache._ref, _current_stream(dev) if stream is None else _handle(stream)))
+                              cache._ref, _current_stream(dev) if stream is None else _streams.handle(stream)))
     return cache
 
 
@@ -266,7 +263,7 @@ def paged_attn_m1(q, cache: PagedCache, table, lens, out=None, *, workspace, sca
         _need_vector(lens, "lens", _I32, len(q))
         _need_vector(workspace, "workspace", torch.uint8)
     if out is None:
-        out = torch.empty_like(q) if q.is_contiguous() else torch.empty(q.shape, dtype=dtype, device=q.device)
+        out = torch.empty_like(q) if stream is None and q.is_contiguous() else _streams.empty(q.shape, dtype, q.device, stream)
         ob, oh = q_heads * head_dim, head_dim
     else:
         _need(out, "out", dtype, 3)
@@ -283,5 +280,5 @@ def paged_attn_m1(q, cache: PagedCache, table, lens, out=None, *, workspace, sca
                    cache._address, workspace.data_ptr(), batch, q_heads, qb if batch > 1 else 0, qh if q_heads > 1 else 0,
                    ob if batch > 1 else 0, oh if q_heads > 1 else 0, step if batch > 1 else wide, wide, window,
                    len(workspace), head_dim ** -0.5 if scale is None else scale, DTYPE_CODES[dtype]),
-        _current_stream(dev) if stream is None else _handle(stream)))
+        _current_stream(dev) if stream is None else _streams.handle(stream)))
     return out
