@@ -11,6 +11,7 @@ import ctypes
 
 import torch
 
+from . import _streams
 from ._lib import SdtError, check, lib, sdt_tile_desc
 from .paged import PagedCache, paged_append, paged_attn_m1, paged_attn_workspace, paged_tables
 
@@ -30,9 +31,7 @@ __all__ = [
 def _stream(stream):
     if stream is None:
         return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-    if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+    return ctypes.c_void_p(_streams.handle(stream))
 
 
 def _one_device(**tensors):
@@ -71,7 +70,7 @@ def _need(t, name, dtype, ndim):
         raise ValueError(f"{name} must be contiguous (tight row-major)")
 
 
-def _gemm_args(A, B, C):
+def _gemm_args(A, B, C, stream):
     _need(A, "A", torch.float16, 2)
     _need(B, "B", torch.float16, 2)
     M, K = A.shape
@@ -79,7 +78,7 @@ def _gemm_args(A, B, C):
     if K != K2:
         raise ValueError(f"inner dimensions differ: A is {tuple(A.shape)}, B is {tuple(B.shape)}")
     if C is None:
-        C = torch.empty((M, N), dtype=torch.float16, device=A.device)
+        C = _streams.empty((M, N), torch.float16, A.device, stream)
     else:
         _need(C, "C", torch.float16, 2)
         if tuple(C.shape) != (M, N):
@@ -90,28 +89,28 @@ def _gemm_args(A, B, C):
 
 def gemm_f16(A: torch.Tensor, B: torch.Tensor, C: torch.Tensor | None = None, *, stream=None):
     """C = A @ B (fp16 in, fp32 accumulate, fp16 out) with the tile chosen from the shape."""
-    M, N, K, C = _gemm_args(A, B, C)
+    M, N, K, C = _gemm_args(A, B, C, stream)
     check(lib().gemm_f16(M, N, K, A.data_ptr(), B.data_ptr(), C.data_ptr(), _stream(stream)))
     return C
 
 
 def gemm_f16_with_tile(A, B, C=None, *, tile, stagger: int = -1, stream=None):
     """gemm_f16 with a forced ladder tile (id or name); stagger -1 auto, 0 off, 1 on."""
-    M, N, K, C = _gemm_args(A, B, C)
+    M, N, K, C = _gemm_args(A, B, C, stream)
     tid = tile_id(tile) if isinstance(tile, str) else int(tile)
     check(lib().gemm_f16_with_tile(M, N, K, A.data_ptr(), B.data_ptr(), C.data_ptr(),
                                    _stream(stream), tid, int(stagger)))
     return C
 
 
-def _gemv_args(x, W, y, wdtype):
+def _gemv_args(x, W, y, wdtype, stream):
     _need(x, "x", torch.bfloat16, 1)
     _need(W, "W", wdtype, 2)
     N, K = W.shape
     if x.shape[0] != K:
         raise ValueError(f"x has length {x.shape[0]}, W is {tuple(W.shape)} (K-major [N, K])")
     if y is None:
-        y = torch.empty(N, dtype=torch.float32, device=x.device)
+        y = _streams.empty(N, torch.float32, x.device, stream)
     else:
         _need(y, "y", torch.float32, 1)
         if y.shape[0] != N:
@@ -122,14 +121,14 @@ def _gemv_args(x, W, y, wdtype):
 
 def gemv_m1_bf16(x, W, y=None, *, stream=None):
     """y[n] = sum_k x[k] W[n, k]; x bf16 [K], W bf16 [N, K] (K-major), y fp32 [N]."""
-    K, N, y = _gemv_args(x, W, y, torch.bfloat16)
+    K, N, y = _gemv_args(x, W, y, torch.bfloat16, stream)
     check(lib().gemv_m1_bf16(K, N, x.data_ptr(), W.data_ptr(), y.data_ptr(), _stream(stream)))
     return y
 
 
 def gemv_m1_q8(x, q, scales, y=None, *, stream=None):
     """q8 decode: W[n, k] = q[n, k] * scales[n, k // 32]; q int8 [N, K], scales fp16 [N, K/32]."""
-    K, N, y = _gemv_args(x, q, y, torch.int8)
+    K, N, y = _gemv_args(x, q, y, torch.int8, stream)
     _need(scales, "scales", torch.float16, 2)
     if K % 32 or tuple(scales.shape) != (N, K // 32):
         raise ValueError(f"scales must be {(N, K // 32)} with K % 32 == 0")
@@ -164,7 +163,7 @@ def _layout_of(T, name):
     raise ValueError(f"{name} needs unit stride in one dimension (row-major or transposed row-major)")
 
 
-def _ex_args(A, B, C):
+def _ex_args(A, B, C, stream):
     """(M, N, K, lda, ldb, ldc, layout, C) of gemm_ex-style views."""
     if not isinstance(A, torch.Tensor) or not isinstance(B, torch.Tensor):
         raise TypeError("A and B must be torch.Tensors")
@@ -180,7 +179,7 @@ def _ex_args(A, B, C):
     a_t, lda = _layout_of(A, "A")
     b_t, ldb = _layout_of(B, "B")
     if C is None:
-        C = torch.empty((M, N), dtype=A.dtype, device=A.device)
+        C = _streams.empty((M, N), A.dtype, A.device, stream)
     else:
         if not isinstance(C, torch.Tensor):
             raise TypeError("C must be a torch.Tensor")
@@ -195,7 +194,7 @@ def _ex_args(A, B, C):
 def gemm_ex(A, B, C=None, *, tile=-1, stream=None):
     """C = A @ B for fp16 or bf16 views of any shape: A [M, K] and B [K, N] may be row-major
     (padded rows allowed) or transposed views (e.g. X.t()); C [M, N] row-major, padding allowed."""
-    M, N, K, lda, ldb, ldc, layout, C = _ex_args(A, B, C)
+    M, N, K, lda, ldb, ldc, layout, C = _ex_args(A, B, C, stream)
     tid = tile_id(tile) if isinstance(tile, str) else int(tile)
     check(lib().gemm_ex(M, N, K, A.data_ptr(), lda, B.data_ptr(), ldb, C.data_ptr(), ldc, DTYPE_CODES[A.dtype],
                         layout, tid, _stream(stream)))
@@ -224,7 +223,7 @@ def gemm_workspace(device=None) -> torch.Tensor:
 def gemm_f16_ws(A, B, C=None, *, workspace, stream=None):
     """gemm_f16 with a workspace (gemm_workspace()) in which a two-CTA tile's partly empty
     last round may split its tiles in K; workspace None runs gemm_f16."""
-    M, N, K, C = _gemm_args(A, B, C)
+    M, N, K, C = _gemm_args(A, B, C, stream)
     if workspace is None:
         check(lib().gemm_f16_ws(M, N, K, A.data_ptr(), B.data_ptr(), C.data_ptr(), None, 0, _stream(stream)))
         return C
@@ -238,7 +237,7 @@ def gemm_f16_ws(A, B, C=None, *, workspace, stream=None):
 def gemm_ex_ws(A, B, C=None, *, workspace, tile=-1, tail_splits: int = -1, stream=None):
     """gemm_ex with a gemm_f16_ws workspace; tail_splits -1 plans the last round, 0 never
     splits it, 2..8 forces that many k-ranges per leftover tile."""
-    M, N, K, lda, ldb, ldc, layout, C = _ex_args(A, B, C)
+    M, N, K, lda, ldb, ldc, layout, C = _ex_args(A, B, C, stream)
     tid = tile_id(tile) if isinstance(tile, str) else int(tile)
     wptr, nbytes = None, 0
     if workspace is not None:
@@ -288,7 +287,7 @@ def splitk_workspace(M: int, N: int, K: int, tile, splits: int, device=None) -> 
 def gemm_f16_splitk(A, B, C=None, *, workspace, tile=-1, splits: int = 0,
                     algo: int = SPLITK_REDUCE_KERNEL, stream=None):
     """Split-K GEMM with a caller-owned workspace (see sdt.h); tile -1 picks tile and splits."""
-    M, N, K, C = _gemm_args(A, B, C)
+    M, N, K, C = _gemm_args(A, B, C, stream)
     tid = tile_id(tile) if isinstance(tile, str) else int(tile)
     nbytes = _workspace(workspace)
     _one_device(A=A, workspace=workspace)
@@ -308,7 +307,7 @@ def gemm_ex_splitk(A, B, C=None, *, workspace, tile=-1, splits: int = 0, algo: i
     sized by splitk_ex_workspace_bytes (algo 0 and 1: `splits` k-slices per output tile) or
     streamk_workspace_bytes (algo SPLITK_STREAM or SPLITK_STREAM_REDUCE: `splits` is the CTA
     count, 0 = one per SM slot)."""
-    M, N, K, lda, ldb, ldc, layout, C = _ex_args(A, B, C)
+    M, N, K, lda, ldb, ldc, layout, C = _ex_args(A, B, C, stream)
     tid = tile_id(tile) if isinstance(tile, str) else int(tile)
     nbytes = _workspace(workspace)
     _one_device(A=A, workspace=workspace)
