@@ -8,6 +8,7 @@ the current stream, without a synchronisation, so a step can be captured in a CU
 from __future__ import annotations
 
 import ctypes
+import math
 import struct
 
 import torch
@@ -29,6 +30,7 @@ _I32, _I64 = torch.int32, torch.int64
 # sdt_paged_step and sdt_paged_attn (include/sdt.h): packing them takes a fraction of what ctypes takes
 # for as many arguments
 _STEP, _ATTN = struct.Struct("8P6q"), struct.Struct("7P10qfi")
+_FLT_MAX = 3.4028234663852886e38
 _functions = {}
 
 
@@ -37,6 +39,19 @@ def _fn(name):
     if f is None:
         f = _functions[name] = getattr(lib(), name)
     return f
+
+
+def _refuse(error, **integers):
+    """Raises what is wrong with the caller's own numbers, which could not be packed."""
+    scale = integers.pop("scale", None)
+    for name, value in integers.items():
+        if not hasattr(value, "__index__"):
+            raise TypeError(f"{name} must be an integer, got {type(value).__name__}") from error
+        if not -2 ** 63 <= value < 2 ** 63:
+            raise ValueError(f"{name} is out of range: {value}") from error
+    if scale is not None and not hasattr(scale, "__float__"):
+        raise TypeError(f"scale must be a number, got {type(scale).__name__}") from error
+    raise error
 
 
 def _need(t, name, dtype, ndim):
@@ -179,9 +194,12 @@ def paged_tables(lens, new_tokens, free_pages, table, *, page_size: int, slots, 
         used = _streams.empty(1, _I32, lens.device, stream)
     else:
         _need_vector(used, "used", _I32, 1)
-    call = _STEP.pack(lens.data_ptr(), new_tokens.data_ptr(), free_pages.data_ptr(), table.data_ptr(), kv_lens.data_ptr(),
-                      starts.data_ptr(), used.data_ptr(), slots.data_ptr(), batch, page_size, wide,
-                      step if batch > 1 else wide, len(free_pages), len(slots))
+    try:
+        call = _STEP.pack(lens.data_ptr(), new_tokens.data_ptr(), free_pages.data_ptr(), table.data_ptr(), kv_lens.data_ptr(),
+                          starts.data_ptr(), used.data_ptr(), slots.data_ptr(), batch, page_size, wide,
+                          step if batch > 1 else wide, len(free_pages), len(slots))
+    except (struct.error, TypeError, ValueError, OverflowError) as e:
+        _refuse(e, page_size=page_size)
     on = _current_stream(dev) if stream is None else _streams.handle(stream)
     if taken is None:
         check(_fn("paged_tables")(call, on))
@@ -274,11 +292,16 @@ def paged_attn_m1(q, cache: PagedCache, table, lens, out=None, *, workspace, sca
         _need(lse, "lse", torch.float32, 2)
         if lse.shape != (batch, q_heads) or not lse.is_contiguous():
             raise ValueError(f"lse must be contiguous {(batch, q_heads)}")
-    # (a dimension of one never steps: its stride may be anything)
-    check(_fn("paged_attn_m1")(
-        _ATTN.pack(q.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), table.data_ptr(), lens.data_ptr(),
-                   cache._address, workspace.data_ptr(), batch, q_heads, qb if batch > 1 else 0, qh if q_heads > 1 else 0,
-                   ob if batch > 1 else 0, oh if q_heads > 1 else 0, step if batch > 1 else wide, wide, window,
-                   len(workspace), head_dim ** -0.5 if scale is None else scale, DTYPE_CODES[dtype]),
-        _current_stream(dev) if stream is None else _streams.handle(stream)))
+    try:  # (a dimension of one never steps: its stride may be anything)
+        if scale is None:
+            scale = head_dim ** -0.5
+        elif _FLT_MAX < abs(scale) < math.inf:
+            raise ValueError(f"scale is out of range: {scale}")
+        call = _ATTN.pack(
+            q.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), table.data_ptr(), lens.data_ptr(), cache._address,
+            workspace.data_ptr(), batch, q_heads, qb if batch > 1 else 0, qh if q_heads > 1 else 0, ob if batch > 1 else 0,
+            oh if q_heads > 1 else 0, step if batch > 1 else wide, wide, window, len(workspace), scale, DTYPE_CODES[dtype])
+    except (struct.error, TypeError, ValueError, OverflowError) as e:
+        _refuse(e, window=window, scale=scale)
+    check(_fn("paged_attn_m1")(call, _current_stream(dev) if stream is None else _streams.handle(stream)))
     return out
