@@ -519,12 +519,11 @@ int paged_tables_taken(const sdt_paged_step *step, int32_t *taken, sdt_stream_t 
  * type), head h of token t at t * k_token + h * k_head elements, head_dim contiguous;
  * bases 16-byte aligned, strides multiples of 8 (of a single token or head: anything).  A
  * negative slot's token is left out; a slot past the cache is left out too and reported by
- * sdt_check_device_status.  Slots that
- * are not negative must differ: tokens with one slot may leave a row mixed from both, in q8
- * under the scale of either.  k and v must not lie at slots that the call writes.  q8: scale
- * = fp16(max|x| * fl32(1/127)), at most 65504, q = x / scale rounded to the nearest integer
- * (ties to even) within +-127, 0 where
- * the scale is 0 or x is NaN.
+ * sdt_check_device_status.  Slots that are not negative must differ: tokens with one slot may
+ * leave a row mixed from both, in q8 under the scale of either.  k and v must not lie at slots
+ * that the call writes.  q8: scale = fp16(max|x| * fl32(1/127)), at most 65504, q = x / scale
+ * rounded to the nearest integer (ties to even) within +-127, 0 where the scale is 0 or x is
+ * NaN.
  */
 int paged_append(int64_t tokens, const void *k, int64_t k_token, int64_t k_head, const void *v, int64_t v_token,
                  int64_t v_head, int dtype, const int64_t *slots, const sdt_paged_cache *cache,
@@ -538,11 +537,12 @@ int paged_append(int64_t tokens, const void *k, int64_t k_token, int64_t k_head,
  * fp16 or bf16 (dtype; a 16-bit cache's own type) with strides in elements (q multiples of
  * 8 and 16-byte aligned, out multiples of 4 and 8-byte aligned).  lse, if not NULL, gets
  * log(sum exp(scores)) as fp32 [batch][q_heads].  A request without keys, or whose scores
- * are all -inf, gets zeros and lse -inf.  What lies in the cache outside the named tokens
- * is not read.  A page id outside the cache is not followed and reported by
- * sdt_check_device_status; the request's out and lse are NaN.  A length past max_pages *
- * page_size is reported and taken as that.  Results do not depend on the order in which the
- * CTAs run.
+ * are all -inf, gets zeros and lse -inf.  A NaN or an infinity among a request's values (or
+ * q8 value scales) makes the outputs of its column (or group) NaN or infinite, and no others.
+ * What lies in the cache outside the named tokens is not read.  A page id outside the cache
+ * is not followed and reported by sdt_check_device_status; the request's out and lse are NaN.
+ * A length past max_pages * page_size is reported and taken as that.  Results do not depend
+ * on the order in which the CTAs run.
  *
  * Workspace: device memory owned by the caller, 256-byte aligned, at least
  * sdt_paged_attn_workspace_bytes() bytes: the 1 MiB counter region of the split-K

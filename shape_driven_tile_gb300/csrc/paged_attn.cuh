@@ -41,12 +41,21 @@
 //
 // Numbers: scores, maxima, sums and outputs stay in fp32.  The reference m moves only when
 // a score passes it by kAttnSlack, so most units rescale nothing; weights are then at most
-// 2^kAttnSlack.  They enter the second product as the sum of two 16-bit values (the rounded
-// weight and the rounded rest): one rounding to 8 bits would cost as much accuracy as the
-// output's own, and the matrix unit has the time.  fp16 ends at 2^-24, where the tokens of a
-// long context beside one that outweighs them all would be rounded to few bits or to zero (131071
-// tokens 16.3 below: their sum 28 % short where one warp had them all).  The reference therefore stays
-// 2^kAttnLower below the largest score: weights reach 2^15 and keep 2^-32 of the largest one.
+// 2^kAttnSlack.  What enters the products in fewer bits:
+//   16-bit caches: weights as the sum of two 16-bit values (the rounded weight and the rounded rest,
+//     2^-16 of a weight in bf16, 2^-22 in fp16): one rounding to 8 bits would cost as much accuracy as
+//     the output's own, and the matrix unit has the time.  fp16 ends at 2^-24, where the tokens of a
+//     long context beside one that outweighs them all would be rounded to few bits or to zero
+//     (131071 tokens 16.3 below: their sum 7 % short with the heavy one in one warp of four).  The
+//     reference therefore stays 2^kAttnLower below the largest score: weights reach 2^15 and keep
+//     2^-32 of the largest one.
+//   q8: weight times value scale in fp16, two parts for fp16 queries (2^-22).  One part for bf16
+//     queries: 2^-11 of a weight, an eighth of the output's rounding, where two would cost 5 to 18 %
+//     (48 requests of 4096 tokens, 8 heads of 128 a request: 77 and 84 us head by head, 16 query heads
+//     a key head 101 and 120).  Below fp16's range 2^-31 of a group's largest scale is kept (v_top).
+//   q8 with bf16 queries: queries in fp16, scaled by a power of two per head: what is 2^-25 of the
+//     head's largest element is lost (load_q).
+// The second part of a weight may be 0 or negative, so an infinite value makes its column NaN.
 #pragma once
 
 #include <type_traits>
@@ -270,7 +279,7 @@ __global__ void __launch_bounds__(NW * 32) paged_attn_kernel(const PagedAttnArgs
     constexpr int SUB = KS < 32 || (DP == 256 && NH == 2) ? 16 : 32;
     using PT = std::conditional_t<Q8, __half, T>;            // operand type of both products
     constexpr float LOWER = !Q8 && std::is_same_v<T, __half> ? kAttnLower : 0.f;  // (q8: see v_top)
-    constexpr bool LOW = !Q8 || std::is_same_v<T, __half>;   // weights in two parts
+    constexpr bool LOW = !Q8 || std::is_same_v<T, __half>;   // weights in two parts (see Numbers above)
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ float st_m[NW][C::HEADS], st_l[NW][C::HEADS];
     __shared__ long long sh_sum[NW], sh_rest;
