@@ -10,11 +10,11 @@
 // bytes (2 in q8), which the matrix instructions do at a fraction of their rate; the design
 // keeps enough bytes in flight and few instructions per byte.  GB300, against the measured
 // copy rate of 6782 GB/s: 64 requests of 1000 to 32768 tokens, 8 key heads of 128 in fp16 (2.42
-// GB), 350 to 363 us on different machines, 6.7 to 6.9 TB/s; one request of 131071 tokens (537 MB) 84.9 us, 6.3 TB/s; 16 ragged
-// requests (62 MB) 16.9 us, of which 2.3 us pass before the first keys arrive and 3.5 us join the
-// split items.  q8 is bound by its arithmetic: 520 instructions per 16 keys and warp to widen,
-// scale and multiply 4 KB (48 requests of 500 to 16000 tokens, 476 MB, 99.5 us, 4.8 TB/s).  Few
-// tokens cost a chain of trips to memory, lengths -> pages -> keys -> output: 3.7 us for 17.
+// GB), 350 to 363 us on different machines, 6.7 to 6.9 TB/s; one request of 131071 tokens (537 MB) 85.1 us, 6.3 TB/s; 16 ragged
+// requests (62 MB) 17.1 us, of which 2.3 us pass before the first keys arrive and 3.5 us join the
+// split items.  q8 is bound by its arithmetic: 533 instructions per 16 keys and warp to widen,
+// scale and multiply 4 KB (48 requests of 500 to 16000 tokens, 476 MB, 100.4 us, 4.7 TB/s).  Few
+// tokens cost a chain of trips to memory, lengths -> pages -> keys -> output: 3.75 us for 17.
 //
 // Work: a unit is TK consecutive keys of one (request, key head, block of query heads).
 // The units of all requests, in that order, are dealt out evenly over one resident grid, so
@@ -100,7 +100,7 @@ struct AttnCfg {
     static constexpr int ROWB = DP * (Q8 ? 1 : 2);        // bytes of a cached row in shared memory
     // Keys per warp of a unit: about 8 KB of keys and values, and room for the warp's o (8 NH x DP
     // fp32), which passes through the stage at an item's end.  Smaller units cost more instructions a key
-    // (q8 of 128, 48 requests of 4096: 16 keys a warp 96.4 us, 32 keys 75.8).
+    // (q8 of 128, 48 requests of 4096: 16 keys a warp 96.4 us, 32 keys 75.8 at the time, 76.4 now).
     static constexpr int KW = Q8 ? (DP == 256 && NH == 1 ? 16 : 32) : (DP == 64 ? 32 : 16);
     static constexpr int TK = KW * NW;                    // keys of a unit
     static constexpr int WK = NW / WH;                    // groups of warps with keys of their own
@@ -115,9 +115,9 @@ struct AttnCfg {
     // Whether a call may have its pieces joined by the second kernel (paged_attn_splits).
     static constexpr bool SPLITS = ROWS * DP >= kAttnSplitValues;
     // The warps of an SM hide each other's latency, so stages beyond two are worth less than another CTA
-    // where one fits: one-warp CTAs, heads of 64 and q8 of 128 take two (that: 109 us with three CTAs an SM,
-    // 126 with three stages and two CTAs).  Four warps of 16-bit heads of 128 have three stages, two CTAs
-    // an SM (one request of 8192 tokens 16.0 us; two stages, three CTAs and their pieces 21.0; 2.42 GB of
+    // where one fits: one-warp CTAs, heads of 64 and q8 of 128 take two (that: 48 requests of 500 to 16000
+    // tokens 100 us with three CTAs an SM, 108 with three stages and two CTAs).  Four warps of 16-bit heads of
+    // 128 have three stages, two CTAs an SM (one request of 8192 tokens 16.0 us; two stages, three CTAs and their pieces 21.0; 2.42 GB of
     // cache the same within 2 %); wider heads have the SM to themselves.
     static constexpr bool fits(int s, int bytes) { return s * (STAGE + ROWS * QROW) + 2048 <= bytes; }
     static constexpr int S = NW == 1 || DP == 64 || (Q8 && DP == 128) ? 2 : fits(3, 113 * 1024) || (!fits(2, 113 * 1024) && fits(3, 227 * 1024)) ? 3 : 2;

@@ -31,12 +31,13 @@ inline int paged_attn_ctas(int nw) { return nw == 1 ? 12 : 3; }
 // `items`: requests x key heads.
 //
 // Up to 8 heads: one warp has them.  Many items take CTAs of one warp, whose items end without a
-// barrier: 256 requests x 16 heads of 64, up to 1000 tokens, 35.5 us (four warps 46.4), q8 33.8
-// (45.5), 128 x 8 heads of 256 39.8 (51.6); with fewer items the pieces of split ones cost more
+// barrier: 256 requests x 16 heads of 64 in fp16, up to 1000 tokens, 32.9 us (four warps 43.0), q8 40.6
+// (45.7), 128 x 8 heads of 256 39.8 (51.6); with fewer items the pieces of split ones cost more
 // (128 x 8 heads of 128, up to 60 tokens, 15.3 us, four warps 10.1), and q8 of 128 is bound by
 // arithmetic that four warps with larger units do less of (46.8, 41.4).
 // More heads: a warp takes 16 where o fits its registers (heads of 128, 16 a key head, 16 requests of
-// 8192 in q8: 40.4 us, 8 a warp 49.4), and 8 of 256-wide ones (90.5 us, 16 a warp 103.9; q8 90.1, 136.2);
+// 8192, 8 key heads, in q8: 71.3 us, 8 a warp 113.4), and 8 of 256-wide ones (90.5 us, 16 a warp 103.9;
+// q8 90.1, 136.2);
 // beyond 32 of those reading the keys once is worth more (64 a key head: 115.4 us, 8 a warp 149.9).
 inline PagedAttnVariant paged_attn_variant(int64_t group, int64_t items, int64_t head_dim, bool q8, int sm_count) {
     const int width = paged_attn_width(head_dim);

@@ -104,7 +104,8 @@ def _need_values(t, name, cache, shape):
 
 
 class PagedCache:
-    """A paged key-value cache: views of the caller's tensors, checked once.
+    """A paged key-value cache: views of the caller's tensors, whose types and shapes are checked once (widths,
+    alignment and strides with each call).
 
     k, v: [num_pages, page_size, kv_heads, head_dim], float16, bfloat16 or int8, any strides
     with head_dim contiguous (a cache that is laid out head by head is given as
@@ -238,7 +239,8 @@ def paged_append(k, v, slots, cache: PagedCache, *, stream=None) -> PagedCache:
 
 
 def paged_attn_workspace(q_heads: int, kv_heads: int, head_dim: int, device=None) -> torch.Tensor:
-    """A zeroed, 256-byte aligned workspace for paged_attn_m1 (owned by the caller; any batch and lengths)."""
+    """A 256-byte aligned workspace for paged_attn_m1 (owned by the caller; any batch and lengths).  Its counters
+    are zeroed on the current stream, which a first call on another stream has to wait for."""
     nbytes = int(lib().sdt_paged_attn_workspace_bytes(q_heads, kv_heads, head_dim))
     if nbytes == 0:
         raise SdtError(-3, lib().sdt_last_error().decode())
@@ -257,7 +259,8 @@ def paged_attn_m1(q, cache: PagedCache, table, lens, out=None, *, workspace, sca
     multiple of the cache's heads: query head i reads key head i // (q_heads // kv_heads).
     table: int32 [batch, max_pages], lens: int32 [batch].  Request b attends to its tokens
     0 .. lens[b] - 1, or with window > 0 to the last `window` of them; without any it gets
-    zeros.  scale: None is 1 / sqrt(head_dim).  lse: float32 [batch, q_heads], if given
+    zeros.  A request that names a page outside the cache gets NaN (and check_device_status()
+    reports it).  scale: None is 1 / sqrt(head_dim).  lse: float32 [batch, q_heads], if given
     receives log(sum(exp(scores))).  workspace: paged_attn_workspace().
     """
     try:
