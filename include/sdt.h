@@ -568,6 +568,114 @@ int paged_attn_m1(const sdt_paged_attn *call, sdt_stream_t stream);
 size_t sdt_paged_attn_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t head_dim);
 
 /* ------------------------------------------------------------------------ */
+/* A layer in 8 bits: fp8 products, their operands, rotary positions          */
+/* ------------------------------------------------------------------------ */
+
+#define SDT_DTYPE_F32 3
+#define SDT_DTYPE_E4M3 4
+#define SDT_DTYPE_E5M2 5
+
+/*
+ * gemm_fp8 -- product of fp8 activations and fp8 weights with a scale per 128 values of k:
+ *   C[m][n] = sum_b a_scales[m][b] * w_scales[n / 128][b] * sum_{k in block b} A[m][k] * W[n][k],
+ * blocks b of 128 consecutive k (the last one may be shorter).  A: M x K, W: N x K ("K-major",
+ * as gemv_m1's), e4m3 or e5m2 each (SDT_DTYPE_E4M3 / _E5M2); scales fp32 of any strides; C:
+ * M x N fp16, bf16 or fp32.  Block sums are formed on the tensor cores, scaled and added in
+ * fp32, and rounded once to C's type.  Results depend on the shape (which decides the tile and
+ * how k is shared out) but not on timing.  A NaN among a row's values or scales makes that row
+ * (of W: that column) of C NaN; memory outside the operands is not read.
+ *
+ * Any M, K >= 0 (M == 0 or N == 0: no-op; K == 0 writes zeros); N a multiple of 8; dimensions
+ * up to 2^30.  A, W and C 16-byte aligned, lda and ldw (elements) multiples of 16 at least K,
+ * ldc a multiple of 8 at least N; a stride of a single row may be anything.  Scales 4-byte
+ * aligned, strides not negative.
+ * tile: 0 picks; 16, 32, 64 or 128 tokens per tile of 128 weight rows, whose blocks `splits`
+ * (0 picks, 1 .. 8) CTAs share.
+ * Errors: SDT_ERR_NULL, SDT_ERR_ALIGN, SDT_ERR_SHAPE (N, dimensions), SDT_ERR_ARG (types,
+ * strides, splits), SDT_ERR_TILE.
+ */
+typedef struct sdt_gemm_fp8 {
+    const void *a;
+    const float *a_scales;
+    const void *w;
+    const float *w_scales;
+    void *c;
+    int64_t M, N, K, lda, ldw, ldc;
+    int64_t as_row, as_block, ws_row, ws_block; /* scale strides in elements */
+    int a_dtype, w_dtype, c_dtype, tile, splits;
+} sdt_gemm_fp8;
+int gemm_fp8(const sdt_gemm_fp8 *call, sdt_stream_t stream);
+/* The tile and splits that gemm_fp8 picks on a GPU with sm_count SMs; needs no GPU. */
+int sdt_gemm_fp8_plan_for(int64_t M, int64_t N, int64_t K, int sm_count, int *tile, int *splits);
+
+/*
+ * quant_fp8 -- gemm_fp8's operand from 16-bit rows: q[t][i] = e4m3(y[t][i] / scales[t][i / 128])
+ * with y = x, or act(gate) * x (activation 1: silu, g / (1 + exp(-g)); 2: gelu's tanh form,
+ * 0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3)))), computed in fp32.  A block's scale is
+ * max(max|y|, 2^-100) / 448; its values are rounded to nearest even and at most 448.  A NaN
+ * stays a NaN of its own; a block that holds an infinity gets an infinite scale and stands for
+ * NaN.  Any number of tokens; width a multiple of 8 up to 65536, tokens * width up to 2^34.
+ * x and gate: fp16 or bf16 (dtype), 16-byte aligned, row strides multiples of 8 (they may be
+ * slices of one row, as a product writes them side by side); q: e4m3, 8-byte aligned, row
+ * stride a multiple of 8; scales: fp32 of any strides.  The outputs must not overlap the inputs
+ * or each other.
+ */
+typedef struct sdt_quant_fp8 {
+    const void *x, *gate; /* gate: NULL with activation 0 */
+    void *q;
+    float *scales;
+    int64_t tokens, width, x_row, gate_row, q_row, s_row, s_block; /* strides in elements */
+    int dtype, activation;
+} sdt_quant_fp8;
+int quant_fp8(const sdt_quant_fp8 *call, sdt_stream_t stream);
+
+/*
+ * rms_norm_fp8 -- the residual's addition, root-mean-square norm, and fp8 output:
+ *   r = x + residual, rounded to their type and written back to residual (without one: r = x);
+ *   y[t][i] = r[t][i] * weight[i] / sqrt(mean_j r[t][j]^2 + eps)      (fp32)
+ * and q, scales of y as quant_fp8 makes them.  out, if not NULL, receives y rounded to x's type.
+ * x, residual, out: fp16 or bf16 (dtype), 16-byte aligned, row strides multiples of 8; weight:
+ * x's type or fp32 (weight_dtype), 16-byte aligned; width up to 32768; sizes and outputs
+ * otherwise as quant_fp8.
+ * The outputs must not overlap the inputs or each other (residual is updated in place).
+ */
+typedef struct sdt_rms_norm_fp8 {
+    const void *x, *weight;
+    void *residual, *out; /* NULL: none */
+    void *q;
+    float *scales;
+    int64_t tokens, width, x_row, r_row, o_row, q_row, s_row, s_block;
+    float eps;
+    int dtype, weight_dtype;
+} sdt_rms_norm_fp8;
+int rms_norm_fp8(const sdt_rms_norm_fp8 *call, sdt_stream_t stream);
+
+/*
+ * rope_qk -- rotary positions of queries and keys.  Pair i of a head is (x, y) = elements
+ * (i, rotary / 2 + i), or (2 i, 2 i + 1) with interleaved; with t = positions[token] *
+ * turns[i] / 2^64 turns (modulo 1, exactly, negative positions too),
+ *   x' = magnitude * (x cos t - y sin t),  y' = magnitude * (y cos t + x sin t)
+ * in fp32, rounded once; inverse turns the other way (with it the call takes gradients of the
+ * outputs to gradients of the inputs).  Elements from rotary on are copied.
+ * q, k, q_out, k_out: [tokens][heads][head_dim] fp16 or bf16 (dtype), head_dim contiguous, any
+ * other strides in elements (16-byte aligned heads are fastest); heads may be 0 (no such side).
+ * An output is its input itself or lies apart from both inputs.  positions: int32 or int64
+ * (position_bytes 4 or 8); turns: uint64 [rotary / 2].  head_dim even, rotary even, at most
+ * head_dim; tokens * heads * head_dim below 2^31.
+ */
+typedef struct sdt_rope_qk {
+    const void *q, *k;
+    void *q_out, *k_out;
+    const void *positions;
+    const uint64_t *turns;
+    int64_t tokens, q_heads, k_heads, head_dim, rotary;
+    int64_t q_token, q_head, k_token, k_head, qo_token, qo_head, ko_token, ko_head;
+    float magnitude;
+    int dtype, position_bytes, interleaved, inverse;
+} sdt_rope_qk;
+int rope_qk(const sdt_rope_qk *call, sdt_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Diagnostics                                                               */
 /* ------------------------------------------------------------------------ */
 

@@ -13,7 +13,9 @@ import torch
 
 from . import _streams
 from ._lib import SdtError, check, lib, sdt_tile_desc
+from .fp8 import gemm_fp8, gemm_fp8_plan, quant_fp8, rms_norm_fp8
 from .paged import PagedCache, paged_append, paged_attn_m1, paged_attn_workspace, paged_tables
+from .rope import RopeTable, rope_frequencies, rope_qk
 
 __all__ = [
     "SdtError", "gemm_f16", "gemm_f16_with_tile", "gemv_m1", "gemv_m1_bf16", "gemv_m1_q8",
@@ -25,6 +27,7 @@ __all__ = [
     "SPLITK_STREAM", "SPLITK_STREAM_REDUCE", "streamk_ctas", "streamk_workspace_bytes",
     "gemm_f16_ws", "gemm_ex_ws", "gemm_workspace_bytes", "gemm_workspace", "pair_tail_plan",
     "PagedCache", "paged_tables", "paged_append", "paged_attn_m1", "paged_attn_workspace",
+    "gemm_fp8", "gemm_fp8_plan", "quant_fp8", "rms_norm_fp8", "RopeTable", "rope_frequencies", "rope_qk",
 ]
 
 

@@ -1,0 +1,348 @@
+// fp8_rows.cu -- rows of 16-bit values to fp8 with a scale per 128: rms_norm_fp8 (with the
+// residual's addition) and quant_fp8 (as they are, or act(gate) * x).
+//
+// Quantisation of one block of 128 values y (the last block of a row may be shorter):
+// top = max(max|y|, 2^-100), scale = top * fl(1/448), q = e4m3(y * (448 / top)), rounded to
+// nearest even; the product is within 2^-22 of y / scale before that rounding, and at most 448
+// up to a rounding that the conversion's saturation takes back.  The floor keeps 448 / top
+// finite for rows of zeros.  A NaN stays a NaN of its own; an infinity makes the scale infinite,
+// so that its whole block stands for NaN.
+//
+// A thread moves 16-byte pieces of 8 values; 16 neighbouring threads hold a block and find its
+// largest value by shuffles.  The norm holds a row in registers between the sum of squares and
+// the scaling, so each value is read once and written once.
+//
+// What bounds it: memory for prompts (see the measured figures at each kernel), the launch for a
+// decode step's rows.
+#include <cuda_fp8.h>
+
+#include <cstring>
+#include <type_traits>
+
+#include "launch.cuh"
+#include "paged.cuh"
+#include "ptx.cuh"
+
+namespace sdt {
+
+constexpr float kE4m3Max = 448.0f;
+constexpr float kTinyTop = 7.888609052210118e-31f;  // 2^-100
+constexpr int64_t kMaxQuantWidth = 65536, kMaxNormWidth = 32768;
+
+enum : int { kGateNone = 0, kGateSilu = 1, kGateGelu = 2 };
+
+template <typename T>
+__device__ __forceinline__ void to_f32(const uint4 &v, float (&f)[8]) {
+    const T *p = reinterpret_cast<const T *>(&v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = static_cast<float>(p[i]);
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 from_f32(const float (&f)[8]) {
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (std::is_same_v<T, __half>) {
+            const __half2 v = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+            memcpy(&h[i], &v, 4);
+        } else {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            memcpy(&h[i], &v, 4);
+        }
+    }
+    return make_uint4(h[0], h[1], h[2], h[3]);
+}
+
+__device__ __forceinline__ float top_of(const float (&f)[8]) {
+    float t = fabsf(f[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) t = fmaxf(t, fabsf(f[i]));
+    return t;
+}
+
+__device__ __forceinline__ uint2 to_e4m3(const float (&f)[8], float inv) {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i] * inv, f[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+        const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i + 2] * inv, f[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+        w[i] = static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+struct RowsOut {
+    uint8_t *q;
+    float *scales;
+    int64_t q_row, s_row, s_block;
+};
+
+// The block's scale and the piece's fp8 values; `group` lanes (16, or a row's 8) hold the block.
+__device__ __forceinline__ void quantise_piece(const RowsOut &o, int64_t row, int piece, const float (&f)[8], int group, bool write) {
+    float top = top_of(f);
+#pragma unroll
+    for (int x = 1; x < 16; x <<= 1)
+        if (x < group) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    top = fmaxf(top, kTinyTop);
+    if (!write) return;
+    *reinterpret_cast<uint2 *>(o.q + row * o.q_row + piece * 8) = to_e4m3(f, kE4m3Max / top);
+    if ((piece & 15) == 0) o.scales[row * o.s_row + (piece >> 4) * o.s_block] = top * (1.0f / kE4m3Max);
+}
+
+// ---- quant_fp8 ----------------------------------------------------------------------------
+
+constexpr int kQuantThreads = 256;
+constexpr int kQuantUnroll = 4;
+
+struct QuantArgs {
+    const char *x, *gate;
+    int64_t x_row, gate_row;  // bytes
+    RowsOut out;
+    uint32_t total;   // padded pieces of all rows
+    int pieces;       // 16-byte pieces of a row
+    FastDiv padded;   // pieces of a row rounded up to whole blocks of 16
+};
+
+template <typename T, int GATE>
+__global__ void __launch_bounds__(kQuantThreads) quant_fp8_kernel(const QuantArgs a) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const uint32_t base = blockIdx.x * (kQuantThreads * kQuantUnroll) + threadIdx.x;
+    uint4 x[kQuantUnroll], g[kQuantUnroll];
+    uint32_t row[kQuantUnroll];
+    int piece[kQuantUnroll];
+    bool have[kQuantUnroll];
+#pragma unroll
+    for (int u = 0; u < kQuantUnroll; ++u) {
+        const uint32_t i = base + u * kQuantThreads;
+        row[u] = a.padded.div(i);
+        piece[u] = static_cast<int>(i - row[u] * a.padded.d);
+        have[u] = i < a.total && piece[u] < a.pieces;
+        x[u] = g[u] = make_uint4(0, 0, 0, 0);
+        if (have[u]) {
+            x[u] = *reinterpret_cast<const uint4 *>(a.x + row[u] * a.x_row + piece[u] * 16);
+            if (GATE) g[u] = *reinterpret_cast<const uint4 *>(a.gate + row[u] * a.gate_row + piece[u] * 16);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kQuantUnroll; ++u) {
+        float f[8];
+        to_f32<T>(x[u], f);
+        if constexpr (GATE != kGateNone) {
+            float h[8];
+            to_f32<T>(g[u], h);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                // g * sigmoid(t): silu has t = g; gelu's tanh form is 0.5 g (1 + tanh(t / 2))
+                const float t = GATE == kGateSilu ? h[i] : h[i] * fmaf(0.0713548162726f, h[i] * h[i], 1.59576912160573f);
+                f[i] *= __fdividef(h[i], 1.0f + __expf(-t));
+            }
+        }
+        quantise_piece(a.out, row[u], piece[u], f, 16, have[u]);
+    }
+}
+
+// ---- rms_norm_fp8 -------------------------------------------------------------------------
+
+constexpr int kNormThreads = 512;  // at most
+
+struct NormArgs {
+    const char *x;
+    char *residual;       // NULL: none
+    const char *weight;
+    char *out16;          // NULL: not wanted
+    int64_t x_row, r_row, o_row;  // bytes
+    RowsOut out;
+    int rows, pieces, per_row;    // per_row: threads of a row, 8, 16, 32 or the whole CTA
+    float inv_width, eps;
+    int weight_f32;
+};
+
+template <typename T, int VPT>
+__global__ void __launch_bounds__(kNormThreads) rms_norm_fp8_kernel(const NormArgs a) {
+    griddep_launch_dependents();
+    const int per = a.per_row, whole = blockDim.x;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * (whole / per) + threadIdx.x / per;
+    const int r = threadIdx.x % per;
+    griddep_wait();
+    const bool live = row < a.rows;
+    uint4 x[VPT], res[VPT];
+#pragma unroll
+    for (int u = 0; u < VPT; ++u) {
+        const int piece = r + u * per;
+        x[u] = res[u] = make_uint4(0, 0, 0, 0);
+        if (live && piece < a.pieces) {
+            x[u] = *reinterpret_cast<const uint4 *>(a.x + row * a.x_row + piece * 16);
+            if (a.residual) res[u] = *reinterpret_cast<const uint4 *>(a.residual + row * a.r_row + piece * 16);
+        }
+    }
+    uint4 w[VPT];
+    if (!a.weight_f32)
+#pragma unroll
+        for (int u = 0; u < VPT; ++u)
+            if (r + u * per < a.pieces) w[u] = *reinterpret_cast<const uint4 *>(a.weight + (r + u * per) * 16);
+    float sum = 0.f;
+#pragma unroll
+    for (int u = 0; u < VPT; ++u) {
+        float f[8];
+        to_f32<T>(x[u], f);
+        if (a.residual) {
+            float h[8];
+            to_f32<T>(res[u], h);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] += h[i];
+            x[u] = from_f32<T>(f);  // the norm is of the sum as it is kept
+            to_f32<T>(x[u], f);
+            const int piece = r + u * per;
+            if (live && piece < a.pieces) *reinterpret_cast<uint4 *>(a.residual + row * a.r_row + piece * 16) = x[u];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = fmaf(f[i], f[i], sum);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+        if (o < per) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (per > 32) {  // (a row is the whole CTA)
+        __shared__ float part[32];
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
+        __syncthreads();
+        sum = (threadIdx.x & 31) < (whole >> 5) ? part[threadIdx.x & 31] : 0.f;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    const float k = rsqrtf(fmaf(sum, a.inv_width, a.eps));
+#pragma unroll
+    for (int u = 0; u < VPT; ++u) {
+        const int piece = r + u * per;
+        const bool have = live && piece < a.pieces;
+        float f[8], h[8];
+        to_f32<T>(x[u], f);
+        if (a.weight_f32) {
+            if (piece < a.pieces) {
+                const float4 lo = *reinterpret_cast<const float4 *>(a.weight + piece * 32), hi = *reinterpret_cast<const float4 *>(a.weight + piece * 32 + 16);
+                h[0] = lo.x; h[1] = lo.y; h[2] = lo.z; h[3] = lo.w; h[4] = hi.x; h[5] = hi.y; h[6] = hi.z; h[7] = hi.w;
+            }
+        } else {
+            to_f32<T>(w[u], h);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = have ? f[i] * k * h[i] : 0.f;
+        if (a.out16 && have) *reinterpret_cast<uint4 *>(a.out16 + row * a.o_row + piece * 16) = from_f32<T>(f);
+        quantise_piece(a.out, row, piece, f, per < 16 ? per : 16, have);
+    }
+}
+
+static int check_out(const char *who, void *q, float *scales, int64_t tokens, int64_t width, int64_t q_row, int64_t s_row,
+                     int64_t s_block) {
+    if (!q || !scales) return fail(SDT_ERR_NULL, "%s: q or scales is NULL", who);
+    if (!aligned(q, 8) || !aligned(scales, 4)) return fail(SDT_ERR_ALIGN, "%s: q must be 8-byte aligned, scales 4-byte", who);
+    if (tokens > 1 && (q_row < width || q_row % 8)) return fail(SDT_ERR_ARG, "%s: q's row stride must be a multiple of 8, at least the width", who);
+    const int64_t blocks = (width + 127) / 128;
+    constexpr int64_t most = int64_t(1) << 32;
+    if (s_row < 0 || s_block < 0 || s_row > most || s_block > most || q_row > most) return fail(SDT_ERR_ARG, "%s: strides must be in 0 .. 2^32", who);
+    const bool rows_out = tokens == 1 || s_row >= (blocks == 1 ? 1 : (blocks - 1) * s_block + 1);
+    const bool blocks_out = blocks == 1 || s_block >= (tokens == 1 ? 1 : (tokens - 1) * s_row + 1);
+    if (!((rows_out && (blocks == 1 || s_block > 0)) || (blocks_out && (tokens == 1 || s_row > 0))))
+        return fail(SDT_ERR_ARG, "%s: scales must not overlap one another", who);
+    return SDT_OK;
+}
+
+static int check_in(const char *who, const char *what, const void *p, int64_t tokens, int64_t row, int64_t width, bool out = false) {
+    if (!p) return fail(SDT_ERR_NULL, "%s: %s is NULL", who, what);
+    if (!aligned(p, 16)) return fail(SDT_ERR_ALIGN, "%s: %s must be 16-byte aligned", who, what);
+    if (tokens > 1 && (row < (out ? width : 0) || row % 8 || row > (int64_t(1) << 32)))
+        return fail(SDT_ERR_ARG, "%s: the row stride of %s must be a multiple of 8 elements%s", who, what, out ? ", at least the width" : "");
+    return SDT_OK;
+}
+
+static int check_size(const char *who, int64_t tokens, int64_t width, int64_t widest, int dtype) {
+    if (width < 0 || width > widest || width % 8) return fail(SDT_ERR_SHAPE, "%s: width must be a multiple of 8 up to %lld (got %lld)", who, (long long)widest, (long long)width);
+    if (tokens < 0 || (width > 0 && tokens > (INT32_MAX - kQuantThreads * kQuantUnroll) / ((width + 127) / 128 * 16)))
+        return fail(SDT_ERR_SHAPE, "%s: tokens * width must be in 0 .. 2^34 (got %lld tokens)", who, (long long)tokens);
+    if (dtype != SDT_DTYPE_F16 && dtype != SDT_DTYPE_BF16) return fail(SDT_ERR_ARG, "%s: dtype must be fp16 or bf16 (got %d)", who, dtype);
+    return SDT_OK;
+}
+
+}  // namespace sdt
+
+using namespace sdt;
+
+extern "C" {
+
+int quant_fp8(const sdt_quant_fp8 *call, sdt_stream_t stream) {
+    clear_error();
+    if (!call) return fail(SDT_ERR_NULL, "quant_fp8: NULL call");
+    sdt_quant_fp8 c;
+    memcpy(&c, call, sizeof c);
+    int rc = check_size("quant_fp8", c.tokens, c.width, kMaxQuantWidth, c.dtype);
+    if (rc) return rc;
+    if (c.activation < 0 || c.activation > 2 || (c.activation != 0) != (c.gate != nullptr))
+        return fail(SDT_ERR_ARG, "quant_fp8: an activation (1 silu, 2 gelu) goes with a gate, and only with one");
+    if (c.tokens == 0 || c.width == 0) return SDT_OK;
+    rc = check_in("quant_fp8", "x", c.x, c.tokens, c.x_row, c.width);
+    if (!rc && c.gate) rc = check_in("quant_fp8", "gate", c.gate, c.tokens, c.gate_row, c.width);
+    if (!rc) rc = check_out("quant_fp8", c.q, c.scales, c.tokens, c.width, c.q_row, c.s_row, c.s_block);
+    if (rc) return rc;
+    rc = current_device(nullptr);
+    if (rc) return rc;
+    const uint32_t padded = static_cast<uint32_t>((c.width + 127) / 128 * 16);
+    QuantArgs a{static_cast<const char *>(c.x), static_cast<const char *>(c.gate), c.x_row * 2, c.gate_row * 2,
+                {static_cast<uint8_t *>(c.q), c.scales, c.q_row, c.s_row, c.s_block},
+                static_cast<uint32_t>(c.tokens) * padded, static_cast<int>(c.width / 8), FastDiv::of(padded)};
+    constexpr uint32_t per_cta = kQuantThreads * kQuantUnroll;
+    const dim3 grid((a.total + per_cta - 1) / per_cta);
+    const bool half = c.dtype == SDT_DTYPE_F16;
+    auto kern = c.activation == kGateNone   ? (half ? quant_fp8_kernel<__half, 0> : quant_fp8_kernel<__nv_bfloat16, 0>)
+                : c.activation == kGateSilu ? (half ? quant_fp8_kernel<__half, 1> : quant_fp8_kernel<__nv_bfloat16, 1>)
+                                            : (half ? quant_fp8_kernel<__half, 2> : quant_fp8_kernel<__nv_bfloat16, 2>);
+    const cudaError_t e = launch_kernel(kern, grid, dim3(kQuantThreads), 0, reinterpret_cast<cudaStream_t>(stream), 1, a);
+    if (e != cudaSuccess) return fail(SDT_ERR_LAUNCH, "quant_fp8 launch failed: %s", cudaGetErrorString(e));
+    return SDT_OK;
+}
+
+int rms_norm_fp8(const sdt_rms_norm_fp8 *call, sdt_stream_t stream) {
+    clear_error();
+    if (!call) return fail(SDT_ERR_NULL, "rms_norm_fp8: NULL call");
+    sdt_rms_norm_fp8 c;
+    memcpy(&c, call, sizeof c);
+    int rc = check_size("rms_norm_fp8", c.tokens, c.width, kMaxNormWidth, c.dtype);
+    if (rc) return rc;
+    if (c.weight_dtype != c.dtype && c.weight_dtype != SDT_DTYPE_F32)
+        return fail(SDT_ERR_ARG, "rms_norm_fp8: weight must have x's type or fp32 (dtype %d)", c.weight_dtype);
+    if (!(c.eps >= 0.0f)) return fail(SDT_ERR_ARG, "rms_norm_fp8: eps must not be negative or NaN");
+    if (c.tokens == 0 || c.width == 0) return SDT_OK;
+    rc = check_in("rms_norm_fp8", "x", c.x, c.tokens, c.x_row, c.width);
+    if (!rc) rc = check_in("rms_norm_fp8", "weight", c.weight, 1, 0, c.width);
+    if (!rc && c.residual) rc = check_in("rms_norm_fp8", "residual", c.residual, c.tokens, c.r_row, c.width, true);
+    if (!rc && c.out) rc = check_in("rms_norm_fp8", "out", c.out, c.tokens, c.o_row, c.width, true);
+    if (!rc) rc = check_out("rms_norm_fp8", c.q, c.scales, c.tokens, c.width, c.q_row, c.s_row, c.s_block);
+    if (rc) return rc;
+    rc = current_device(nullptr);
+    if (rc) return rc;
+    NormArgs a{static_cast<const char *>(c.x), static_cast<char *>(c.residual), static_cast<const char *>(c.weight),
+               static_cast<char *>(c.out), c.x_row * 2, c.r_row * 2, c.o_row * 2,
+               {static_cast<uint8_t *>(c.q), c.scales, c.q_row, c.s_row, c.s_block},
+               static_cast<int>(c.tokens), static_cast<int>(c.width / 8), 0, 1.0f / static_cast<float>(c.width), c.eps,
+               c.weight_dtype == SDT_DTYPE_F32};
+    // rows of up to 32 pieces: several to a CTA, a power of two of threads each
+    int vpt = 1, threads = 128;
+    if (a.pieces <= 32) {
+        a.per_row = a.pieces <= 8 ? 8 : a.pieces <= 16 ? 16 : 32;
+    } else {
+        while (vpt < 8 && a.pieces > vpt * kNormThreads) vpt *= 2;
+        a.per_row = threads = ((a.pieces + vpt - 1) / vpt + 31) / 32 * 32;
+    }
+    const int per_cta = threads / a.per_row;
+    const dim3 grid(static_cast<unsigned>((c.tokens + per_cta - 1) / per_cta));
+    const bool half = c.dtype == SDT_DTYPE_F16;
+    auto kern = vpt == 1   ? (half ? rms_norm_fp8_kernel<__half, 1> : rms_norm_fp8_kernel<__nv_bfloat16, 1>)
+                : vpt == 2 ? (half ? rms_norm_fp8_kernel<__half, 2> : rms_norm_fp8_kernel<__nv_bfloat16, 2>)
+                : vpt == 4 ? (half ? rms_norm_fp8_kernel<__half, 4> : rms_norm_fp8_kernel<__nv_bfloat16, 4>)
+                           : (half ? rms_norm_fp8_kernel<__half, 8> : rms_norm_fp8_kernel<__nv_bfloat16, 8>);
+    const cudaError_t e = launch_kernel(kern, grid, dim3(threads), 0, reinterpret_cast<cudaStream_t>(stream), 1, a);
+    if (e != cudaSuccess) return fail(SDT_ERR_LAUNCH, "rms_norm_fp8 launch failed: %s", cudaGetErrorString(e));
+    return SDT_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,154 @@
+// gemm_fp8.cu -- host side of gemm_fp8: checks, the choice of tile and splits, tensor maps.
+#include "gemm_fp8.cuh"
+
+#include <algorithm>
+#include <cstring>
+
+#include "gemm_fp8_launch.cuh"
+#include "host_common.cuh"
+#include "tensor_map.cuh"
+
+namespace sdt {
+
+constexpr int64_t kFp8MaxDim = int64_t(1) << 30;
+constexpr int kFp8MaxSplits = 8;  // CTAs of a portable cluster
+
+struct Fp8Plan {
+    int tile, splits;
+};
+
+// `tile`: 0, or the tile that the caller asks for.
+static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int sm_count, int tile = 0) {
+    Fp8Plan p;
+    p.tile = tile ? tile : M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    const int64_t tiles = ((M + p.tile - 1) / p.tile) * ((N + 127) / 128), kb = (K + kFp8Block - 1) / kFp8Block;
+    const int64_t slots = 2 * sm_count;
+    double best = 0;
+    p.splits = 1;
+    for (int s = 1; s <= kFp8MaxSplits && s <= kb; ++s) {
+        // k-blocks one after another on a slot, each CTA's start and end counted as four
+        const double t = double((tiles * s + slots - 1) / slots) * (double((kb + s - 1) / s) + 4.0);
+        if (s == 1 || t < best) {
+            best = t;
+            p.splits = s;
+        }
+    }
+    return p;
+}
+
+static bool is_fp8(int t) { return t == SDT_DTYPE_E4M3 || t == SDT_DTYPE_E5M2; }
+static bool at(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+static int check_fp8(const sdt_gemm_fp8 &c) {
+    if (c.M < 0 || c.N < 0 || c.K < 0 || c.M > kFp8MaxDim || c.N > kFp8MaxDim || c.K > kFp8MaxDim)
+        return fail(SDT_ERR_SHAPE, "gemm_fp8: M, N and K must be in 0 .. 2^30 (got %lld, %lld, %lld)", (long long)c.M,
+                    (long long)c.N, (long long)c.K);
+    if (c.N % 8) return fail(SDT_ERR_SHAPE, "gemm_fp8: N must be a multiple of 8 (got %lld)", (long long)c.N);
+    if (!is_fp8(c.a_dtype) || !is_fp8(c.w_dtype)) return fail(SDT_ERR_ARG, "gemm_fp8: A and W must be e4m3 or e5m2");
+    if (c.c_dtype != SDT_DTYPE_F16 && c.c_dtype != SDT_DTYPE_BF16 && c.c_dtype != SDT_DTYPE_F32)
+        return fail(SDT_ERR_ARG, "gemm_fp8: C must be fp16, bf16 or fp32 (dtype %d)", c.c_dtype);
+    if (c.tile != 0 && c.tile != 16 && c.tile != 32 && c.tile != 64 && c.tile != 128)
+        return fail(SDT_ERR_TILE, "gemm_fp8: no tile %d", c.tile);
+    if (c.splits < 0 || c.splits > kFp8MaxSplits) return fail(SDT_ERR_ARG, "gemm_fp8: splits must be in 0 .. %d", kFp8MaxSplits);
+    if (c.M == 0 || c.N == 0) return SDT_OK;
+    if (!c.c) return fail(SDT_ERR_NULL, "gemm_fp8: C is NULL");
+    if (!at(c.c, 16)) return fail(SDT_ERR_ALIGN, "gemm_fp8: C must be 16-byte aligned");
+    if (c.M > 1 && (c.ldc < c.N || c.ldc % 8)) return fail(SDT_ERR_ARG, "gemm_fp8: ldc must be a multiple of 8, at least N (got %lld)", (long long)c.ldc);
+    if (c.K == 0) return SDT_OK;
+    if (!c.a || !c.w || !c.a_scales || !c.w_scales) return fail(SDT_ERR_NULL, "gemm_fp8: NULL operand or scales");
+    if (!at(c.a, 16) || !at(c.w, 16)) return fail(SDT_ERR_ALIGN, "gemm_fp8: A and W must be 16-byte aligned");
+    if (!at(c.a_scales, 4) || !at(c.w_scales, 4)) return fail(SDT_ERR_ALIGN, "gemm_fp8: scales must be 4-byte aligned");
+    if (c.M > 1 && (c.lda < c.K || c.lda % 16)) return fail(SDT_ERR_ARG, "gemm_fp8: lda must be a multiple of 16, at least K (got %lld)", (long long)c.lda);
+    if (c.N > 1 && (c.ldw < c.K || c.ldw % 16)) return fail(SDT_ERR_ARG, "gemm_fp8: ldw must be a multiple of 16, at least K (got %lld)", (long long)c.ldw);
+    // strides that TMA takes (below 2^40 bytes), and scale offsets within 64 bits
+    constexpr int64_t most = int64_t(1) << 32;
+    if (c.lda >= most || c.ldw >= most || c.ldc >= most) return fail(SDT_ERR_ARG, "gemm_fp8: strides must be below 2^32 elements");
+    for (int64_t s : {c.as_row, c.as_block, c.ws_row, c.ws_block})
+        if (s < 0 || s >= most) return fail(SDT_ERR_ARG, "gemm_fp8: scale strides must be in 0 .. 2^32 (got %lld)", (long long)s);
+    return SDT_OK;
+}
+
+static int run_swap(const sdt_gemm_fp8 &c, const Fp8Plan &plan, Fp8Args &a, int64_t lda, int64_t ldw, cudaStream_t stream) {
+    a.num_m_tiles = int((c.M + plan.tile - 1) / plan.tile);
+    a.num_n_tiles = int((c.N + 127) / 128);
+    a.splits = plan.splits;
+    if (int64_t(a.num_m_tiles) * a.num_n_tiles * a.splits > INT32_MAX) return fail(SDT_ERR_SHAPE, "gemm_fp8: grid too large");
+    // W is the MMA's first operand here
+    a.idesc = (1u << 4) | ((c.w_dtype == SDT_DTYPE_E5M2 ? 1u : 0u) << 7) | ((c.a_dtype == SDT_DTYPE_E5M2 ? 1u : 0u) << 10);
+    CUtensorMap tmW, tmX;
+    int rc = tensor_map_2d(c.w, c.w_dtype, uint64_t(c.K), uint64_t(c.N), uint64_t(ldw), 128, &tmW, kFp8Block);
+    if (!rc) rc = tensor_map_2d(c.a, c.a_dtype, uint64_t(c.K), uint64_t(c.M), uint64_t(lda), plan.tile, &tmX, kFp8Block);
+    if (rc) return rc;
+    int e = plan.tile == 16   ? launch_fp8_swap<16>(tmW, tmX, a, stream)
+            : plan.tile == 32 ? launch_fp8_swap<32>(tmW, tmX, a, stream)
+            : plan.tile == 64 ? launch_fp8_swap<64>(tmW, tmX, a, stream)
+                              : launch_fp8_swap<128>(tmW, tmX, a, stream);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(SDT_ERR_LAUNCH, "gemm_fp8 launch failed: %s", cudaGetErrorString(cudaError_t(e)));
+    }
+    return SDT_OK;
+}
+
+}  // namespace sdt
+
+using namespace sdt;
+
+extern "C" {
+
+int sdt_gemm_fp8_plan_for(int64_t M, int64_t N, int64_t K, int sm_count, int *tile, int *splits) {
+    clear_error();
+    if (!tile || !splits) return fail(SDT_ERR_NULL, "NULL output pointer");
+    if (M < 1 || N < 1 || K < 1 || M > kFp8MaxDim || N > kFp8MaxDim || K > kFp8MaxDim || sm_count < 1)
+        return fail(SDT_ERR_SHAPE, "M, N, K must be in 1 .. 2^30 and sm_count positive");
+    const Fp8Plan p = fp8_plan(M, N, K, sm_count);
+    *tile = p.tile;
+    *splits = p.splits;
+    return SDT_OK;
+}
+
+int gemm_fp8(const sdt_gemm_fp8 *call, sdt_stream_t stream_h) {
+    clear_error();
+    if (!call) return fail(SDT_ERR_NULL, "gemm_fp8: NULL call");
+    sdt_gemm_fp8 c;
+    memcpy(&c, call, sizeof c);  // (a packed call may lie at any address)
+    int rc = check_fp8(c);
+    if (rc || c.M == 0 || c.N == 0) return rc;
+    DeviceInfo dev;
+    rc = current_device(&dev);
+    if (rc) return rc;
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_h);
+    // a dimension of one never steps: its stride may be anything
+    const auto up16 = [](int64_t k) { return (k + 15) / 16 * 16; };
+    const int64_t lda = c.M > 1 ? c.lda : up16(c.K), ldw = c.N > 1 ? c.ldw : up16(c.K), ldc = c.M > 1 ? c.ldc : c.N;
+    const size_t size = c.c_dtype == SDT_DTYPE_F32 ? 4 : 2;
+    if (c.K == 0) {
+        const cudaError_t e = cudaMemset2DAsync(c.c, size_t(ldc) * size, 0, size_t(c.N) * size, size_t(c.M), stream);
+        if (e == cudaSuccess) return SDT_OK;
+        cudaGetLastError();
+        return fail(SDT_ERR_CUDA, "gemm_fp8: zeroing C failed: %s", cudaGetErrorString(e));
+    }
+    Fp8Args a;
+    memset(&a, 0, sizeof a);
+    a.a_scales = c.a_scales;
+    a.w_scales = c.w_scales;
+    a.C = c.c;
+    a.as_row = c.as_row;
+    a.as_block = c.as_block;
+    a.ws_row = c.ws_row;
+    a.ws_block = c.ws_block;
+    a.ldc = ldc;
+    a.M = int(c.M);
+    a.N = int(c.N);
+    a.num_kb = int((c.K + kFp8Block - 1) / kFp8Block);
+    a.c_dtype = c.c_dtype;
+    a.timeout_ns = wait_timeout_ns();
+    rc = status_word(&a.status);
+    if (rc) return rc;
+    Fp8Plan plan = fp8_plan(c.M, c.N, c.K, dev.sm_count, c.tile);
+    if (c.splits) plan.splits = c.splits;
+    plan.splits = std::min(plan.splits, a.num_kb);
+    return run_swap(c, plan, a, lda, ldw, stream);
+}
+
+}  // extern "C"

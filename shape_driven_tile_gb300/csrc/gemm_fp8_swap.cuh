@@ -1,0 +1,289 @@
+// gemm_fp8_swap.cuh -- gemm_fp8 for few tokens: 128 weight rows by BT tokens per tile, the
+// tile's k-blocks shared by a cluster of CTAs.
+//
+// The product runs as W . A^T, so that the many weight rows fill the MMA's 128 rows and BT
+// (16, 32, 64 or 128) tokens its columns: a weight byte is read from memory once for up to BT
+// tokens, and a single token costs what the weights' bytes cost.  The accumulator's lane is a
+// weight row and its column a token: the weight scale is the tile's, the token scales come from
+// shared memory as four at a time.
+//
+// What bounds it at few tokens is the stream of weights, so the work is cut to fill the GPU:
+// the CTAs of a cluster take consecutive ranges of the k-blocks of one tile, hold their sums in
+// registers, write them to their own shared memory at the end, and each adds up a share of the
+// tile's values from all of them through distributed shared memory, in rank order (results do
+// not depend on timing) and without a workspace.
+//
+// Tensor memory is freed before the cluster meets: no CTA holds any while it waits for another
+// one, so kernels of several streams cannot block each other over it.
+//
+// Roles: warp 0 lane 0 feeds the ring (TMA), warp 1 issues the MMAs, the rest scale and add.
+#pragma once
+
+#include "gemm_fp8.cuh"
+
+namespace sdt {
+
+template <int BT>
+struct SwapCfg {
+    static constexpr int ROWS = 128;  // weight rows per tile
+    static constexpr int EPI_WARPS = BT == 128 ? 8 : 4;
+    static constexpr int COLS = BT * 4 / EPI_WARPS;  // tokens per epilogue warp
+    static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+    static constexpr int W_BYTES = ROWS * kFp8Block;
+    static constexpr int X_BYTES = BT * kFp8Block;
+    static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
+    static constexpr int ACC_BUFS = BT == 128 ? 2 : 4;
+    static constexpr int TMEM_COLS = ACC_BUFS * BT;  // 64 .. 256: two CTAs of an SM always fit
+    static constexpr int STAGES = BT == 16 ? 5 : BT == 32 ? 5 : BT == 64 ? 4 : 3;
+    static constexpr int CHUNK = BT == 128 ? 8 : 512 / BT;  // k-blocks whose scales are in shared memory at a time
+    static constexpr int SCALE_BYTES = CHUNK * BT * 4;
+    static constexpr int PER_THREAD = CHUNK * BT / (32 * EPI_WARPS);  // scales each epilogue thread brings
+    static constexpr int CTRL_BYTES = 512;
+    static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 2 * SCALE_BYTES + CTRL_BYTES;
+    static_assert(BT == 16 || BT == 32 || BT == 64 || BT == 128, "tokens per tile");
+    static_assert(STAGES * STAGE_BYTES >= ROWS * BT * 4, "the sums reuse the ring");
+    static_assert(SMEM_BYTES <= 115712, "two CTAs share an SM");
+};
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+template <int BT>
+__global__ void __launch_bounds__(SwapCfg<BT>::THREADS, 2)
+    gemm_fp8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                         const Fp8Args p) {
+    using Cfg = SwapCfg<BT>;
+    constexpr int S = Cfg::STAGES, NB = Cfg::ACC_BUFS, E = Cfg::EPI_WARPS * 32;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t smW = base, smX = base + S * Cfg::W_BYTES;
+    const uint32_t smS = base + S * Cfg::STAGE_BYTES;  // two chunks of scales
+    const uint32_t bars = smS + 2 * Cfg::SCALE_BYTES;
+    const uint32_t full = bars, empty = bars + 8 * S, acc_full = bars + 16 * S, acc_empty = acc_full + 8 * NB;
+    volatile uint32_t *ctrl = reinterpret_cast<volatile uint32_t *>(smem_raw + (acc_empty + 8 * NB - smem_u32(smem_raw)));
+    // ctrl[0]: TMEM base   ctrl[1]: a role gave up   ctrl[2]: blocks the producer asked for
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = p.splits > 1 ? cluster_ctarank() : 0;
+    const int tile = static_cast<int>(blockIdx.x) / p.splits;
+    // tokens fastest: CTAs that run together share weights through L2
+    const int n_tile = tile / p.num_m_tiles, m_tile = tile - n_tile * p.num_m_tiles;
+    const int n0 = n_tile * Cfg::ROWS, m0 = m_tile * BT;
+    const int kb0 = static_cast<int>(static_cast<int64_t>(rank) * p.num_kb / p.splits);
+    const int kb1 = static_cast<int>(static_cast<int64_t>(rank + 1) * p.num_kb / p.splits);
+    const int nkb = kb1 - kb0;
+    const uint64_t lim = p.timeout_ns;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full + 8 * s, 1);
+            mbar_init(empty + 8 * s, 1);
+        }
+        for (int b = 0; b < NB; ++b) {
+            mbar_init(acc_full + 8 * b, 1);
+            mbar_init(acc_empty + 8 * b, Cfg::EPI_WARPS);
+        }
+        ctrl[1] = 0;
+        ctrl[2] = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(const_cast<uint32_t *>(&ctrl[0])), Cfg::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = ctrl[0];
+    griddep_launch_dependents();
+    griddep_wait();
+
+    uint64_t acc[Cfg::COLS / 2];
+#pragma unroll
+    for (int j = 0; j < Cfg::COLS / 2; ++j) acc[j] = 0;
+    bool good = true;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int s = 0, issued = 0;
+            uint32_t phase = 0;
+            for (int i = 0; i < nkb; ++i) {
+                if (!mbar_wait_for(empty + 8 * s, phase ^ 1u, lim)) {
+                    record_status(p.status, kSiteProducer | (i << 8));
+                    ctrl[1] = 1;
+                    break;
+                }
+                if (ctrl[1]) break;
+                mbar_arrive_expect_tx(full + 8 * s, Cfg::STAGE_BYTES);
+                tma_load_2d(smW + s * Cfg::W_BYTES, &tmW, full + 8 * s, (kb0 + i) * kFp8Block, n0);
+                tma_load_2d(smX + s * Cfg::X_BYTES, &tmX, full + 8 * s, (kb0 + i) * kFp8Block, m0);
+                ++issued;
+                if (++s == S) { s = 0; phase ^= 1u; }
+            }
+            ctrl[2] = issued;
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = idesc_for(p.idesc, Cfg::ROWS, BT);
+            const uint64_t w0 = smem_desc_sw128(smW, 16, 1024), x0 = smem_desc_sw128(smX, 16, 1024);
+            int s = 0, b = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            for (int i = 0; i < nkb; ++i) {
+                if (!mbar_wait_for(acc_empty + 8 * b, acc_phase ^ 1u, lim) || !mbar_wait_for(full + 8 * s, phase, lim)) {
+                    record_status(p.status, kSiteMma | (i << 8));
+                    ctrl[1] = 1;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t wd = w0 + static_cast<uint64_t>(s) * (Cfg::W_BYTES >> 4);
+                const uint64_t xd = x0 + static_cast<uint64_t>(s) * (Cfg::X_BYTES >> 4);
+#pragma unroll
+                for (int kk = 0; kk < kFp8Block / 32; ++kk)
+                    umma_fp8(tmem_base + b * BT, wd + 2 * kk, xd + 2 * kk, idesc, kk > 0);
+                umma_commit(empty + 8 * s);
+                umma_commit(acc_full + 8 * b);
+                if (++s == S) { s = 0; phase ^= 1u; }
+                if (++b == NB) { b = 0; acc_phase ^= 1u; }
+            }
+        }
+        __syncwarp();
+    } else {
+        const int q = warp & 3;                                   // TMEM lane quarter
+        const int col0 = Cfg::EPI_WARPS == 8 ? ((warp - 2) >> 2) * Cfg::COLS : 0;
+        const int t = static_cast<int>(threadIdx.x) - 64;
+        // scales of chunk c, weight and token scale multiplied: [block][token]
+        float mine[Cfg::PER_THREAD];
+        const bool by_token = p.as_row == 1;  // neighbouring threads take neighbouring values
+        auto place = [&](int u, int &kb, int &j) {
+            const int e = u * E + t;
+            if (by_token) { kb = e / BT; j = e % BT; }
+            else { kb = e % Cfg::CHUNK; j = e / Cfg::CHUNK; }
+        };
+        auto fetch = [&](int c) {
+#pragma unroll
+            for (int u = 0; u < Cfg::PER_THREAD; ++u) {
+                int kb, j;
+                place(u, kb, j);
+                kb += kb0 + c * Cfg::CHUNK;
+                mine[u] = 0.f;
+                if (kb < kb1 && m0 + j < p.M)
+                    mine[u] = p.a_scales[(m0 + j) * p.as_row + kb * p.as_block] * p.w_scales[n_tile * p.ws_row + kb * p.ws_block];
+            }
+        };
+        auto store = [&](int c) {
+#pragma unroll
+            for (int u = 0; u < Cfg::PER_THREAD; ++u) {
+                int kb, j;
+                place(u, kb, j);
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(smS + (c & 1) * Cfg::SCALE_BYTES + (kb * BT + j) * 4), "f"(mine[u]) : "memory");
+            }
+        };
+        fetch(0);
+        store(0);
+        named_barrier(1, E);
+        int b = 0;
+        uint32_t acc_phase = 0;
+        const uint32_t taddr0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + col0;
+        for (int i = 0; i < nkb; ++i) {
+            const int c = i / Cfg::CHUNK, r = i % Cfg::CHUNK;
+            const bool more = (c + 1) * Cfg::CHUNK < nkb;
+            if (r == 0 && more) fetch(c + 1);
+            if (good && !warp_wait(acc_full + 8 * b, acc_phase, 4 * lim, lane)) {
+                if (lane == 0) {
+                    record_status(p.status, kSiteEpilogue | (i << 8));
+                    ctrl[1] = 1;
+                }
+                good = false;  // (the warps still meet at their barriers)
+            }
+            if (good) {
+                tc_fence_after();
+                const uint32_t sc = smS + (c & 1) * Cfg::SCALE_BYTES + (r * BT + col0) * 4;
+#pragma unroll
+                for (int h = 0; h < Cfg::COLS; h += 16) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x16(taddr0 + b * BT + h, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4) {
+                        const float4 f = ld_shared_f4(sc + (h + j) * 4);
+                        uint64_t &a0 = acc[(h + j) / 2], &a1 = acc[(h + j) / 2 + 1];
+                        a0 = fma2(pack2(v[j], v[j + 1]), pack2(f.x, f.y), a0);
+                        a1 = fma2(pack2(v[j + 2], v[j + 3]), pack2(f.z, f.w), a1);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(acc_empty + 8 * b);
+            }
+            if (++b == NB) { b = 0; acc_phase ^= 1u; }
+            if (r == Cfg::CHUNK - 1 && more) {
+                // chunk c+1 goes where chunk c-1 was: every warp has left that one at the last barrier
+                store(c + 1);
+                named_barrier(1, E);
+            }
+        }
+        // every MMA has completed, so the ring is free: the sums, [token][weight row]
+        if (good) {
+            const int row = q * 32 + lane;
+#pragma unroll
+            for (int j = 0; j < Cfg::COLS; j += 2) {
+                const float2 f = unpack2(acc[j / 2]);
+                const uint32_t at = base + ((col0 + j) * Cfg::ROWS + row) * 4;
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(f.x) : "memory");
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + Cfg::ROWS * 4), "f"(f.y) : "memory");
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && ctrl[1]) {  // copies in flight end before the CTA does
+        const int issued = static_cast<int>(ctrl[2]);
+        for (int i = max(0, issued - S); i < issued; ++i)
+            if (!mbar_wait_for(full + 8 * (i % S), static_cast<uint32_t>((i / S) & 1), lim)) {
+                record_status(p.status, kSiteDrain);
+                break;
+            }
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
+    }
+    if (p.splits > 1) cluster_sync();  // every CTA's sums are in its shared memory
+
+    // this CTA's share of the tokens, 4 weight rows a thread
+    const int t0 = static_cast<int>(rank) * BT / p.splits, t1 = (static_cast<int>(rank) + 1) * BT / p.splits;
+    const int n_left = p.N - n0, m_left = p.M - m0;
+    for (int e = t0 * 32 + static_cast<int>(threadIdx.x); e < t1 * 32; e += Cfg::THREADS) {
+        const int j = e >> 5, n = (e & 31) * 4;
+        if (j >= m_left || n >= n_left) continue;
+        const uint32_t at = base + (j * Cfg::ROWS + n) * 4;
+        float4 f = p.splits > 1 ? ld_cluster_f4(mapa_shared(at, 0)) : ld_shared_f4(at);
+        for (int r = 1; r < p.splits; ++r) {
+            const float4 g = ld_cluster_f4(mapa_shared(at, static_cast<uint32_t>(r)));
+            f.x += g.x; f.y += g.y; f.z += g.z; f.w += g.w;
+        }
+        const int64_t to = static_cast<int64_t>(m0 + j) * p.ldc + n0 + n;  // N is a multiple of 8
+        if (p.c_dtype == SDT_DTYPE_F32) {
+            *reinterpret_cast<float4 *>(static_cast<float *>(p.C) + to) = f;
+        } else {
+            const uint4 h = pack8_f32(f, f, p.c_dtype == SDT_DTYPE_BF16);
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.C) + to) = make_uint2(h.x, h.y);
+        }
+    }
+    if (p.splits > 1) cluster_sync();  // nobody reads this CTA's shared memory any more
+}
+
+}  // namespace sdt

@@ -27,6 +27,7 @@
 #include "gemm_pair.cuh"
 #include "gemm_streamk.cuh"
 #include "host_common.cuh"
+#include "tensor_map.cuh"
 
 namespace sdt {
 
@@ -417,14 +418,13 @@ static std::mutex g_map_mu;
 static std::map<MapKey, CUtensorMap> g_maps;
 static uint64_t g_map_encodes = 0;
 
-// 2-D 16-bit tensor map (fp16 or bf16) with a box of `box_inner` contiguous elements
+// 2-D tensor map (fp16, bf16, fp8 or fp32) with a box of `box_inner` contiguous elements
 // by `box_outer` rows; `inner` is the contiguous dimension.  Operand maps use 64 x
 // rows boxes with the 128-byte swizzle: elements outside [0, inner) x [0, outer) read
 // as zero, which is what lets tiles overhang ragged edges.  The C map of the TMA
 // stores uses 32 x 32 boxes with the 64-byte swizzle: elements outside are not written.
-static int tensor_map_2d(const void *ptr, int dtype, uint64_t inner, uint64_t outer, uint64_t row_stride_bytes,
-                         int box_outer, CUtensorMap *out, int box_inner = 64,
-                         CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+int tensor_map_2d(const void *ptr, int dtype, uint64_t inner, uint64_t outer, uint64_t row_stride_bytes, int box_outer,
+                  CUtensorMap *out, int box_inner, CUtensorMapSwizzle swizzle) {
     const MapKey key = map_key(ptr, inner, outer, row_stride_bytes, dtype, box_outer, box_inner, int(swizzle));
     {
         std::lock_guard<std::mutex> lock(g_map_mu);
@@ -441,8 +441,10 @@ static int tensor_map_2d(const void *ptr, int dtype, uint64_t inner, uint64_t ou
     cuuint64_t strides[1] = {row_stride_bytes};
     cuuint32_t box[2] = {cuuint32_t(box_inner), cuuint32_t(box_outer)};
     cuuint32_t estr[2] = {1, 1};
-    const CUtensorMapDataType dt =
-        dtype == SDT_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const CUtensorMapDataType dt = dtype == SDT_DTYPE_BF16                               ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                   : dtype == SDT_DTYPE_E4M3 || dtype == SDT_DTYPE_E5M2 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : dtype == SDT_DTYPE_F32                             ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                                                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     CUresult r = fn(&m, dt, 2, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                     swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(SDT_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", int(r));
