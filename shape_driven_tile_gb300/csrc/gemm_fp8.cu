@@ -20,11 +20,15 @@ struct Fp8Plan {
 // `tile`: 0, or the tile that the caller asks for.
 static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int sm_count, int tile = 0) {
     Fp8Plan p;
+    p.splits = 1;
+    if (tile == 256 || (tile == 0 && M > 256)) {
+        p.tile = 256;
+        return p;
+    }
     p.tile = tile ? tile : M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
     const int64_t tiles = ((M + p.tile - 1) / p.tile) * ((N + 127) / 128), kb = (K + kFp8Block - 1) / kFp8Block;
     const int64_t slots = 2 * sm_count;
     double best = 0;
-    p.splits = 1;
     for (int s = 1; s <= kFp8MaxSplits && s <= kb; ++s) {
         // k-blocks one after another on a slot, each CTA's start and end counted as four
         const double t = double((tiles * s + slots - 1) / slots) * (double((kb + s - 1) / s) + 4.0);
@@ -47,7 +51,7 @@ static int check_fp8(const sdt_gemm_fp8 &c) {
     if (!is_fp8(c.a_dtype) || !is_fp8(c.w_dtype)) return fail(SDT_ERR_ARG, "gemm_fp8: A and W must be e4m3 or e5m2");
     if (c.c_dtype != SDT_DTYPE_F16 && c.c_dtype != SDT_DTYPE_BF16 && c.c_dtype != SDT_DTYPE_F32)
         return fail(SDT_ERR_ARG, "gemm_fp8: C must be fp16, bf16 or fp32 (dtype %d)", c.c_dtype);
-    if (c.tile != 0 && c.tile != 16 && c.tile != 32 && c.tile != 64 && c.tile != 128)
+    if (c.tile != 0 && c.tile != 16 && c.tile != 32 && c.tile != 64 && c.tile != 128 && c.tile != 256)
         return fail(SDT_ERR_TILE, "gemm_fp8: no tile %d", c.tile);
     if (c.splits < 0 || c.splits > kFp8MaxSplits) return fail(SDT_ERR_ARG, "gemm_fp8: splits must be in 0 .. %d", kFp8MaxSplits);
     if (c.M == 0 || c.N == 0) return SDT_OK;
@@ -83,6 +87,34 @@ static int run_swap(const sdt_gemm_fp8 &c, const Fp8Plan &plan, Fp8Args &a, int6
             : plan.tile == 32 ? launch_fp8_swap<32>(tmW, tmX, a, stream)
             : plan.tile == 64 ? launch_fp8_swap<64>(tmW, tmX, a, stream)
                               : launch_fp8_swap<128>(tmW, tmX, a, stream);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(SDT_ERR_LAUNCH, "gemm_fp8 launch failed: %s", cudaGetErrorString(cudaError_t(e)));
+    }
+    return SDT_OK;
+}
+
+static int run_pair(const sdt_gemm_fp8 &c, Fp8Args &a, int64_t lda, int64_t ldw, const DeviceInfo &dev, cudaStream_t stream) {
+    const int64_t tiles = ((c.M + 255) / 256) * ((c.N + 255) / 256);
+    if (tiles > INT32_MAX / 2) return fail(SDT_ERR_SHAPE, "gemm_fp8: grid too large");
+    a.num_m_tiles = int((c.M + 255) / 256);
+    a.num_n_tiles = int((c.N + 255) / 256);
+    a.splits = 1;
+    a.raster_group = 8;
+    const int pairs = std::max(1, dev.sm_count / 2);
+    // the tiles of a last round that leaves at least half of the pairs idle run as halves
+    const int left = int(tiles % pairs);
+    a.tail_start = int(tiles) - (2 * left <= pairs ? left : 0);
+    a.num_items = int(tiles) + (int(tiles) - a.tail_start);
+    a.idesc = (1u << 4) | ((c.a_dtype == SDT_DTYPE_E5M2 ? 1u : 0u) << 7) | ((c.w_dtype == SDT_DTYPE_E5M2 ? 1u : 0u) << 10);
+    CUtensorMap tmA, tmB, tmC;
+    int rc = tensor_map_2d(c.a, c.a_dtype, uint64_t(c.K), uint64_t(c.M), uint64_t(lda), 128, &tmA, kFp8Block);
+    if (!rc) rc = tensor_map_2d(c.w, c.w_dtype, uint64_t(c.K), uint64_t(c.N), uint64_t(ldw), 64, &tmB, kFp8Block);
+    // C leaves in boxes of 64-byte rows
+    const uint64_t size = c.c_dtype == SDT_DTYPE_F32 ? 4 : 2;
+    if (!rc) rc = tensor_map_2d(c.c, c.c_dtype, uint64_t(c.N), uint64_t(c.M), uint64_t(a.ldc) * size, 32, &tmC, int(64 / size), CU_TENSOR_MAP_SWIZZLE_64B);
+    if (rc) return rc;
+    const int e = launch_fp8_pair(tmA, tmB, tmC, a, std::min(pairs, a.num_items), stream);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return fail(SDT_ERR_LAUNCH, "gemm_fp8 launch failed: %s", cudaGetErrorString(cudaError_t(e)));
@@ -148,6 +180,7 @@ int gemm_fp8(const sdt_gemm_fp8 *call, sdt_stream_t stream_h) {
     Fp8Plan plan = fp8_plan(c.M, c.N, c.K, dev.sm_count, c.tile);
     if (c.splits) plan.splits = c.splits;
     plan.splits = std::min(plan.splits, a.num_kb);
+    if (plan.tile == 256) return run_pair(c, a, lda, ldw, dev, stream);
     return run_swap(c, plan, a, lda, ldw, stream);
 }
 

@@ -30,7 +30,9 @@ struct Fp8Args {
     int M, N, num_kb;        // num_kb: 128-deep blocks of k
     int num_m_tiles, num_n_tiles;
     int splits;              // CTAs of the cluster that share a tile's blocks (swapped form)
-    int raster_group;        // pair form: m-tiles per raster band
+    // two-CTA form: m-tiles per raster band; items [0, tail_start) are whole tiles, those from
+    // there to num_items halves of the tiles left for a partly empty round
+    int raster_group, tail_start, num_items;
     uint32_t idesc;          // types of the MMA's operands
     int c_dtype;
     unsigned long long timeout_ns;
@@ -57,26 +59,88 @@ __device__ __forceinline__ void umma_fp8_pair(uint32_t d_tmem, uint64_t a_desc, 
         : "memory");
 }
 
-// Two fp32 values in a 64-bit register: one instruction multiplies and adds both.
-__device__ __forceinline__ uint64_t pack2(float x, float y) {
-    uint64_t v;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
-    return v;
+// A bounded wait that reads the timer only after many failed polls: these kernels' roles wait for
+// one another every block, for a few hundred cycles.  RELAXED: what is waited for is that another
+// CTA's reads of tensor memory are over, no memory of its; an acquire at cluster scope would
+// refresh the SM's cache each time.
+template <bool RELAXED = false>
+__device__ __forceinline__ bool mbar_wait_soon(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+    const auto complete = [&] {
+        if (!RELAXED) return mbar_try_wait(bar, parity);
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        return ok != 0;
+    };
+#pragma unroll 1
+    for (int polls = 0; polls < 256; ++polls)
+        if (complete()) return true;
+    const uint64_t deadline = global_timer_ns() + limit_ns;
+    uint32_t polls = 0;
+    while (!complete())
+        if ((++polls & 63u) == 0 && global_timer_ns() > deadline) return false;
+    return true;
 }
-__device__ __forceinline__ uint64_t pack2(uint32_t x, uint32_t y) {
-    uint64_t v;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(x), "r"(y));
-    return v;
+
+// The same for a whole warp, which leaves it converged.
+template <bool RELAXED = false>
+__device__ __forceinline__ bool warp_wait_soon(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+    return __all_sync(0xffffffffu, mbar_wait_soon<RELAXED>(bar, parity, limit_ns));
 }
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-    float2 f;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-    return f;
+
+// Whether the phase is complete, without waiting.  Even a wait for a complete phase takes some 150
+// cycles, so every role asks for its next barrier before it works on the present one, and waits
+// only if the answer was no.
+template <bool RELAXED = false>
+__device__ __forceinline__ bool mbar_peek(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    if (RELAXED)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    return ok != 0;
 }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
+// After a peek: true at once if it saw the phase complete, otherwise a bounded wait.  Whole warp.
+template <bool RELAXED = false>
+__device__ __forceinline__ bool warp_wait_peeked(bool peeked, uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+    return __all_sync(0xffffffffu, peeked) || warp_wait_soon<RELAXED>(bar, parity, limit_ns);
+}
+
+// One lane of a converged warp.  A warp that issues copies or MMAs runs its loop as a whole and
+// elects a lane for the instructions alone: addresses and descriptors then stay in uniform
+// registers, which these instructions take them from.  (As one lane's own loop, a block's four
+// MMAs and their barriers took 650 cycles, its two or three copies 600.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok));
+    return ok != 0;
+}
+
+// Hint: bring a box into L2.
+__device__ __forceinline__ void tma_prefetch_l2_2d(const CUtensorMap *map, int32_t x, int32_t y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y)
+                 : "memory");
 }
 
 __device__ __forceinline__ void named_barrier(int id, int threads) {

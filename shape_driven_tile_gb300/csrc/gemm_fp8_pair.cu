@@ -1,0 +1,18 @@
+// The two-CTA form of gemm_fp8.
+#include "gemm_fp8_pair.cuh"
+
+#include "gemm_fp8_launch.cuh"
+#include "gemm_launch.cuh"
+
+namespace sdt {
+
+int launch_fp8_pair(const CUtensorMap &tmA, const CUtensorMap &tmB, const CUtensorMap &tmC, const Fp8Args &args, int pairs,
+                    cudaStream_t stream) {
+    using Cfg = Fp8PairCfg;
+    static std::atomic<int> configured[64];
+    if (int e = ensure_smem(gemm_fp8_pair_kernel, Cfg::SMEM_BYTES, configured)) return e;
+    return launch_kernel(gemm_fp8_pair_kernel, dim3(2 * static_cast<unsigned>(pairs)), dim3(Cfg::THREADS), size_t(Cfg::SMEM_BYTES),
+                         stream, 2, tmA, tmB, tmC, args);
+}
+
+}  // namespace sdt

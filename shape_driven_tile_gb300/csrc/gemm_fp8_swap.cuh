@@ -26,7 +26,7 @@ namespace sdt {
 template <int BT>
 struct SwapCfg {
     static constexpr int ROWS = 128;  // weight rows per tile
-    static constexpr int EPI_WARPS = BT == 128 ? 8 : 4;
+    static constexpr int EPI_WARPS = BT == 16 ? 4 : 8;
     static constexpr int COLS = BT * 4 / EPI_WARPS;  // tokens per epilogue warp
     static constexpr int THREADS = 64 + 32 * EPI_WARPS;
     static constexpr int W_BYTES = ROWS * kFp8Block;
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(SwapCfg<BT>::THREADS, 2)
     volatile uint32_t *ctrl = reinterpret_cast<volatile uint32_t *>(smem_raw + (acc_empty + 8 * NB - smem_u32(smem_raw)));
     // ctrl[0]: TMEM base   ctrl[1]: a role gave up   ctrl[2]: blocks the producer asked for
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t rank = p.splits > 1 ? cluster_ctarank() : 0;
     const int tile = static_cast<int>(blockIdx.x) / p.splits;
     // tokens fastest: CTAs that run together share weights through L2
@@ -108,45 +108,60 @@ __global__ void __launch_bounds__(SwapCfg<BT>::THREADS, 2)
     tc_fence_after();
     const uint32_t tmem_base = ctrl[0];
     griddep_launch_dependents();
+    // while the kernel before this one still runs, L2 may fetch this CTA's first weights (what L2
+    // holds is never stale); nothing else is read yet
+    if (warp == 0 && lane < min(S, nkb)) tma_prefetch_l2_2d(&tmW, (kb0 + lane) * kFp8Block, n0);
     griddep_wait();
 
-    uint64_t acc[Cfg::COLS / 2];
+    float acc[Cfg::COLS];
 #pragma unroll
-    for (int j = 0; j < Cfg::COLS / 2; ++j) acc[j] = 0;
+    for (int j = 0; j < Cfg::COLS; ++j) acc[j] = 0.f;
     bool good = true;
 
     if (warp == 0) {
-        if (lane == 0) {
-            int s = 0, issued = 0;
-            uint32_t phase = 0;
-            for (int i = 0; i < nkb; ++i) {
-                if (!mbar_wait_for(empty + 8 * s, phase ^ 1u, lim)) {
-                    record_status(p.status, kSiteProducer | (i << 8));
-                    ctrl[1] = 1;
-                    break;
-                }
-                if (ctrl[1]) break;
+        int s = 0, issued = 0;
+        uint32_t phase = 0;
+        bool ready = true;  // the ring's slots are free at first
+        for (int i = 0; i < nkb; ++i) {
+            if (!warp_wait_peeked(ready, empty + 8 * s, phase ^ 1u, lim)) {
+                if (lane == 0) record_status(p.status, kSiteProducer | (i << 8));
+                ctrl[1] = 1;
+                break;
+            }
+            if (i >= S && ctrl[1]) break;
+            const int s_next = s + 1 == S ? 0 : s + 1;
+            const uint32_t phase_next = s + 1 == S ? phase ^ 1u : phase;
+            if (i + 1 >= S) ready = mbar_peek(empty + 8 * s_next, phase_next ^ 1u);
+            if (elect_one()) {
                 mbar_arrive_expect_tx(full + 8 * s, Cfg::STAGE_BYTES);
                 tma_load_2d(smW + s * Cfg::W_BYTES, &tmW, full + 8 * s, (kb0 + i) * kFp8Block, n0);
                 tma_load_2d(smX + s * Cfg::X_BYTES, &tmX, full + 8 * s, (kb0 + i) * kFp8Block, m0);
-                ++issued;
-                if (++s == S) { s = 0; phase ^= 1u; }
             }
-            ctrl[2] = issued;
+            __syncwarp();
+            ++issued;
+            s = s_next;
+            phase = phase_next;
         }
+        ctrl[2] = issued;
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = idesc_for(p.idesc, Cfg::ROWS, BT);
-            const uint64_t w0 = smem_desc_sw128(smW, 16, 1024), x0 = smem_desc_sw128(smX, 16, 1024);
-            int s = 0, b = 0;
-            uint32_t phase = 0, acc_phase = 0;
-            for (int i = 0; i < nkb; ++i) {
-                if (!mbar_wait_for(acc_empty + 8 * b, acc_phase ^ 1u, lim) || !mbar_wait_for(full + 8 * s, phase, lim)) {
-                    record_status(p.status, kSiteMma | (i << 8));
-                    ctrl[1] = 1;
-                    break;
-                }
-                tc_fence_after();
+        const uint32_t idesc = idesc_for(p.idesc, Cfg::ROWS, BT);
+        const uint64_t w0 = smem_desc_sw128(smW, 16, 1024), x0 = smem_desc_sw128(smX, 16, 1024);
+        int s = 0, b = 0;
+        uint32_t phase = 0, acc_phase = 0;
+        bool loaded = false, empty_acc = true;
+        for (int i = 0; i < nkb; ++i) {
+            if (!warp_wait_peeked(empty_acc, acc_empty + 8 * b, acc_phase ^ 1u, lim) ||
+                !warp_wait_peeked(loaded, full + 8 * s, phase, lim)) {
+                if (lane == 0) record_status(p.status, kSiteMma | (i << 8));
+                ctrl[1] = 1;
+                break;
+            }
+            tc_fence_after();
+            const int s_next = s + 1 == S ? 0 : s + 1, b_next = b + 1 == NB ? 0 : b + 1;
+            const uint32_t phase_next = s + 1 == S ? phase ^ 1u : phase, acc_phase_next = b + 1 == NB ? acc_phase ^ 1u : acc_phase;
+            loaded = mbar_peek(full + 8 * s_next, phase_next);
+            if (i + 1 >= NB) empty_acc = mbar_peek(acc_empty + 8 * b_next, acc_phase_next ^ 1u);
+            if (elect_one()) {
                 const uint64_t wd = w0 + static_cast<uint64_t>(s) * (Cfg::W_BYTES >> 4);
                 const uint64_t xd = x0 + static_cast<uint64_t>(s) * (Cfg::X_BYTES >> 4);
 #pragma unroll
@@ -154,11 +169,13 @@ __global__ void __launch_bounds__(SwapCfg<BT>::THREADS, 2)
                     umma_fp8(tmem_base + b * BT, wd + 2 * kk, xd + 2 * kk, idesc, kk > 0);
                 umma_commit(empty + 8 * s);
                 umma_commit(acc_full + 8 * b);
-                if (++s == S) { s = 0; phase ^= 1u; }
-                if (++b == NB) { b = 0; acc_phase ^= 1u; }
             }
+            __syncwarp();
+            s = s_next;
+            b = b_next;
+            phase = phase_next;
+            acc_phase = acc_phase_next;
         }
-        __syncwarp();
     } else {
         const int q = warp & 3;                                   // TMEM lane quarter
         const int col0 = Cfg::EPI_WARPS == 8 ? ((warp - 2) >> 2) * Cfg::COLS : 0;
@@ -195,12 +212,13 @@ __global__ void __launch_bounds__(SwapCfg<BT>::THREADS, 2)
         named_barrier(1, E);
         int b = 0;
         uint32_t acc_phase = 0;
+        bool done = false;
         const uint32_t taddr0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + col0;
         for (int i = 0; i < nkb; ++i) {
             const int c = i / Cfg::CHUNK, r = i % Cfg::CHUNK;
             const bool more = (c + 1) * Cfg::CHUNK < nkb;
             if (r == 0 && more) fetch(c + 1);
-            if (good && !warp_wait(acc_full + 8 * b, acc_phase, 4 * lim, lane)) {
+            if (good && !warp_wait_peeked(done, acc_full + 8 * b, acc_phase, 4 * lim)) {
                 if (lane == 0) {
                     record_status(p.status, kSiteEpilogue | (i << 8));
                     ctrl[1] = 1;
@@ -211,21 +229,36 @@ __global__ void __launch_bounds__(SwapCfg<BT>::THREADS, 2)
                 tc_fence_after();
                 const uint32_t sc = smS + (c & 1) * Cfg::SCALE_BYTES + (r * BT + col0) * 4;
 #pragma unroll
-                for (int h = 0; h < Cfg::COLS; h += 16) {
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x16(taddr0 + b * BT + h, v);
-                    tmem_ld_wait();
+                for (int h = 0; h < Cfg::COLS; h += 32) {
+                    // up to 32 columns on their way while the scales of the first 16 come from shared memory
+                    uint32_t v[2][32];
+                    constexpr int parts = Cfg::COLS >= 32 ? 2 : 1;
+                    tmem_ld_32x32b_x16(taddr0 + b * BT + h, v[0]);
+                    if (parts == 2) tmem_ld_32x32b_x16(taddr0 + b * BT + h + 16, v[1]);
 #pragma unroll
-                    for (int j = 0; j < 16; j += 4) {
-                        const float4 f = ld_shared_f4(sc + (h + j) * 4);
-                        uint64_t &a0 = acc[(h + j) / 2], &a1 = acc[(h + j) / 2 + 1];
-                        a0 = fma2(pack2(v[j], v[j + 1]), pack2(f.x, f.y), a0);
-                        a1 = fma2(pack2(v[j + 2], v[j + 3]), pack2(f.z, f.w), a1);
+                    for (int g = 0; g < parts; ++g) {
+                        float4 f[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) f[j] = ld_shared_f4(sc + (h + 16 * g + 4 * j) * 4);
+                        if (g == 0) {
+                            tmem_ld_wait();
+                            if (h + 16 * parts >= Cfg::COLS) {  // every column has been read
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(acc_empty + 8 * b);
+                                done = mbar_peek(acc_full + 8 * (b + 1 == NB ? 0 : b + 1), b + 1 == NB ? acc_phase ^ 1u : acc_phase);
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            float *to = acc + h + 16 * g + 4 * j;
+                            to[0] = fmaf(__uint_as_float(v[g][4 * j]), f[j].x, to[0]);
+                            to[1] = fmaf(__uint_as_float(v[g][4 * j + 1]), f[j].y, to[1]);
+                            to[2] = fmaf(__uint_as_float(v[g][4 * j + 2]), f[j].z, to[2]);
+                            to[3] = fmaf(__uint_as_float(v[g][4 * j + 3]), f[j].w, to[3]);
+                        }
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(acc_empty + 8 * b);
             }
             if (++b == NB) { b = 0; acc_phase ^= 1u; }
             if (r == Cfg::CHUNK - 1 && more) {
@@ -238,12 +271,8 @@ __global__ void __launch_bounds__(SwapCfg<BT>::THREADS, 2)
         if (good) {
             const int row = q * 32 + lane;
 #pragma unroll
-            for (int j = 0; j < Cfg::COLS; j += 2) {
-                const float2 f = unpack2(acc[j / 2]);
-                const uint32_t at = base + ((col0 + j) * Cfg::ROWS + row) * 4;
-                asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(f.x) : "memory");
-                asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + Cfg::ROWS * 4), "f"(f.y) : "memory");
-            }
+            for (int j = 0; j < Cfg::COLS; ++j)
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((col0 + j) * Cfg::ROWS + row) * 4), "f"(acc[j]) : "memory");
         }
     }
 

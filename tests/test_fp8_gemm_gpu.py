@@ -6,7 +6,7 @@ import shape_driven_tile_gb300 as sdt
 from _fp8 import E4M3, E5M2, assert_near, fp8_values, product, scale_values
 
 pytestmark = pytest.mark.gpu
-TILES = [16, 32, 64, 128]
+TILES = [16, 32, 64, 128, 256]
 
 
 def operands(m, n, k, seed=0, at=E4M3, wt=E4M3):
@@ -25,7 +25,7 @@ def check(a, sa, w, sw, out=None, **kw):
 
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float16, torch.float32])
 @pytest.mark.parametrize("m,n,k", [(1, 8, 16), (1, 128, 128), (3, 136, 144), (16, 256, 1024), (17, 248, 2000), (33, 1000, 640),
-                                   (65, 128, 4112), (128, 384, 256), (129, 520, 1296), (300, 264, 400), (1000, 136, 272)])
+                                   (65, 128, 4112), (128, 384, 256), (129, 520, 1296), (300, 264, 400), (1000, 136, 272), (513, 2056, 1040)])
 def test_sizes(cuda_device, m, n, k, out):
     check(*operands(m, n, k), out_dtype=out)
 
