@@ -25,7 +25,7 @@ static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int sm_count, int tile 
         p.tile = 256;
         return p;
     }
-    p.tile = tile ? tile : M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    p.tile = tile ? tile : M <= 16 ? 16 : M <= 32 ? 32 : 64;
     const int64_t tiles = ((M + p.tile - 1) / p.tile) * ((N + 127) / 128), kb = (K + kFp8Block - 1) / kFp8Block;
     const int64_t slots = 2 * sm_count;
     double best = 0;
@@ -51,7 +51,7 @@ static int check_fp8(const sdt_gemm_fp8 &c) {
     if (!is_fp8(c.a_dtype) || !is_fp8(c.w_dtype)) return fail(SDT_ERR_ARG, "gemm_fp8: A and W must be e4m3 or e5m2");
     if (c.c_dtype != SDT_DTYPE_F16 && c.c_dtype != SDT_DTYPE_BF16 && c.c_dtype != SDT_DTYPE_F32)
         return fail(SDT_ERR_ARG, "gemm_fp8: C must be fp16, bf16 or fp32 (dtype %d)", c.c_dtype);
-    if (c.tile != 0 && c.tile != 16 && c.tile != 32 && c.tile != 64 && c.tile != 128 && c.tile != 256)
+    if (c.tile != 0 && c.tile != 16 && c.tile != 32 && c.tile != 64 && c.tile != 256)
         return fail(SDT_ERR_TILE, "gemm_fp8: no tile %d", c.tile);
     if (c.splits < 0 || c.splits > kFp8MaxSplits) return fail(SDT_ERR_ARG, "gemm_fp8: splits must be in 0 .. %d", kFp8MaxSplits);
     if (c.M == 0 || c.N == 0) return SDT_OK;
@@ -85,8 +85,7 @@ static int run_swap(const sdt_gemm_fp8 &c, const Fp8Plan &plan, Fp8Args &a, int6
     if (rc) return rc;
     int e = plan.tile == 16   ? launch_fp8_swap<16>(tmW, tmX, a, stream)
             : plan.tile == 32 ? launch_fp8_swap<32>(tmW, tmX, a, stream)
-            : plan.tile == 64 ? launch_fp8_swap<64>(tmW, tmX, a, stream)
-                              : launch_fp8_swap<128>(tmW, tmX, a, stream);
+                              : launch_fp8_swap<64>(tmW, tmX, a, stream);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return fail(SDT_ERR_LAUNCH, "gemm_fp8 launch failed: %s", cudaGetErrorString(cudaError_t(e)));

@@ -2,16 +2,18 @@
 // tile's k-blocks shared by a cluster of CTAs.
 //
 // The product runs as W . A^T, so that the many weight rows fill the MMA's 128 rows and BT
-// (16, 32, 64 or 128) tokens its columns: a weight byte is read from memory once for up to BT
+// (16, 32 or 64) tokens its columns: a weight byte is read from memory once for up to BT
 // tokens, and a single token costs what the weights' bytes cost.  The accumulator's lane is a
 // weight row and its column a token: the weight scale is the tile's, the token scales come from
 // shared memory as four at a time.
 //
 // What bounds it at few tokens is the stream of weights, so the work is cut to fill the GPU:
-// the CTAs of a cluster take consecutive ranges of the k-blocks of one tile, hold their sums in
-// registers, write them to their own shared memory at the end, and each adds up a share of the
-// tile's values from all of them through distributed shared memory, in rank order (results do
-// not depend on timing) and without a workspace.
+// the CTAs of a cluster take consecutive ranges of the k-blocks of one tile and hold their sums
+// in registers.  At the end each token belongs to one of them, and the others store their sums of
+// it into a buffer of that CTA's shared memory that nothing else uses, so one meeting of the
+// cluster is enough; they are added in rank order (results do not depend on timing), without a
+// workspace.  (Sums left in place and read by the owner took a second meeting and eight dependent
+// reads from other SMs: 2 us of a 5 us call.)
 //
 // Tensor memory is freed before the cluster meets: no CTA holds any while it waits for another
 // one, so kernels of several streams cannot block each other over it.
@@ -32,26 +34,24 @@ struct SwapCfg {
     static constexpr int W_BYTES = ROWS * kFp8Block;
     static constexpr int X_BYTES = BT * kFp8Block;
     static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
-    static constexpr int ACC_BUFS = BT == 128 ? 2 : 4;
+    static constexpr int ACC_BUFS = 4;
     static constexpr int TMEM_COLS = ACC_BUFS * BT;  // 64 .. 256: two CTAs of an SM always fit
-    static constexpr int STAGES = BT == 16 ? 5 : BT == 32 ? 5 : BT == 64 ? 4 : 3;
-    static constexpr int CHUNK = BT == 128 ? 8 : 512 / BT;  // k-blocks whose scales are in shared memory at a time
+    static constexpr int STAGES = BT == 16 ? 5 : BT == 32 ? 4 : 3;
+    static constexpr int CHUNK = 512 / BT;  // k-blocks whose scales are in shared memory at a time
     static constexpr int SCALE_BYTES = CHUNK * BT * 4;
     static constexpr int PER_THREAD = CHUNK * BT / (32 * EPI_WARPS);  // scales each epilogue thread brings
+    // rows of 128 sums that a CTA receives: S shares of at most ceil(BT / S) tokens, S <= 8
+    static constexpr int SUM_ROWS = BT == 16 ? 21 : BT == 32 ? 36 : 70;
+    static constexpr int SUM_BYTES = SUM_ROWS * ROWS * 4;
     static constexpr int CTRL_BYTES = 512;
-    static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 2 * SCALE_BYTES + CTRL_BYTES;
-    static_assert(BT == 16 || BT == 32 || BT == 64 || BT == 128, "tokens per tile");
-    static_assert(STAGES * STAGE_BYTES >= ROWS * BT * 4, "the sums reuse the ring");
+    static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 2 * SCALE_BYTES + SUM_BYTES + CTRL_BYTES;
+    static_assert(BT == 16 || BT == 32 || BT == 64, "tokens per tile");
     static_assert(SMEM_BYTES <= 115712, "two CTAs share an SM");
 };
 
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
+// One value to the same place of another CTA's shared memory.
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
@@ -70,7 +70,8 @@ __global__ void __launch_bounds__(SwapCfg<BT>::THREADS, 2)
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t smW = base, smX = base + S * Cfg::W_BYTES;
     const uint32_t smS = base + S * Cfg::STAGE_BYTES;  // two chunks of scales
-    const uint32_t bars = smS + 2 * Cfg::SCALE_BYTES;
+    const uint32_t smR = smS + 2 * Cfg::SCALE_BYTES;   // sums from the cluster's CTAs: [CTA][token of this one's share][row]
+    const uint32_t bars = smR + Cfg::SUM_BYTES;
     const uint32_t full = bars, empty = bars + 8 * S, acc_full = bars + 16 * S, acc_empty = acc_full + 8 * NB;
     volatile uint32_t *ctrl = reinterpret_cast<volatile uint32_t *>(smem_raw + (acc_empty + 8 * NB - smem_u32(smem_raw)));
     // ctrl[0]: TMEM base   ctrl[1]: a role gave up   ctrl[2]: blocks the producer asked for
@@ -84,6 +85,7 @@ __global__ void __launch_bounds__(SwapCfg<BT>::THREADS, 2)
     const int kb0 = static_cast<int>(static_cast<int64_t>(rank) * p.num_kb / p.splits);
     const int kb1 = static_cast<int>(static_cast<int64_t>(rank + 1) * p.num_kb / p.splits);
     const int nkb = kb1 - kb0;
+    const int tokens = min(BT, p.M - m0), share = (tokens + p.splits - 1) / p.splits;  // of this tile, of a CTA in the end
     const uint64_t lim = p.timeout_ns;
 
     if (threadIdx.x == 0) {
@@ -107,6 +109,7 @@ __global__ void __launch_bounds__(SwapCfg<BT>::THREADS, 2)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = ctrl[0];
+    if (p.splits > 1) cluster_arrive_relaxed();  // "this CTA has started"
     griddep_launch_dependents();
     // while the kernel before this one still runs, L2 may fetch this CTA's first weights (what L2
     // holds is never stale); nothing else is read yet
@@ -180,8 +183,9 @@ __global__ void __launch_bounds__(SwapCfg<BT>::THREADS, 2)
         const int q = warp & 3;                                   // TMEM lane quarter
         const int col0 = Cfg::EPI_WARPS == 8 ? ((warp - 2) >> 2) * Cfg::COLS : 0;
         const int t = static_cast<int>(threadIdx.x) - 64;
-        // scales of chunk c, weight and token scale multiplied: [block][token]
-        float mine[Cfg::PER_THREAD];
+        // scales of chunk c, weight and token scale multiplied (on their way into shared memory, when
+        // the loads have long arrived): [block][token]
+        float token[Cfg::PER_THREAD], weight[Cfg::PER_THREAD];
         const bool by_token = p.as_row == 1;  // neighbouring threads take neighbouring values
         auto place = [&](int u, int &kb, int &j) {
             const int e = u * E + t;
@@ -194,9 +198,9 @@ __global__ void __launch_bounds__(SwapCfg<BT>::THREADS, 2)
                 int kb, j;
                 place(u, kb, j);
                 kb += kb0 + c * Cfg::CHUNK;
-                mine[u] = 0.f;
-                if (kb < kb1 && m0 + j < p.M)
-                    mine[u] = p.a_scales[(m0 + j) * p.as_row + kb * p.as_block] * p.w_scales[n_tile * p.ws_row + kb * p.ws_block];
+                const bool in = kb < kb1 && m0 + j < p.M;
+                token[u] = in ? p.a_scales[(m0 + j) * p.as_row + kb * p.as_block] : 0.f;
+                weight[u] = in ? p.w_scales[n_tile * p.ws_row + kb * p.ws_block] : 0.f;
             }
         };
         auto store = [&](int c) {
@@ -204,7 +208,7 @@ __global__ void __launch_bounds__(SwapCfg<BT>::THREADS, 2)
             for (int u = 0; u < Cfg::PER_THREAD; ++u) {
                 int kb, j;
                 place(u, kb, j);
-                asm volatile("st.shared.f32 [%0], %1;" ::"r"(smS + (c & 1) * Cfg::SCALE_BYTES + (kb * BT + j) * 4), "f"(mine[u]) : "memory");
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(smS + (c & 1) * Cfg::SCALE_BYTES + (kb * BT + j) * 4), "f"(token[u] * weight[u]) : "memory");
             }
         };
         fetch(0);
@@ -267,14 +271,22 @@ __global__ void __launch_bounds__(SwapCfg<BT>::THREADS, 2)
                 named_barrier(1, E);
             }
         }
-        // every MMA has completed, so the ring is free: the sums, [token][weight row]
+        // each token's sums to the CTA that adds them up
+        if (p.splits > 1) cluster_wait();
         if (good) {
-            const int row = q * 32 + lane;
+            const uint32_t to = smR + rank * static_cast<uint32_t>(share * Cfg::ROWS * 4) + (q * 32 + lane) * 4;
+            int owner = col0 / share, at = col0 - owner * share;
 #pragma unroll
-            for (int j = 0; j < Cfg::COLS; ++j)
-                asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((col0 + j) * Cfg::ROWS + row) * 4), "f"(acc[j]) : "memory");
+            for (int j = 0; j < Cfg::COLS; ++j) {
+                if (col0 + j < tokens) {
+                    const uint32_t here = to + at * (Cfg::ROWS * 4);
+                    st_cluster_f32(p.splits > 1 ? mapa_shared(here, static_cast<uint32_t>(owner)) : here, acc[j]);
+                    if (++at == share) { at = 0; ++owner; }
+                }
+            }
         }
     }
+    if (warp < 2 && p.splits > 1) cluster_wait();
 
     tc_fence_before();
     __syncthreads();
@@ -290,21 +302,19 @@ __global__ void __launch_bounds__(SwapCfg<BT>::THREADS, 2)
         tc_fence_after();
         tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
     }
-    if (p.splits > 1) cluster_sync();  // every CTA's sums are in its shared memory
+    if (p.splits > 1) cluster_sync();  // every CTA's sums are where they are added
 
-    // this CTA's share of the tokens, 4 weight rows a thread
-    const int t0 = static_cast<int>(rank) * BT / p.splits, t1 = (static_cast<int>(rank) + 1) * BT / p.splits;
-    const int n_left = p.N - n0, m_left = p.M - m0;
-    for (int e = t0 * 32 + static_cast<int>(threadIdx.x); e < t1 * 32; e += Cfg::THREADS) {
+    // this CTA's share of the tokens, in rank order, 4 weight rows a thread
+    const int first = static_cast<int>(rank) * share, count = min(share, tokens - first);
+    for (int e = static_cast<int>(threadIdx.x); e < count * 32; e += Cfg::THREADS) {
         const int j = e >> 5, n = (e & 31) * 4;
-        if (j >= m_left || n >= n_left) continue;
-        const uint32_t at = base + (j * Cfg::ROWS + n) * 4;
-        float4 f = p.splits > 1 ? ld_cluster_f4(mapa_shared(at, 0)) : ld_shared_f4(at);
+        if (n0 + n >= p.N) continue;
+        float4 f = ld_shared_f4(smR + (j * Cfg::ROWS + n) * 4);
         for (int r = 1; r < p.splits; ++r) {
-            const float4 g = ld_cluster_f4(mapa_shared(at, static_cast<uint32_t>(r)));
+            const float4 g = ld_shared_f4(smR + ((r * share + j) * Cfg::ROWS + n) * 4);
             f.x += g.x; f.y += g.y; f.z += g.z; f.w += g.w;
         }
-        const int64_t to = static_cast<int64_t>(m0 + j) * p.ldc + n0 + n;  // N is a multiple of 8
+        const int64_t to = static_cast<int64_t>(m0 + first + j) * p.ldc + n0 + n;  // N is a multiple of 8
         if (p.c_dtype == SDT_DTYPE_F32) {
             *reinterpret_cast<float4 *>(static_cast<float *>(p.C) + to) = f;
         } else {
@@ -312,7 +322,6 @@ __global__ void __launch_bounds__(SwapCfg<BT>::THREADS, 2)
             *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.C) + to) = make_uint2(h.x, h.y);
         }
     }
-    if (p.splits > 1) cluster_sync();  // nobody reads this CTA's shared memory any more
 }
 
 }  // namespace sdt

@@ -150,4 +150,4 @@ def test_frequencies_of_the_scalings():
 @pytest.mark.parametrize("n,k", [(8, 16), (4096, 14336), (12288, 4096), (248, 2000), (28672, 8192)])
 def test_plans(m, n, k):
     tile, splits = sdt.gemm_fp8_plan(m, n, k)
-    assert 1 <= splits <= min(8, -(-k // 128)) and (tile >= min(m, 128) or m > 128)
+    assert 1 <= splits <= min(8, -(-k // 128)) and (tile >= min(m, 64) or m > 64)
