@@ -17,24 +17,48 @@ struct Fp8Plan {
     int tile, splits;
 };
 
+// The items of the two-CTA tiles: whole tiles up to tail_start, then, if the last round would leave
+// at least half of the pairs idle, its tiles as two halves each.
+struct Fp8PairItems {
+    int64_t tail_start, num_items, pairs;
+};
+static Fp8PairItems fp8_pair_items(int64_t M, int64_t N, int sm_count) {
+    const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256), pairs = std::max(1, sm_count / 2), left = tiles % pairs;
+    const int64_t whole = 2 * left <= pairs ? tiles - left : tiles;
+    return {whole, whole + 2 * (tiles - whole), pairs};
+}
+
+// Swapped tiles run with as many CTAs per tile as still run at once, two to an SM.  kResident is the
+// share of the 2 x SMs places that clusters of 1 .. 8 CTAs can take (GPCs hold whole clusters only;
+// measured on 152 SMs).  A second round costs more than the split gains: 64 x 6144 x 4096 takes
+// 8.4 us in 48 clusters of 4 and 13.2 us in 48 of 6, of which 46 fit; 1 x 28672 x 8192 takes 37 us
+// unsplit and 42 split in 4.
+//
+// Two-CTA tiles take over where the estimates say so, microseconds fitted to measured shapes: a
+// swapped tile's CTA takes 0.55 a block beside another one, a two-CTA tile 0.44 a block, or 0.30 as
+// two half-width items.  Measured, swapped against two-CTA: 200 x 4096 x 4096 12.7 and 12.8,
+// 256 x 8192 x 4096 19.9 and 14.8, 333 x 5000 x 4208 22.8 and 18.5, 512 x 4096 x 4096 19.6 and 13.7;
+// 128 x 4096 x 14336, whose 16 two-CTA tiles would sum 112 blocks each, 18.7 and over 25.  Up to 64
+// tokens the two-CTA tile's rows are three quarters empty: swapped.
 // `tile`: 0, or the tile that the caller asks for.
 static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int sm_count, int tile = 0) {
+    constexpr double kResident[kFp8MaxSplits] = {1.0, 1.0, 0.908, 0.947, 0.921, 0.908, 0.691, 0.789};
+    const int64_t kb = (K + kFp8Block - 1) / kFp8Block;
     Fp8Plan p;
     p.splits = 1;
-    if (tile == 256 || (tile == 0 && M > 256)) {
-        p.tile = 256;
-        return p;
-    }
     p.tile = tile ? tile : M <= 16 ? 16 : M <= 32 ? 32 : 64;
-    const int64_t tiles = ((M + p.tile - 1) / p.tile) * ((N + 127) / 128), kb = (K + kFp8Block - 1) / kFp8Block;
-    const int64_t slots = 2 * sm_count;
-    double best = 0;
-    for (int s = 1; s <= kFp8MaxSplits && s <= kb; ++s) {
-        // k-blocks one after another on a slot, each CTA's start and end counted as four
-        const double t = double((tiles * s + slots - 1) / slots) * (double((kb + s - 1) / s) + 4.0);
-        if (s == 1 || t < best) {
-            best = t;
-            p.splits = s;
+    if (p.tile == 256) return p;
+    const int64_t tiles = ((M + p.tile - 1) / p.tile) * ((N + 127) / 128);
+    for (int s = 2; s <= kFp8MaxSplits && 2 * s <= kb; ++s)  // (two blocks a CTA at least)
+        if (double(tiles) * s <= kResident[s - 1] * 2 * sm_count) p.splits = s;
+    if (tile == 0 && M > 64) {
+        const Fp8PairItems items = fp8_pair_items(M, N, sm_count);
+        const double rounds = double(tiles) * p.splits / (2 * sm_count);
+        const double swapped = 3.5 + 0.55 * double((kb + p.splits - 1) / p.splits) * std::max(1.0, rounds);
+        const double paired = 4.0 + double(kb) * (0.44 * double((items.tail_start + items.pairs - 1) / items.pairs) + (items.num_items > items.tail_start ? 0.30 : 0.0));
+        if (paired < swapped) {
+            p.tile = 256;
+            p.splits = 1;
         }
     }
     return p;
@@ -94,17 +118,14 @@ static int run_swap(const sdt_gemm_fp8 &c, const Fp8Plan &plan, Fp8Args &a, int6
 }
 
 static int run_pair(const sdt_gemm_fp8 &c, Fp8Args &a, int64_t lda, int64_t ldw, const DeviceInfo &dev, cudaStream_t stream) {
-    const int64_t tiles = ((c.M + 255) / 256) * ((c.N + 255) / 256);
-    if (tiles > INT32_MAX / 2) return fail(SDT_ERR_SHAPE, "gemm_fp8: grid too large");
+    const Fp8PairItems items = fp8_pair_items(c.M, c.N, dev.sm_count);
+    if (items.num_items > INT32_MAX / 2) return fail(SDT_ERR_SHAPE, "gemm_fp8: grid too large");
     a.num_m_tiles = int((c.M + 255) / 256);
     a.num_n_tiles = int((c.N + 255) / 256);
     a.splits = 1;
     a.raster_group = 8;
-    const int pairs = std::max(1, dev.sm_count / 2);
-    // the tiles of a last round that leaves at least half of the pairs idle run as halves
-    const int left = int(tiles % pairs);
-    a.tail_start = int(tiles) - (2 * left <= pairs ? left : 0);
-    a.num_items = int(tiles) + (int(tiles) - a.tail_start);
+    a.tail_start = int(items.tail_start);
+    a.num_items = int(items.num_items);
     a.idesc = (1u << 4) | ((c.a_dtype == SDT_DTYPE_E5M2 ? 1u : 0u) << 7) | ((c.w_dtype == SDT_DTYPE_E5M2 ? 1u : 0u) << 10);
     CUtensorMap tmA, tmB, tmC;
     int rc = tensor_map_2d(c.a, c.a_dtype, uint64_t(c.K), uint64_t(c.M), uint64_t(lda), 128, &tmA, kFp8Block);
@@ -113,7 +134,7 @@ static int run_pair(const sdt_gemm_fp8 &c, Fp8Args &a, int64_t lda, int64_t ldw,
     const uint64_t size = c.c_dtype == SDT_DTYPE_F32 ? 4 : 2;
     if (!rc) rc = tensor_map_2d(c.c, c.c_dtype, uint64_t(c.N), uint64_t(c.M), uint64_t(a.ldc) * size, 32, &tmC, int(64 / size), CU_TENSOR_MAP_SWIZZLE_64B);
     if (rc) return rc;
-    const int e = launch_fp8_pair(tmA, tmB, tmC, a, std::min(pairs, a.num_items), stream);
+    const int e = launch_fp8_pair(tmA, tmB, tmC, a, int(std::min(items.pairs, items.num_items)), stream);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return fail(SDT_ERR_LAUNCH, "gemm_fp8 launch failed: %s", cudaGetErrorString(cudaError_t(e)));

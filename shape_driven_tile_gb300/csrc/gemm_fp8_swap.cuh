@@ -113,7 +113,10 @@ __global__ void __launch_bounds__(SwapCfg<BT>::THREADS, 2)
     griddep_launch_dependents();
     // while the kernel before this one still runs, L2 may fetch this CTA's first weights (what L2
     // holds is never stale); nothing else is read yet
-    if (warp == 0 && lane < min(S, nkb)) tma_prefetch_l2_2d(&tmW, (kb0 + lane) * kFp8Block, n0);
+    if (warp == 0) {
+        if (lane < min(S, nkb)) tma_prefetch_l2_2d(&tmW, (kb0 + lane) * kFp8Block, n0);
+        if (lane == 31) tma_prefetch_desc(&tmX);
+    }
     griddep_wait();
 
     float acc[Cfg::COLS];

@@ -123,16 +123,21 @@ def gemm_fp8_plan(M: int, N: int, K: int, sm_count: int = 152) -> tuple[int, int
 
 
 def _outputs(q, scales, tokens, width, device, stream):
+    """(q, scales, their strides) of a call that may be given them."""
     blocks = -(-width // BLOCK)
     if q is None:
-        q = _streams.empty((tokens, width), _E4M3, device, stream)
+        shape = (tokens, width)
+        q = torch.empty(shape, dtype=_E4M3, device=device) if stream is None else _streams.empty(shape, _E4M3, device, stream)
+        q_row = width
     else:
         _need_rows(q, "q", (_E4M3,), (tokens, width))
+        q_row = q.stride(0)
     if scales is None:
-        scales = _streams.empty((tokens, blocks), _F32, device, stream)
-    else:
-        _need(scales, "scales", (_F32,), (tokens, blocks))
-    return q, scales
+        shape = (tokens, blocks)
+        scales = torch.empty(shape, dtype=_F32, device=device) if stream is None else _streams.empty(shape, _F32, device, stream)
+        return q, scales, q_row, blocks, 1
+    _need(scales, "scales", (_F32,), (tokens, blocks))
+    return q, scales, q_row, *scales.stride()
 
 
 def quant_fp8(x, gate=None, *, activation: str = "silu", q=None, scales=None, stream=None):
@@ -158,6 +163,7 @@ def quant_fp8(x, gate=None, *, activation: str = "silu", q=None, scales=None, st
     if not good:
         _need_rows(x, "x", ROW_CODES, (None, None))
         row = x.stride(0)
+        tokens, width = x.shape
         if gate is not None:
             _need_rows(gate, "gate", (x.dtype,), x.shape)
             gate_row = gate.stride(0)
@@ -168,9 +174,9 @@ def quant_fp8(x, gate=None, *, activation: str = "silu", q=None, scales=None, st
         code, gate_ptr = ACTIVATIONS.get(activation, 0), gate.data_ptr()
         if not code:
             raise ValueError(f"activation must be {' or '.join(map(repr, ACTIVATIONS))}, got {activation!r}")
-    q, scales = _outputs(q, scales, tokens, width, x.device, stream)
-    call = _QUANT.pack(x.data_ptr(), gate_ptr, q.data_ptr(), scales.data_ptr(), tokens, width, row, gate_row, q.stride(0),
-                       *scales.stride(), ROW_CODES[dtype], code)
+    q, scales, q_row, s_row, s_block = _outputs(q, scales, tokens, width, x.device, stream)
+    call = _QUANT.pack(x.data_ptr(), gate_ptr, q.data_ptr(), scales.data_ptr(), tokens, width, row, gate_row, q_row,
+                       s_row, s_block, ROW_CODES[dtype], code)
     check(_fn("quant_fp8")(call, _current_stream(dev) if stream is None else _streams.handle(stream)))
     return q, scales
 
@@ -190,28 +196,35 @@ def rms_norm_fp8(x, weight, residual=None, *, eps: float = 1e-6, out=None, q=Non
         row, along = x.stride()
         good = (dtype in ROW_CODES and along == 1 and x.get_device() == dev and weight.shape == (width,)
                 and (weight.dtype is dtype or weight.dtype is _F32) and weight.get_device() == dev and weight.is_contiguous())
-        for t in (residual, out):
-            if t is not None:
-                good = good and t.dtype is dtype and t.shape == x.shape and t.stride(1) == 1 and t.get_device() == dev
+        res_ptr = res_row = out_ptr = out_row = 0
+        if residual is not None:
+            res_row, along = residual.stride()
+            res_ptr = residual.data_ptr()
+            good = good and along == 1 and residual.dtype is dtype and residual.shape == x.shape and residual.get_device() == dev
+        if out is not None:
+            out_row, along = out.stride()
+            out_ptr = out.data_ptr()
+            good = good and along == 1 and out.dtype is dtype and out.shape == x.shape and out.get_device() == dev
     except (AttributeError, TypeError, ValueError, RuntimeError):
         good = False
     if not good:
         _need_rows(x, "x", ROW_CODES, (None, None))
-        row = x.stride(0)
+        (tokens, width), row = x.shape, x.stride(0)
         _need(weight, "weight", (x.dtype, _F32), (x.shape[1],))
         if not weight.is_contiguous():
             raise ValueError("weight must be contiguous")
         for name, t in (("residual", residual), ("out", out)):
             if t is not None:
                 _need_rows(t, name, (x.dtype,), x.shape)
-    q, scales = _outputs(q, scales, tokens, width, x.device, stream)
+        # nothing is wrong: a row of one value, say, whose stride may be anything
+        res_ptr, res_row = (0, 0) if residual is None else (residual.data_ptr(), residual.stride(0))
+        out_ptr, out_row = (0, 0) if out is None else (out.data_ptr(), out.stride(0))
+    q, scales, q_row, s_row, s_block = _outputs(q, scales, tokens, width, x.device, stream)
     if not hasattr(eps, "__float__"):
         raise TypeError(f"eps must be a number, got {type(eps).__name__}")
-    res_ptr, res_row = (0, 0) if residual is None else (residual.data_ptr(), residual.stride(0))
-    out_ptr, out_row = (0, 0) if out is None else (out.data_ptr(), out.stride(0))
     try:
         call = _NORM.pack(x.data_ptr(), weight.data_ptr(), res_ptr, out_ptr, q.data_ptr(), scales.data_ptr(), tokens, width, row,
-                          res_row, out_row, q.stride(0), *scales.stride(), eps, ROW_CODES[dtype], 3 if weight.dtype is _F32 else ROW_CODES[dtype])
+                          res_row, out_row, q_row, s_row, s_block, eps, ROW_CODES[dtype], 3 if weight.dtype is _F32 else ROW_CODES[dtype])
     except OverflowError as e:
         raise ValueError(f"eps is out of range: {eps}") from e
     check(_fn("rms_norm_fp8")(call, _current_stream(dev) if stream is None else _streams.handle(stream)))

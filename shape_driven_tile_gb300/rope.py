@@ -103,7 +103,7 @@ class RopeTable:
         self.frequencies = tuple(frequencies)
         turns = [_turns(f) for f in frequencies]
         self.turns = torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64, device=device or "cuda")
-        self.device_index = self.turns.get_device()
+        self.turns_ptr, self.device_index = self.turns.data_ptr(), self.turns.get_device()
 
 
 def _turns(frequency: float) -> int:
@@ -151,14 +151,16 @@ def rope_qk(q, k, positions, table: RopeTable, *, q_out=None, k_out=None, invers
     try:
         dev, dtype = _current_device(), q.dtype
         tokens, q_heads, head_dim = q.shape
-        k_heads = 0
+        q_token, q_head, along = q.stride()
+        k_heads = k_ptr = k_token = k_head = 0
         good = (table.device_index == dev and table.rotary <= head_dim and dtype in VALUE_CODES and q.get_device() == dev
-                and (q.stride(2) == 1 or head_dim <= 1) and positions.get_device() == dev and positions.shape == (tokens,)
+                and along == 1 and positions.get_device() == dev and positions.shape == (tokens,)
                 and positions.dtype in POSITION_BYTES and positions.is_contiguous())
         if k is not None:
-            k_heads = k.shape[1]
-            good = (good and k.dtype is dtype and k.shape == (tokens, k_heads, head_dim) and k.get_device() == dev
-                    and (k.stride(2) == 1 or head_dim <= 1))
+            k_tokens, k_heads, k_dim = k.shape
+            k_token, k_head, along = k.stride()
+            k_ptr = k.data_ptr()
+            good = good and k.dtype is dtype and k_tokens == tokens and k_dim == head_dim and along == 1 and k.get_device() == dev
     except (AttributeError, TypeError, ValueError, RuntimeError):
         good = False
     if not good:
@@ -175,24 +177,37 @@ def rope_qk(q, k, positions, table: RopeTable, *, q_out=None, k_out=None, invers
         _need(positions, "positions", POSITION_BYTES, 1)
         if positions.shape[0] != tokens or not positions.is_contiguous():
             raise ValueError(f"positions must be {tokens} contiguous entries")
-    if q_out is None:
-        q_out = _streams.empty(q.shape, dtype, q.device, stream)
-    elif q_out is not q:
+    if q_out is q:
+        qo_token, qo_head = q_token, q_head
+    elif q_out is None:
+        q_out = _new(q, stream)
+        qo_token, qo_head = q_heads * head_dim, head_dim
+    else:
         _need_heads(q_out, "q_out", (dtype,), q.shape)
+        qo_token, qo_head, _ = q_out.stride()
+    ko_ptr = ko_token = ko_head = 0
     if k is None:
         if k_out is not None:
             raise ValueError("k_out goes with k")
-        sides = (q.data_ptr(), 0, q_out.data_ptr(), 0)
-        k_strides = ko_strides = (0, 0)
     else:
-        if k_out is None:
-            k_out = _streams.empty(k.shape, dtype, k.device, stream)
-        elif k_out is not k:
+        if k_out is k:
+            ko_token, ko_head = k_token, k_head
+        elif k_out is None:
+            k_out = _new(k, stream)
+            ko_token, ko_head = k_heads * head_dim, head_dim
+        else:
             _need_heads(k_out, "k_out", (dtype,), k.shape)
-        sides = (q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr())
-        k_strides, ko_strides = k.stride()[:2], k_out.stride()[:2]
-    call = _ROPE.pack(*sides, positions.data_ptr(), table.turns.data_ptr(), tokens, q_heads, k_heads, head_dim, table.rotary,
-                      *q.stride()[:2], *k_strides, *q_out.stride()[:2], *ko_strides, table.magnitude, VALUE_CODES[dtype],
-                      POSITION_BYTES[positions.dtype], table.interleaved, bool(inverse))
+            ko_token, ko_head, _ = k_out.stride()
+        ko_ptr = k_out.data_ptr()
+    call = _ROPE.pack(q.data_ptr(), k_ptr, q_out.data_ptr(), ko_ptr, positions.data_ptr(), table.turns_ptr, tokens, q_heads, k_heads,
+                      head_dim, table.rotary, q_token, q_head, k_token, k_head, qo_token, qo_head, ko_token, ko_head, table.magnitude,
+                      VALUE_CODES[dtype], POSITION_BYTES[positions.dtype], table.interleaved, bool(inverse))
     check(_fn("rope_qk")(call, _current_stream(dev) if stream is None else _streams.handle(stream)))
     return q_out, k_out
+
+
+def _new(x, stream):
+    """An output as x, contiguous."""
+    if stream is None:
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    return _streams.empty(x.shape, x.dtype, x.device, stream)
