@@ -2,10 +2,10 @@
 // residual's addition) and quant_fp8 (as they are, or act(gate) * x).
 //
 // Quantisation of one block of 128 values y (the last block of a row may be shorter):
-// top = max(max|y|, 2^-100), scale = top * fl(1/448), q = e4m3(y * (448 / top)), rounded to
+// top = max(max|y|, 2^-100), scale = top * fl(1/448), q = e4m3(y * (1 / scale)), rounded to
 // nearest even; the product is within 2^-22 of y / scale before that rounding, and at most 448
-// up to a rounding that the conversion's saturation takes back.  The floor keeps 448 / top
-// finite for rows of zeros.  A NaN stays a NaN of its own; an infinity makes the scale infinite,
+// up to roundings that the conversion's saturation takes back.  The floor keeps 1 / scale finite
+// for rows of zeros.  A NaN stays a NaN of its own; an infinity makes the scale infinite,
 // so that its whole block stands for NaN.
 //
 // A thread moves 16-byte pieces of 8 values; 16 neighbouring threads hold a block and find its
@@ -31,45 +31,61 @@ constexpr int64_t kMaxQuantWidth = 65536, kMaxNormWidth = 32768;
 
 enum : int { kGateNone = 0, kGateSilu = 1, kGateGelu = 2 };
 
+// Eight values as four pairs: one instruction multiplies or adds both of a pair.
 template <typename T>
-__device__ __forceinline__ void to_f32(const uint4 &v, float (&f)[8]) {
-    const T *p = reinterpret_cast<const T *>(&v);
+__device__ __forceinline__ void to_f32(const uint4 &v, float2 (&f)[4]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = static_cast<float>(p[i]);
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (std::is_same_v<T, __half>) {
+            __half2 h;
+            memcpy(&h, &w[i], 4);
+            f[i] = __half22float2(h);
+        } else {
+            f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+        }
+    }
 }
 
 template <typename T>
-__device__ __forceinline__ uint4 from_f32(const float (&f)[8]) {
+__device__ __forceinline__ uint4 from_f32(const float2 (&f)[4]) {
     uint32_t h[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if constexpr (std::is_same_v<T, __half>) {
-            const __half2 v = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+            const __half2 v = __float22half2_rn(f[i]);
             memcpy(&h[i], &v, 4);
         } else {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            const __nv_bfloat162 v = __float22bfloat162_rn(f[i]);
             memcpy(&h[i], &v, 4);
         }
     }
     return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
-__device__ __forceinline__ float top_of(const float (&f)[8]) {
-    float t = fabsf(f[0]);
-#pragma unroll
-    for (int i = 1; i < 8; ++i) t = fmaxf(t, fabsf(f[i]));
-    return t;
+// max(|a|, |b|, |c|); a NaN counts only if all are.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+    float d;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float top_of(const float2 (&f)[4]) {
+    const float t = max3_abs(f[0].x, f[0].y, f[1].x), u = max3_abs(f[1].y, f[2].x, f[2].y);
+    return max3_abs(max3_abs(t, u, f[3].x), f[3].y, kTinyTop);
 }
 
-__device__ __forceinline__ uint2 to_e4m3(const float (&f)[8], float inv) {
-    uint32_t w[2];
+__device__ __forceinline__ uint2 to_e4m3(const float2 (&f)[4], float inv) {
+    uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i] * inv, f[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-        const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i + 2] * inv, f[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
-        w[i] = static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
-    }
-    return make_uint2(w[0], w[1]);
+    for (int i = 0; i < 4; ++i) w[i] = __nv_cvt_float2_to_fp8x2(__fmul2_rn(f[i], make_float2(inv, inv)), __NV_SATFINITE, __NV_E4M3);
+    return make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410));
+}
+
+// 1 / x to about half a step more than rounding, for normal x of up to 2^126.
+__device__ __forceinline__ float reciprocal(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return fmaf(fmaf(-x, r, 1.0f), r, r);
 }
 
 struct RowsOut {
@@ -79,21 +95,37 @@ struct RowsOut {
 };
 
 // The block's scale and the piece's fp8 values; `group` lanes (16, or a row's 8) hold the block.
-__device__ __forceinline__ void quantise_piece(const RowsOut &o, int64_t row, int piece, const float (&f)[8], int group, bool write) {
+// q and scale: where they go, used only if `write`.
+__device__ __forceinline__ void quantise_piece(uint8_t *q, float *scale, int piece, const float2 (&f)[4], int group, bool write) {
     float top = top_of(f);
 #pragma unroll
     for (int x = 1; x < 16; x <<= 1)
         if (x < group) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    top = fmaxf(top, kTinyTop);
+    const float s = top * (1.0f / kE4m3Max);
     if (!write) return;
-    *reinterpret_cast<uint2 *>(o.q + row * o.q_row + piece * 8) = to_e4m3(f, kE4m3Max / top);
-    if ((piece & 15) == 0) o.scales[row * o.s_row + (piece >> 4) * o.s_block] = top * (1.0f / kE4m3Max);
+    *reinterpret_cast<uint2 *>(q) = to_e4m3(f, reciprocal(s));
+    if ((piece & 15) == 0) *scale = s;
+}
+
+// 1 / (1 + exp(-t)) to some 1.5 steps of fp32, by exp(-|t|): its argument is taken in two parts (a
+// rounded one alone is off by |t| steps), the reciprocal gets a Newton step.  (Values next to a
+// border of the fp8 grid fall on its other side as often as such errors reach it; without these
+// two steps twice as many did.)  Below 2^-126 it is 0; a NaN counts as infinity here.
+__device__ __forceinline__ float sigmoid(float t) {
+    const float a = fminf(fabsf(t), 100.0f), x = a * -1.44269504f;
+    const float rest = fmaf(a, -1.44269504f, -x) * 0.6931472f;
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
+    e = fmaf(e, rest, e);
+    const float d = 1.0f + e;
+    r = reciprocal(d);
+    return t < 0.0f ? e * r : r;
 }
 
 // ---- quant_fp8 ----------------------------------------------------------------------------
 
 constexpr int kQuantThreads = 256;
-constexpr int kQuantUnroll = 4;
+constexpr int kQuantUnroll = 2;
 
 struct QuantArgs {
     const char *x, *gate;
@@ -127,25 +159,27 @@ __global__ void __launch_bounds__(kQuantThreads) quant_fp8_kernel(const QuantArg
     }
 #pragma unroll
     for (int u = 0; u < kQuantUnroll; ++u) {
-        float f[8];
+        float2 f[4];
         to_f32<T>(x[u], f);
         if constexpr (GATE != kGateNone) {
-            float h[8];
+            float2 h[4];
             to_f32<T>(g[u], h);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 4; ++i) {
                 // g * sigmoid(t): silu has t = g; gelu's tanh form is 0.5 g (1 + tanh(t / 2))
-                const float t = GATE == kGateSilu ? h[i] : h[i] * fmaf(0.0713548162726f, h[i] * h[i], 1.59576912160573f);
-                f[i] *= __fdividef(h[i], 1.0f + __expf(-t));
+                float2 t = h[i];
+                if (GATE == kGateGelu) {
+                    const float2 c1 = make_float2(1.59576912160573f, 1.59576912160573f), c3 = make_float2(0.0713548162726f, 0.0713548162726f);
+                    t = __fmul2_rn(h[i], __ffma2_rn(c3, __fmul2_rn(h[i], h[i]), c1));
+                }
+                f[i] = __fmul2_rn(f[i], __fmul2_rn(h[i], make_float2(sigmoid(t.x), sigmoid(t.y))));
             }
         }
-        quantise_piece(a.out, row[u], piece[u], f, 16, have[u]);
+        quantise_piece(a.out.q + row[u] * a.out.q_row + piece[u] * 8, a.out.scales + row[u] * a.out.s_row + (piece[u] >> 4) * a.out.s_block, piece[u], f, 16, have[u]);
     }
 }
 
 // ---- rms_norm_fp8 -------------------------------------------------------------------------
-
-constexpr int kNormThreads = 512;  // at most
 
 struct NormArgs {
     const char *x;
@@ -159,78 +193,119 @@ struct NormArgs {
     int weight_f32;
 };
 
-template <typename T, int VPT>
-__global__ void __launch_bounds__(kNormThreads) rms_norm_fp8_kernel(const NormArgs a) {
+// A CTA walks over its rows (or groups of short rows), the next ones on their way into registers
+// while it works on the present ones; the weights stay in registers.  VPT pieces a thread; rows of
+// more than 16384 values (VPT 8) have no registers for a second row and load one after another.
+constexpr int kNormThreads = 512;  // at most
+
+// Registers of a thread, and how many threads an SM then holds: without a residual half as much is
+// on its way per thread, so it takes more of them (16384 rows of 2880: 38.9 us with 768, 43.1 with 512).
+constexpr int norm_registers(int vpt, bool residual) { return vpt <= 2 ? 64 : vpt == 4 && !residual ? 80 : 128; }
+constexpr int norm_resident(int vpt, bool residual) { return vpt <= 2 ? 1024 : vpt == 4 && !residual ? 768 : 512; }
+
+template <typename T, int VPT, bool RES>
+__global__ void __maxnreg__(norm_registers(VPT, RES)) rms_norm_fp8_kernel(const NormArgs a) {
+    constexpr bool kAhead = VPT <= 4;
+    __shared__ float part[2][32];
     griddep_launch_dependents();
     const int per = a.per_row, whole = blockDim.x;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (whole / per) + threadIdx.x / per;
-    const int r = threadIdx.x % per;
+    const int r = threadIdx.x % per, step = gridDim.x * (whole / per);
+    int row = blockIdx.x * (whole / per) + threadIdx.x / per;
     griddep_wait();
-    const bool live = row < a.rows;
-    uint4 x[VPT], res[VPT];
+    uint4 x[VPT], res[RES ? VPT : 1], w[VPT];
+    const auto load = [&](int at) {
 #pragma unroll
-    for (int u = 0; u < VPT; ++u) {
-        const int piece = r + u * per;
-        x[u] = res[u] = make_uint4(0, 0, 0, 0);
-        if (live && piece < a.pieces) {
-            x[u] = *reinterpret_cast<const uint4 *>(a.x + row * a.x_row + piece * 16);
-            if (a.residual) res[u] = *reinterpret_cast<const uint4 *>(a.residual + row * a.r_row + piece * 16);
-        }
-    }
-    uint4 w[VPT];
-    if (!a.weight_f32)
-#pragma unroll
-        for (int u = 0; u < VPT; ++u)
-            if (r + u * per < a.pieces) w[u] = *reinterpret_cast<const uint4 *>(a.weight + (r + u * per) * 16);
-    float sum = 0.f;
-#pragma unroll
-    for (int u = 0; u < VPT; ++u) {
-        float f[8];
-        to_f32<T>(x[u], f);
-        if (a.residual) {
-            float h[8];
-            to_f32<T>(res[u], h);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] += h[i];
-            x[u] = from_f32<T>(f);  // the norm is of the sum as it is kept
-            to_f32<T>(x[u], f);
+        for (int u = 0; u < VPT; ++u) {
             const int piece = r + u * per;
-            if (live && piece < a.pieces) *reinterpret_cast<uint4 *>(a.residual + row * a.r_row + piece * 16) = x[u];
+            x[u] = make_uint4(0, 0, 0, 0);
+            if (RES) res[u] = make_uint4(0, 0, 0, 0);
+            if (at < a.rows && piece < a.pieces) {
+                x[u] = *reinterpret_cast<const uint4 *>(a.x + at * a.x_row + piece * 16);
+                if (RES) res[u] = *reinterpret_cast<const uint4 *>(a.residual + at * a.r_row + piece * 16);
+            }
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(f[i], f[i], sum);
-    }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1)
-        if (o < per) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (per > 32) {  // (a row is the whole CTA)
-        __shared__ float part[32];
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
-        __syncthreads();
-        sum = (threadIdx.x & 31) < (whole >> 5) ? part[threadIdx.x & 31] : 0.f;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    }
-    const float k = rsqrtf(fmaf(sum, a.inv_width, a.eps));
+    };
+    load(row);
 #pragma unroll
     for (int u = 0; u < VPT; ++u) {
-        const int piece = r + u * per;
-        const bool have = live && piece < a.pieces;
-        float f[8], h[8];
-        to_f32<T>(x[u], f);
-        if (a.weight_f32) {
-            if (piece < a.pieces) {
-                const float4 lo = *reinterpret_cast<const float4 *>(a.weight + piece * 32), hi = *reinterpret_cast<const float4 *>(a.weight + piece * 32 + 16);
-                h[0] = lo.x; h[1] = lo.y; h[2] = lo.z; h[3] = lo.w; h[4] = hi.x; h[5] = hi.y; h[6] = hi.z; h[7] = hi.w;
-            }
-        } else {
-            to_f32<T>(w[u], h);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = have ? f[i] * k * h[i] : 0.f;
-        if (a.out16 && have) *reinterpret_cast<uint4 *>(a.out16 + row * a.o_row + piece * 16) = from_f32<T>(f);
-        quantise_piece(a.out, row, piece, f, per < 16 ? per : 16, have);
+        w[u] = make_uint4(0, 0, 0, 0);
+        if (kAhead && !a.weight_f32 && r + u * per < a.pieces) w[u] = *reinterpret_cast<const uint4 *>(a.weight + (r + u * per) * 16);
     }
+    // (every thread of a CTA takes as many turns: they meet in them)
+    for (int first = blockIdx.x * (whole / per), turn = 0; first < a.rows; first += step, row += step, turn ^= 1) {
+        const bool live = row < a.rows;
+        uint4 v[VPT];
+        float2 sums = make_float2(0.f, 0.f);
+        char *res_row = a.residual + row * a.r_row + r * 16;
+#pragma unroll
+        for (int u = 0; u < VPT; ++u) {
+            v[u] = x[u];
+            float2 f[4];
+            to_f32<T>(x[u], f);
+            if constexpr (RES) {
+                float2 h[4];
+                to_f32<T>(res[u], h);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = __fadd2_rn(f[i], h[i]);
+                v[u] = from_f32<T>(f);  // the norm is of the sum as it is kept
+                to_f32<T>(v[u], f);
+                if (live && r + u * per < a.pieces) *reinterpret_cast<uint4 *>(res_row + u * per * 16) = v[u];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sums = __ffma2_rn(f[i], f[i], sums);
+        }
+        if (kAhead) load(row + step);
+        float sum = sums.x + sums.y;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1)
+            if (o < per) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (per > 32) {  // (a row is the whole CTA; two places, so that one meeting a row is enough)
+            if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x >> 5] = sum;
+            __syncthreads();
+            sum = (threadIdx.x & 31) < (whole >> 5) ? part[turn][threadIdx.x & 31] : 0.f;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        }
+        const float k = rsqrtf(fmaf(sum, a.inv_width, a.eps));
+        uint8_t *q = a.out.q + row * a.out.q_row + r * 8;
+        float *scale = a.out.scales + row * a.out.s_row + (r >> 4) * a.out.s_block;
+#pragma unroll
+        for (int u = 0; u < VPT; ++u) {
+            const int piece = r + u * per;
+            const bool have = live && piece < a.pieces;
+            float2 f[4], h[4];
+            to_f32<T>(v[u], f);
+            if (a.weight_f32) {
+                float4 lo = make_float4(0, 0, 0, 0), hi = lo;
+                if (piece < a.pieces) {
+                    lo = *reinterpret_cast<const float4 *>(a.weight + piece * 32);
+                    hi = *reinterpret_cast<const float4 *>(a.weight + piece * 32 + 16);
+                }
+                h[0] = make_float2(lo.x, lo.y); h[1] = make_float2(lo.z, lo.w); h[2] = make_float2(hi.x, hi.y); h[3] = make_float2(hi.z, hi.w);
+            } else {
+                if (!kAhead && piece < a.pieces) w[u] = *reinterpret_cast<const uint4 *>(a.weight + piece * 16);
+                to_f32<T>(w[u], h);
+            }
+            // (pieces past the row are zeros throughout)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = __fmul2_rn(__fmul2_rn(f[i], make_float2(k, k)), h[i]);
+            if (a.out16 && have) *reinterpret_cast<uint4 *>(a.out16 + row * a.o_row + piece * 16) = from_f32<T>(f);
+            quantise_piece(q + u * per * 8, scale + (u * per >> 4) * a.out.s_block, piece, f, per < 16 ? per : 16, have);
+        }
+        if (!kAhead) load(row + step);
+    }
+}
+
+template <typename T, bool RES>
+static auto norm_kernel(int vpt) {
+    return vpt == 1   ? rms_norm_fp8_kernel<T, 1, RES>
+           : vpt == 2 ? rms_norm_fp8_kernel<T, 2, RES>
+           : vpt == 4 ? rms_norm_fp8_kernel<T, 4, RES>
+                      : rms_norm_fp8_kernel<T, 8, RES>;
+}
+template <typename T>
+static auto norm_kernel(int vpt, bool residual) {
+    return residual ? norm_kernel<T, true>(vpt) : norm_kernel<T, false>(vpt);
 }
 
 static int check_out(const char *who, void *q, float *scales, int64_t tokens, int64_t width, int64_t q_row, int64_t s_row,
@@ -318,28 +393,29 @@ int rms_norm_fp8(const sdt_rms_norm_fp8 *call, sdt_stream_t stream) {
     if (!rc && c.out) rc = check_in("rms_norm_fp8", "out", c.out, c.tokens, c.o_row, c.width, true);
     if (!rc) rc = check_out("rms_norm_fp8", c.q, c.scales, c.tokens, c.width, c.q_row, c.s_row, c.s_block);
     if (rc) return rc;
-    rc = current_device(nullptr);
-    if (rc) return rc;
     NormArgs a{static_cast<const char *>(c.x), static_cast<char *>(c.residual), static_cast<const char *>(c.weight),
                static_cast<char *>(c.out), c.x_row * 2, c.r_row * 2, c.o_row * 2,
                {static_cast<uint8_t *>(c.q), c.scales, c.q_row, c.s_row, c.s_block},
                static_cast<int>(c.tokens), static_cast<int>(c.width / 8), 0, 1.0f / static_cast<float>(c.width), c.eps,
                c.weight_dtype == SDT_DTYPE_F32};
-    // rows of up to 32 pieces: several to a CTA, a power of two of threads each
-    int vpt = 1, threads = 128;
-    if (a.pieces <= 32) {
-        a.per_row = a.pieces <= 8 ? 8 : a.pieces <= 16 ? 16 : 32;
-    } else {
-        while (vpt < 8 && a.pieces > vpt * kNormThreads) vpt *= 2;
-        a.per_row = threads = ((a.pieces + vpt - 1) / vpt + 31) / 32 * 32;
-    }
+    // Few rows are spread over as many threads as they have pieces; many rows take four pieces a
+    // thread, so that each has several loads on their way.  Rows of few threads share a CTA, a power
+    // of two of threads each.
+    DeviceInfo dev;
+    rc = current_device(&dev);
+    if (rc) return rc;
+    const bool many = c.tokens >= 4 * dev.sm_count;
+    int vpt = many ? 4 : 1, threads = 128;
+    while (vpt < 8 && a.pieces > vpt * kNormThreads) vpt *= 2;
+    while (vpt > 1 && a.pieces <= vpt * 8) vpt /= 2;  // a block's 16 pieces stay with 16 neighbours
+    const int per = (a.pieces + vpt - 1) / vpt;
+    if (per <= 32) a.per_row = a.pieces <= 8 ? 8 : per <= 16 ? 16 : 32;
+    else a.per_row = threads = (per + 31) / 32 * 32;
     const int per_cta = threads / a.per_row;
-    const dim3 grid(static_cast<unsigned>((c.tokens + per_cta - 1) / per_cta));
-    const bool half = c.dtype == SDT_DTYPE_F16;
-    auto kern = vpt == 1   ? (half ? rms_norm_fp8_kernel<__half, 1> : rms_norm_fp8_kernel<__nv_bfloat16, 1>)
-                : vpt == 2 ? (half ? rms_norm_fp8_kernel<__half, 2> : rms_norm_fp8_kernel<__nv_bfloat16, 2>)
-                : vpt == 4 ? (half ? rms_norm_fp8_kernel<__half, 4> : rms_norm_fp8_kernel<__nv_bfloat16, 4>)
-                           : (half ? rms_norm_fp8_kernel<__half, 8> : rms_norm_fp8_kernel<__nv_bfloat16, 8>);
+    const int64_t groups = (c.tokens + per_cta - 1) / per_cta;
+    const int resident = dev.sm_count * (norm_resident(vpt, c.residual != nullptr) / threads);
+    const dim3 grid(static_cast<unsigned>(groups < resident ? groups : resident));
+    auto kern = c.dtype == SDT_DTYPE_F16 ? norm_kernel<__half>(vpt, c.residual != nullptr) : norm_kernel<__nv_bfloat16>(vpt, c.residual != nullptr);
     const cudaError_t e = launch_kernel(kern, grid, dim3(threads), 0, reinterpret_cast<cudaStream_t>(stream), 1, a);
     if (e != cudaSuccess) return fail(SDT_ERR_LAUNCH, "rms_norm_fp8 launch failed: %s", cudaGetErrorString(e));
     return SDT_OK;
