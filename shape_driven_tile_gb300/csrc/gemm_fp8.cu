@@ -28,40 +28,48 @@ static Fp8PairItems fp8_pair_items(int64_t M, int64_t N, int sm_count) {
     return {whole, whole + 2 * (tiles - whole), pairs};
 }
 
-// Swapped tiles run with as many CTAs per tile as still run at once, two to an SM.  kResident is the
-// share of the 2 x SMs places that clusters of 1 .. 8 CTAs can take (GPCs hold whole clusters only;
-// measured on 152 SMs).  A second round costs more than the split gains: 64 x 6144 x 4096 takes
-// 8.4 us in 48 clusters of 4 and 13.2 us in 48 of 6, of which 46 fit; 1 x 28672 x 8192 takes 37 us
-// unsplit and 42 split in 4.
-//
-// Two-CTA tiles take over where the estimates say so, microseconds fitted to measured shapes: a
-// swapped tile's CTA takes 0.55 a block beside another one, a two-CTA tile 0.44 a block, or 0.30 as
-// two half-width items.  Measured, swapped against two-CTA: 200 x 4096 x 4096 12.7 and 12.8,
-// 256 x 8192 x 4096 19.9 and 14.8, 333 x 5000 x 4208 22.8 and 18.5, 512 x 4096 x 4096 19.6 and 13.7;
-// 128 x 4096 x 14336, whose 16 two-CTA tiles would sum 112 blocks each, 18.7 and over 25.  Up to 64
-// tokens the two-CTA tile's rows are three quarters empty: swapped.
+// Tiles of up to 128 tokens run with as many CTAs per tile as still run at once, two to an SM (one
+// with 128 tokens).  kResident is the share of those places that clusters of 1 .. 8 CTAs can take
+// (GPCs hold whole clusters only; measured on 152 SMs).  A second round costs more than the split
+// gains: 64 x 6144 x 4096 takes 8.4 us in 48 clusters of 4 and 13.2 us in 48 of 6, of which 46 fit;
+// 1 x 28672 x 8192 takes 37 us unsplit and 42 split in 4.
+static int fp8_splits(int tile, int64_t tiles, int64_t kb, int sm_count) {
+    constexpr double kResident[kFp8MaxSplits] = {1.0, 1.0, 0.908, 0.947, 0.921, 0.908, 0.691, 0.789};
+    const int places = tile == 128 ? sm_count : 2 * sm_count;
+    int splits = 1;
+    for (int s = 2; s <= kFp8MaxSplits && 2 * s <= kb; ++s)  // (two blocks a CTA at least)
+        if (double(tiles) * s <= kResident[s - 1] * places) splits = s;
+    return splits;
+}
+
+// The tile: up to 64 tokens the smallest that holds them (larger ones are mostly empty rows), above
+// that the smallest of three estimates in microseconds, fitted to measured shapes: a block takes a
+// CTA of 64 tokens 0.55 beside another one, a CTA of 128 alone 0.33, a two-CTA tile 0.44, or 0.30 as
+// half-width items.  Measured with 64, 128 and two-CTA tiles: 100 x 4096 x 4096 8.7, 8.2 and 12.8,
+// 200 x 4096 x 4096 12.7, 10.1 and 12.8, 128 x 4096 x 14336 18.9, 17.2 and over 25, 333 x 5000 x
+// 4208 23.4, 17.6 and 18.5, 512 x 4096 x 4096 19.9, 13.5 and 13.9, 1021 x 2560 x 7168 46.7, 39.8 and
+// 27.4, 120 x 1024 x 8192 8.0, 8.6 and more.
 // `tile`: 0, or the tile that the caller asks for.
 static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int sm_count, int tile = 0) {
-    constexpr double kResident[kFp8MaxSplits] = {1.0, 1.0, 0.908, 0.947, 0.921, 0.908, 0.691, 0.789};
     const int64_t kb = (K + kFp8Block - 1) / kFp8Block;
-    Fp8Plan p;
-    p.splits = 1;
-    p.tile = tile ? tile : M <= 16 ? 16 : M <= 32 ? 32 : 64;
-    if (p.tile == 256) return p;
-    const int64_t tiles = ((M + p.tile - 1) / p.tile) * ((N + 127) / 128);
-    for (int s = 2; s <= kFp8MaxSplits && 2 * s <= kb; ++s)  // (two blocks a CTA at least)
-        if (double(tiles) * s <= kResident[s - 1] * 2 * sm_count) p.splits = s;
-    if (tile == 0 && M > 64) {
-        const Fp8PairItems items = fp8_pair_items(M, N, sm_count);
-        const double rounds = double(tiles) * p.splits / (2 * sm_count);
-        const double swapped = 3.5 + 0.55 * double((kb + p.splits - 1) / p.splits) * std::max(1.0, rounds);
-        const double paired = 4.0 + double(kb) * (0.44 * double((items.tail_start + items.pairs - 1) / items.pairs) + (items.num_items > items.tail_start ? 0.30 : 0.0));
-        if (paired < swapped) {
-            p.tile = 256;
-            p.splits = 1;
-        }
+    const auto tiles = [&](int t) { return ((M + t - 1) / t) * ((N + 127) / 128); };
+    if (tile == 0) tile = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+    else if (tile == 256) return {256, 1};
+    else return {tile, fp8_splits(tile, tiles(tile), kb, sm_count)};
+    Fp8Plan best{tile, fp8_splits(tile, tiles(tile), kb, sm_count)};
+    if (M <= 64) return best;
+    const auto blocks = [&](int splits) { return double((kb + splits - 1) / splits); };
+    double least = 3.5 + 0.55 * blocks(best.splits) * std::max(1.0, double(tiles(64)) * best.splits / (2 * sm_count));
+    const int splits = fp8_splits(128, tiles(128), kb, sm_count);
+    const double alone = 3.5 + 0.33 * blocks(splits) * double((tiles(128) * splits + sm_count - 1) / sm_count);
+    if (alone < least) {
+        least = alone;
+        best = {128, splits};
     }
-    return p;
+    const Fp8PairItems items = fp8_pair_items(M, N, sm_count);
+    const double rounds = double((items.tail_start + items.pairs - 1) / items.pairs);
+    if (4.0 + double(kb) * (0.44 * rounds + (items.num_items > items.tail_start ? 0.30 : 0.0)) < least) best = {256, 1};
+    return best;
 }
 
 static bool is_fp8(int t) { return t == SDT_DTYPE_E4M3 || t == SDT_DTYPE_E5M2; }
@@ -75,7 +83,7 @@ static int check_fp8(const sdt_gemm_fp8 &c) {
     if (!is_fp8(c.a_dtype) || !is_fp8(c.w_dtype)) return fail(SDT_ERR_ARG, "gemm_fp8: A and W must be e4m3 or e5m2");
     if (c.c_dtype != SDT_DTYPE_F16 && c.c_dtype != SDT_DTYPE_BF16 && c.c_dtype != SDT_DTYPE_F32)
         return fail(SDT_ERR_ARG, "gemm_fp8: C must be fp16, bf16 or fp32 (dtype %d)", c.c_dtype);
-    if (c.tile != 0 && c.tile != 16 && c.tile != 32 && c.tile != 64 && c.tile != 256)
+    if (c.tile != 0 && c.tile != 16 && c.tile != 32 && c.tile != 64 && c.tile != 128 && c.tile != 256)
         return fail(SDT_ERR_TILE, "gemm_fp8: no tile %d", c.tile);
     if (c.splits < 0 || c.splits > kFp8MaxSplits) return fail(SDT_ERR_ARG, "gemm_fp8: splits must be in 0 .. %d", kFp8MaxSplits);
     if (c.M == 0 || c.N == 0) return SDT_OK;
@@ -101,15 +109,17 @@ static int run_swap(const sdt_gemm_fp8 &c, const Fp8Plan &plan, Fp8Args &a, int6
     a.num_n_tiles = int((c.N + 127) / 128);
     a.splits = plan.splits;
     if (int64_t(a.num_m_tiles) * a.num_n_tiles * a.splits > INT32_MAX) return fail(SDT_ERR_SHAPE, "gemm_fp8: grid too large");
-    // W is the MMA's first operand here
-    a.idesc = (1u << 4) | ((c.w_dtype == SDT_DTYPE_E5M2 ? 1u : 0u) << 7) | ((c.a_dtype == SDT_DTYPE_E5M2 ? 1u : 0u) << 10);
+    // W is the MMA's first operand, but for tiles of 128 tokens
+    const uint32_t a_type = c.a_dtype == SDT_DTYPE_E5M2 ? 1u : 0u, w_type = c.w_dtype == SDT_DTYPE_E5M2 ? 1u : 0u;
+    a.idesc = (1u << 4) | ((plan.tile == 128 ? a_type : w_type) << 7) | ((plan.tile == 128 ? w_type : a_type) << 10);
     CUtensorMap tmW, tmX;
     int rc = tensor_map_2d(c.w, c.w_dtype, uint64_t(c.K), uint64_t(c.N), uint64_t(ldw), 128, &tmW, kFp8Block);
     if (!rc) rc = tensor_map_2d(c.a, c.a_dtype, uint64_t(c.K), uint64_t(c.M), uint64_t(lda), plan.tile, &tmX, kFp8Block);
     if (rc) return rc;
     int e = plan.tile == 16   ? launch_fp8_swap<16>(tmW, tmX, a, stream)
             : plan.tile == 32 ? launch_fp8_swap<32>(tmW, tmX, a, stream)
-                              : launch_fp8_swap<64>(tmW, tmX, a, stream);
+            : plan.tile == 64 ? launch_fp8_swap<64>(tmW, tmX, a, stream)
+                              : launch_fp8_swap<128>(tmW, tmX, a, stream);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return fail(SDT_ERR_LAUNCH, "gemm_fp8 launch failed: %s", cudaGetErrorString(cudaError_t(e)));

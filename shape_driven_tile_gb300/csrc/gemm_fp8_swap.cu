@@ -20,5 +20,6 @@ int launch_fp8_swap(const CUtensorMap &tmW, const CUtensorMap &tmX, const Fp8Arg
 template int launch_fp8_swap<16>(const CUtensorMap &, const CUtensorMap &, const Fp8Args &, cudaStream_t);
 template int launch_fp8_swap<32>(const CUtensorMap &, const CUtensorMap &, const Fp8Args &, cudaStream_t);
 template int launch_fp8_swap<64>(const CUtensorMap &, const CUtensorMap &, const Fp8Args &, cudaStream_t);
+template int launch_fp8_swap<128>(const CUtensorMap &, const CUtensorMap &, const Fp8Args &, cudaStream_t);
 
 }  // namespace sdt

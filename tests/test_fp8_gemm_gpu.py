@@ -6,7 +6,7 @@ import shape_driven_tile_gb300 as sdt
 from _fp8 import E4M3, E5M2, assert_near, fp8_values, product, scale_values
 
 pytestmark = pytest.mark.gpu
-TILES = [16, 32, 64, 256]
+TILES = [16, 32, 64, 128, 256]
 
 
 def operands(m, n, k, seed=0, at=E4M3, wt=E4M3):
