@@ -137,7 +137,8 @@ __device__ __forceinline__ bool elect_one() {
     return ok != 0;
 }
 
-// The two halves of a meeting of the cluster; the first one publishes nothing.
+// The two halves of a meeting of the cluster; the relaxed first half publishes nothing.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 

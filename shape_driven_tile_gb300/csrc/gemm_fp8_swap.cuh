@@ -18,8 +18,9 @@
 // workspace.  (Sums left in place and read by the owner took a second meeting and eight dependent
 // reads from other SMs: 2 us of a 5 us call.)
 //
-// Tensor memory is freed before the cluster meets: no CTA holds any while it waits for another
-// one, so kernels of several streams cannot block each other over it.
+// No CTA holds tensor memory while it waits for another one (it asks for it after it has said that
+// it started, and frees it before it waits for the sums), so kernels of several streams cannot
+// block each other over it.
 //
 // Roles: warp 0 lane 0 feeds the ring (TMA), warp 1 issues the MMAs, the rest scale and add.
 #pragma once
@@ -115,6 +116,12 @@ __global__ void __launch_bounds__(SwapCfg<BT>::THREADS, SwapCfg<BT>::PER_SM)
         ctrl[2] = 0;
         fence_mbar_init();
     }
+    if (p.splits > 1) {
+        // "this CTA has started", before it asks for tensor memory: the others wait for this and must
+        // not wait for that
+        __syncwarp();
+        cluster_arrive_relaxed();
+    }
     if (warp == 1) {
         tmem_alloc(smem_u32(const_cast<uint32_t *>(&ctrl[0])), Cfg::TMEM_COLS);
         tmem_relinquish();
@@ -123,7 +130,6 @@ __global__ void __launch_bounds__(SwapCfg<BT>::THREADS, SwapCfg<BT>::PER_SM)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = ctrl[0];
-    if (p.splits > 1) cluster_arrive_relaxed();  // "this CTA has started"
     griddep_launch_dependents();
     // while the kernel before this one still runs, L2 may fetch this CTA's first weights (what L2
     // holds is never stale); nothing else is read yet
@@ -330,11 +336,13 @@ __global__ void __launch_bounds__(SwapCfg<BT>::THREADS, SwapCfg<BT>::PER_SM)
                 break;
             }
     }
+    // every CTA's sums are where they are added; between the two halves of the meeting tensor memory is freed
+    if (p.splits > 1) cluster_arrive();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
     }
-    if (p.splits > 1) cluster_sync();  // every CTA's sums are where they are added
+    if (p.splits > 1) cluster_wait();
 
     // this CTA's share of the tokens, in rank order, 4 weight rows a thread
     const int first = static_cast<int>(rank) * share, count = min(share, tokens - first);
