@@ -30,15 +30,17 @@ static Fp8PairItems fp8_pair_items(int64_t M, int64_t N, int sm_count) {
 
 // Tiles of up to 128 tokens run with as many CTAs per tile as still run at once, two to an SM (one
 // with 128 tokens).  kResident is the share of those places that clusters of 1 .. 8 CTAs can take
-// (GPCs hold whole clusters only; measured on 152 SMs).  A second round costs more than the split
-// gains: 64 x 6144 x 4096 takes 8.4 us in 48 clusters of 4 and 13.2 us in 48 of 6, of which 46 fit;
+// (GPCs hold whole clusters only; by occupancy queries and start times on 152 SMs).  A second round
+// costs more than the split gains: 64 x 6144 x 4096 takes 8.4 us in 48 clusters of 4 and 13.2 us in 48 of 6, of which 46 fit;
 // 1 x 28672 x 8192 takes 37 us unsplit and 42 split in 4.
 static int fp8_splits(int tile, int64_t tiles, int64_t kb, int sm_count) {
-    constexpr double kResident[kFp8MaxSplits] = {1.0, 1.0, 0.908, 0.947, 0.921, 0.908, 0.691, 0.789};
-    const int places = tile == 128 ? sm_count : 2 * sm_count;
+    constexpr double kResident[2][kFp8MaxSplits] = {{1.0, 1.0, 0.908, 0.947, 0.921, 0.908, 0.737, 0.843},
+                                                    {1.0, 1.0, 0.908, 0.947, 0.921, 0.908, 0.691, 0.789}};
+    const bool alone = tile == 128;
+    const int places = alone ? sm_count : 2 * sm_count;
     int splits = 1;
     for (int s = 2; s <= kFp8MaxSplits && 2 * s <= kb; ++s)  // (two blocks a CTA at least)
-        if (double(tiles) * s <= kResident[s - 1] * places) splits = s;
+        if (double(tiles) * s <= kResident[alone][s - 1] * places) splits = s;
     return splits;
 }
 
