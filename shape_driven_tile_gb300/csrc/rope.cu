@@ -189,6 +189,8 @@ extern "C" int rope_qk(const sdt_rope_qk *call, sdt_stream_t stream) {
         if ((i % 2 ? (i % 4 == 1 ? c.q_heads : c.k_heads) : c.tokens) == 1) step[i] = 0;
     int rc = c.q_heads ? check_rope_side("q", c.q, c.q_out, c.tokens, c.q_heads, c.head_dim, step[0], step[1], step[4], step[5]) : SDT_OK;
     if (!rc && c.k_heads) rc = check_rope_side("k", c.k, c.k_out, c.tokens, c.k_heads, c.head_dim, step[2], step[3], step[6], step[7]);
+    if (!rc && c.q_heads && c.k_heads && (c.q_out == c.k_out || c.q_out == c.k || c.k_out == c.q))
+        rc = fail(SDT_ERR_ARG, "rope_qk: the output of one side must not be the other side's tensor");
     if (rc) return rc;
     if (c.rotary && (!c.positions || !c.turns)) return fail(SDT_ERR_NULL, "rope_qk: positions or turns is NULL");
     if (!aligned(c.positions, static_cast<uintptr_t>(c.position_bytes)) || !aligned(c.turns, 8))

@@ -76,7 +76,8 @@ def test_norm(change, status):
     (dict(head_dim=2 ** 17), SHAPE), (dict(tokens=-1), SHAPE), (dict(q_heads=-1), SHAPE), (dict(k_heads=65536), SHAPE), (dict(tokens=2 ** 24), SHAPE),
     (dict(position_bytes=2), ARG), (dict(q=None), NULL), (dict(k_out=None), NULL), (dict(positions=None), NULL), (dict(turns=None), NULL),
     (dict(q=A + 1), ALIGN), (dict(positions=A + 4), ALIGN), (dict(turns=A + 4), ALIGN), (dict(q_token=-1), ARG), (dict(k_head=2 ** 41), ARG),
-    (dict(qo_head=32), ARG), (dict(qo_token=64), ARG), (dict(ko_token=0), ARG), (dict(q_out=A + 128), ARG), (dict(q_out=A, qo_token=512), ARG)])
+    (dict(qo_head=32), ARG), (dict(qo_token=64), ARG), (dict(ko_token=0), ARG), (dict(q_out=A + 128), ARG), (dict(q_out=A, qo_token=512), ARG), (dict(q_out=4 * A), ARG), (dict(q_out=2 * A), ARG),
+    (dict(k_out=A), ARG)])
 def test_rope(change, status):
     assert called("rope_qk", rope._ROPE, ROPE, change) == status
 

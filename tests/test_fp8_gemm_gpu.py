@@ -126,3 +126,34 @@ def test_captured_and_on_another_stream(cuda_device, m):
     sa.copy_(sa.flip(0).clone())
     graph.replay()
     assert torch.equal(out, want.flip(0))
+
+
+@pytest.mark.parametrize("tile", [64, 128, 256])
+def test_outputs_past_32_bits(cuda_device, tile):
+    """More than 2^31 results: the last rows and a few between."""
+    m, n, k = 131088, 16400, 128
+    a, sa, w, sw = operands(m, n, k, seed=17)
+    got = sdt.gemm_fp8(a, sa, w, sw, tile=tile, splits=0 if tile == 256 else 1)
+    sdt.check_device_status()
+    at = torch.tensor([0, 1, 65535, 130943, 131000, m - 2, m - 1], device=cuda_device)
+    want, slack = product(a[at], sa[at], w, sw)
+    assert_near(got[at], want, slack)
+    del got
+    torch.cuda.empty_cache()
+
+
+def test_both_kernels_side_by_side(cuda_device):
+    """Calls on three streams at once, in every form, give what they give alone."""
+    jobs = [(operands(m, n, k, seed=20 + i), tile) for i, (m, n, k, tile) in enumerate(
+        [(1, 4096, 4096, 16), (700, 2048, 2048, 256), (40, 4096, 8192, 64), (100, 2048, 4096, 128), (3, 1024, 8192, 16)])]
+    want = [sdt.gemm_fp8(*ops, tile=tile) for ops, tile in jobs]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for turn in range(40):
+        for i, (ops, tile) in enumerate(jobs):
+            with torch.cuda.stream(streams[(turn + i) % 3]):
+                got.append((i, sdt.gemm_fp8(*ops, tile=tile)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, want[i]) for i, t in got)
+    sdt.check_device_status()

@@ -168,10 +168,33 @@ def test_captured_and_on_another_stream(cuda_device):
         assert all(torch.equal(a.float(), b) for a, b in zip(got, want))
 
 
-def test_a_block_of_one_token_does_not_depend_on_others(cuda_device):
-    """The same row gives the same bits whatever the number of tokens."""
+def test_one_row_does_not_depend_on_others(cuda_device):
+    """A row alone and among others: the same bits quantised; normed, the same values (the order of a row's sum
+    depends on the number of rows)."""
     x = rows(700, 2048, torch.bfloat16, 13)
     w = rows(1, 2048, torch.bfloat16, 14)[0]
-    all_q, all_s = sdt.rms_norm_fp8(x, w)
-    q, s = sdt.rms_norm_fp8(x[300:301], w)
+    all_q, all_s = sdt.quant_fp8(x)
+    q, s = sdt.quant_fp8(x[300:301])
     assert torch.equal(q.float(), all_q[300:301].float()) and torch.equal(s, all_s[300:301])
+    v = x[300:301].double()
+    y = v * w.double() / torch.sqrt(v.square().mean(1, keepdim=True) + 1e-6)
+    for q, s in (sdt.rms_norm_fp8(x[300:301], w), [t[300:301] for t in sdt.rms_norm_fp8(x, w)]):
+        assert_quantised(q, s, y, (2048 / 8 + 16) * 2.0 ** -24)
+
+
+def test_rows_past_32_bits(cuda_device):
+    """Inputs of more than 2^32 bytes: the last rows are those of a call on them alone."""
+    t, d = 270000, 8192
+    x = torch.zeros((t, d), dtype=torch.bfloat16, device=cuda_device)
+    tail = rows(3, d, torch.bfloat16, 15)
+    x[-3:] = tail
+    w = rows(1, d, torch.bfloat16, 16)[0]
+    q, s = sdt.quant_fp8(x)
+    want = sdt.quant_fp8(tail)
+    assert torch.equal(q[-3:].float(), want[0].float()) and torch.equal(s[-3:], want[1]) and (q[-4].float() == 0).all()
+    q, s = sdt.rms_norm_fp8(x, w, x.clone(), q=q, scales=s)
+    v = (tail.float() + tail.float()).to(torch.bfloat16).double()
+    y = v * w.double() / torch.sqrt(v.square().mean(1, keepdim=True) + 1e-6)
+    assert_quantised(q[-3:], s[-3:], y, (d / 8 + 16) * 2.0 ** -24)
+    del x, q, s
+    torch.cuda.empty_cache()
