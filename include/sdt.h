@@ -590,7 +590,8 @@ size_t sdt_paged_attn_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t
  * ldc a multiple of 8 at least N; a stride of a single row may be anything.  Scales 4-byte
  * aligned, strides not negative.
  * tile: 0 picks; 16, 32, 64 or 128 tokens per tile of 128 weight rows, whose blocks `splits`
- * (0 picks, 1 .. 8) CTAs share; 256: two-CTA tiles of 256 x 256, which are not split.
+ * (0 picks, 1 .. 8) CTAs share; 192 or 256: two-CTA tiles of 256 tokens by that many
+ * outputs, which are not split.
  * Errors: SDT_ERR_NULL, SDT_ERR_ALIGN, SDT_ERR_SHAPE (N, dimensions), SDT_ERR_ARG (types,
  * strides, splits), SDT_ERR_TILE.
  */

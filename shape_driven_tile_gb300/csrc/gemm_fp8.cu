@@ -17,14 +17,14 @@ struct Fp8Plan {
     int tile, splits;
 };
 
-// The items of the two-CTA tiles: whole tiles up to tail_start, then, if the last round would leave
-// at least half of the pairs idle, its tiles as two halves each.
+// The items of the two-CTA tiles (256 tokens by `width` outputs): whole tiles up to tail_start, then, if
+// the last round would leave at least half of the pairs idle, 256-wide tiles as two halves each.
 struct Fp8PairItems {
     int64_t tail_start, num_items, pairs;
 };
-static Fp8PairItems fp8_pair_items(int64_t M, int64_t N, int sm_count) {
-    const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256), pairs = std::max(1, sm_count / 2), left = tiles % pairs;
-    const int64_t whole = 2 * left <= pairs ? tiles - left : tiles;
+static Fp8PairItems fp8_pair_items(int64_t M, int64_t N, int sm_count, int width) {
+    const int64_t tiles = ((M + 255) / 256) * ((N + width - 1) / width), pairs = std::max(1, sm_count / 2), left = tiles % pairs;
+    const int64_t whole = width == 256 && 2 * left <= pairs ? tiles - left : tiles;
     return {whole, whole + 2 * (tiles - whole), pairs};
 }
 
@@ -45,18 +45,18 @@ static int fp8_splits(int tile, int64_t tiles, int64_t kb, int sm_count) {
 }
 
 // The tile: up to 64 tokens the smallest that holds them (larger ones are mostly empty rows), above
-// that the smallest of three estimates in microseconds, fitted to measured shapes: a block takes a
-// CTA of 64 tokens 0.55 beside another one, a CTA of 128 alone 0.33, a two-CTA tile 0.44, or 0.30 as
-// half-width items.  Measured with 64, 128 and two-CTA tiles: 100 x 4096 x 4096 8.7, 8.2 and 12.8,
-// 200 x 4096 x 4096 12.7, 10.1 and 12.8, 128 x 4096 x 14336 18.9, 17.2 and over 25, 333 x 5000 x
-// 4208 23.4, 17.6 and 18.5, 512 x 4096 x 4096 19.9, 13.5 and 13.9, 1021 x 2560 x 7168 46.7, 39.8 and
-// 27.4, 120 x 1024 x 8192 8.0, 8.6 and more.
+// that the smallest of four estimates in microseconds, fitted to measured shapes: a block takes a
+// CTA of 64 tokens 0.55 beside another one, a CTA of 128 alone 0.33, a two-CTA tile 0.44 (0.36 if it
+// is 192 wide, 0.30 as half-width items).  Measured with 64, 128, 192 and 256: 100 x 4096 x 4096 8.7,
+// 8.2, -, 12.8; 200 x 4096 x 4096 12.7, 10.2, -, 12.9; 128 x 4096 x 14336 18.9, 17.2, -, over 25;
+// 333 x 5000 x 4208 23.0, 17.2, 16.5, 19.2; 512 x 4096 x 4096 19.9, 13.3, 15.0, 13.8; 1021 x 2560 x
+// 7168 47, 40, 23.3, 27.4; 2048 x 5120 x 4096 84, 67, 39.6, 43.1; 4096^3 128, 94, 62.9, 57.6.
 // `tile`: 0, or the tile that the caller asks for.
 static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int sm_count, int tile = 0) {
     const int64_t kb = (K + kFp8Block - 1) / kFp8Block;
     const auto tiles = [&](int t) { return ((M + t - 1) / t) * ((N + 127) / 128); };
     if (tile == 0) tile = M <= 16 ? 16 : M <= 32 ? 32 : 64;
-    else if (tile == 256) return {256, 1};
+    else if (tile > 128) return {tile, 1};
     else return {tile, fp8_splits(tile, tiles(tile), kb, sm_count)};
     Fp8Plan best{tile, fp8_splits(tile, tiles(tile), kb, sm_count)};
     if (M <= 64) return best;
@@ -68,9 +68,15 @@ static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int sm_count, int tile 
         least = alone;
         best = {128, splits};
     }
-    const Fp8PairItems items = fp8_pair_items(M, N, sm_count);
-    const double rounds = double((items.tail_start + items.pairs - 1) / items.pairs);
-    if (4.0 + double(kb) * (0.44 * rounds + (items.num_items > items.tail_start ? 0.30 : 0.0)) < least) best = {256, 1};
+    for (int width : {256, 192}) {
+        const Fp8PairItems items = fp8_pair_items(M, N, sm_count, width);
+        const double rounds = double((items.tail_start + items.pairs - 1) / items.pairs);
+        const double paired = 4.0 + double(kb) * ((width == 256 ? 0.44 : 0.36) * rounds + (items.num_items > items.tail_start ? 0.30 : 0.0));
+        if (paired < least) {
+            least = paired;
+            best = {width, 1};
+        }
+    }
     return best;
 }
 
@@ -85,7 +91,7 @@ static int check_fp8(const sdt_gemm_fp8 &c) {
     if (!is_fp8(c.a_dtype) || !is_fp8(c.w_dtype)) return fail(SDT_ERR_ARG, "gemm_fp8: A and W must be e4m3 or e5m2");
     if (c.c_dtype != SDT_DTYPE_F16 && c.c_dtype != SDT_DTYPE_BF16 && c.c_dtype != SDT_DTYPE_F32)
         return fail(SDT_ERR_ARG, "gemm_fp8: C must be fp16, bf16 or fp32 (dtype %d)", c.c_dtype);
-    if (c.tile != 0 && c.tile != 16 && c.tile != 32 && c.tile != 64 && c.tile != 128 && c.tile != 256)
+    if (c.tile != 0 && c.tile != 16 && c.tile != 32 && c.tile != 64 && c.tile != 128 && c.tile != 192 && c.tile != 256)
         return fail(SDT_ERR_TILE, "gemm_fp8: no tile %d", c.tile);
     if (c.splits < 0 || c.splits > kFp8MaxSplits) return fail(SDT_ERR_ARG, "gemm_fp8: splits must be in 0 .. %d", kFp8MaxSplits);
     if (c.M == 0 || c.N == 0) return SDT_OK;
@@ -129,11 +135,11 @@ static int run_swap(const sdt_gemm_fp8 &c, const Fp8Plan &plan, Fp8Args &a, int6
     return SDT_OK;
 }
 
-static int run_pair(const sdt_gemm_fp8 &c, Fp8Args &a, int64_t lda, int64_t ldw, const DeviceInfo &dev, cudaStream_t stream) {
-    const Fp8PairItems items = fp8_pair_items(c.M, c.N, dev.sm_count);
+static int run_pair(const sdt_gemm_fp8 &c, int width, Fp8Args &a, int64_t lda, int64_t ldw, const DeviceInfo &dev, cudaStream_t stream) {
+    const Fp8PairItems items = fp8_pair_items(c.M, c.N, dev.sm_count, width);
     if (items.num_items > INT32_MAX / 2) return fail(SDT_ERR_SHAPE, "gemm_fp8: grid too large");
     a.num_m_tiles = int((c.M + 255) / 256);
-    a.num_n_tiles = int((c.N + 255) / 256);
+    a.num_n_tiles = int((c.N + width - 1) / width);
     a.splits = 1;
     a.raster_group = 8;
     a.tail_start = int(items.tail_start);
@@ -141,12 +147,13 @@ static int run_pair(const sdt_gemm_fp8 &c, Fp8Args &a, int64_t lda, int64_t ldw,
     a.idesc = (1u << 4) | ((c.a_dtype == SDT_DTYPE_E5M2 ? 1u : 0u) << 7) | ((c.w_dtype == SDT_DTYPE_E5M2 ? 1u : 0u) << 10);
     CUtensorMap tmA, tmB, tmC;
     int rc = tensor_map_2d(c.a, c.a_dtype, uint64_t(c.K), uint64_t(c.M), uint64_t(lda), 128, &tmA, kFp8Block);
-    if (!rc) rc = tensor_map_2d(c.w, c.w_dtype, uint64_t(c.K), uint64_t(c.N), uint64_t(ldw), 64, &tmB, kFp8Block);
+    if (!rc) rc = tensor_map_2d(c.w, c.w_dtype, uint64_t(c.K), uint64_t(c.N), uint64_t(ldw), width == 256 ? 64 : width / 2, &tmB, kFp8Block);
     // C leaves in boxes of 64-byte rows
     const uint64_t size = c.c_dtype == SDT_DTYPE_F32 ? 4 : 2;
     if (!rc) rc = tensor_map_2d(c.c, c.c_dtype, uint64_t(c.N), uint64_t(c.M), uint64_t(a.ldc) * size, 32, &tmC, int(64 / size), CU_TENSOR_MAP_SWIZZLE_64B);
     if (rc) return rc;
-    const int e = launch_fp8_pair(tmA, tmB, tmC, a, int(std::min(items.pairs, items.num_items)), stream);
+    const int pairs = int(std::min(items.pairs, items.num_items));
+    const int e = width == 256 ? launch_fp8_pair<256>(tmA, tmB, tmC, a, pairs, stream) : launch_fp8_pair<192>(tmA, tmB, tmC, a, pairs, stream);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return fail(SDT_ERR_LAUNCH, "gemm_fp8 launch failed: %s", cudaGetErrorString(cudaError_t(e)));
@@ -212,7 +219,7 @@ int gemm_fp8(const sdt_gemm_fp8 *call, sdt_stream_t stream_h) {
     Fp8Plan plan = fp8_plan(c.M, c.N, c.K, dev.sm_count, c.tile);
     if (c.splits) plan.splits = c.splits;
     plan.splits = std::min(plan.splits, a.num_kb);
-    if (plan.tile == 256) return run_pair(c, a, lda, ldw, dev, stream);
+    if (plan.tile > 128) return run_pair(c, plan.tile, a, lda, ldw, dev, stream);
     return run_swap(c, plan, a, lda, ldw, stream);
 }
 

@@ -6,13 +6,17 @@
 
 namespace sdt {
 
+template <int WIDTH>
 int launch_fp8_pair(const CUtensorMap &tmA, const CUtensorMap &tmB, const CUtensorMap &tmC, const Fp8Args &args, int pairs,
                     cudaStream_t stream) {
-    using Cfg = Fp8PairCfg;
+    using Cfg = Fp8PairCfg<WIDTH>;
     static std::atomic<int> configured[64];
-    if (int e = ensure_smem(gemm_fp8_pair_kernel, Cfg::SMEM_BYTES, configured)) return e;
-    return launch_kernel(gemm_fp8_pair_kernel, dim3(2 * static_cast<unsigned>(pairs)), dim3(Cfg::THREADS), size_t(Cfg::SMEM_BYTES),
+    if (int e = ensure_smem(gemm_fp8_pair_kernel<WIDTH>, Cfg::SMEM_BYTES, configured)) return e;
+    return launch_kernel(gemm_fp8_pair_kernel<WIDTH>, dim3(2 * static_cast<unsigned>(pairs)), dim3(Cfg::THREADS), size_t(Cfg::SMEM_BYTES),
                          stream, 2, tmA, tmB, tmC, args);
 }
+
+template int launch_fp8_pair<256>(const CUtensorMap &, const CUtensorMap &, const CUtensorMap &, const Fp8Args &, int, cudaStream_t);
+template int launch_fp8_pair<192>(const CUtensorMap &, const CUtensorMap &, const CUtensorMap &, const Fp8Args &, int, cudaStream_t);
 
 }  // namespace sdt

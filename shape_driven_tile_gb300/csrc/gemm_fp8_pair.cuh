@@ -1,5 +1,5 @@
 // gemm_fp8_pair.cuh -- gemm_fp8 for many tokens: persistent two-CTA tiles of 256 tokens by 256
-// outputs.
+// (or 192) outputs.
 //
 // A pair of CTAs runs M = 256 MMAs (cta_group::2) as gemm_pair.cuh does: each CTA stages its own
 // 128 token rows and half of the tile's weight rows per 128-deep block, 32 KB that feed 512
@@ -17,7 +17,9 @@
 // an MMA of 128 columns takes about as long as one of 256), one-CTA tiles too (522 us), and so
 // were 16 epilogue warps (433 us).
 //
-// The tiles of a last, partly empty round run as two half-width items each.
+// The tiles of a last, partly empty round run as two half-width items each.  192-wide tiles are for
+// shapes of few tiles, which 256-wide ones spread over fewer pairs (1021 x 2560 x 7168: 56 tiles on
+// 76 pairs instead of 40, 23.3 us against 27.4).
 //
 // Roles (384 threads): warp 0 feeds the ring (TMA), warp 1 of the leader issues the MMAs, warps 2
 // and 3 copy scales, warps 4..11 are the epilogue, which takes over registers of the first four
@@ -29,13 +31,15 @@
 
 namespace sdt {
 
+template <int WIDTH>
 struct Fp8PairCfg {
-    static constexpr int BM = 256, BN = 256, CTA_M = 128;
+    static constexpr int BM = 256, BN = WIDTH, CTA_M = 128;
     static constexpr int A_BYTES = CTA_M * kFp8Block, B_BYTES = BN / 2 * kFp8Block;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int STAGES = 5;
     static constexpr int THREADS = 384, EPI_WARPS = 8;
-    static constexpr int ACC_BUFS = 2, TMEM_COLS = ACC_BUFS * BN;
+    static constexpr int ACC_BUFS = 2, ACC_STEP = 256, TMEM_COLS = ACC_BUFS * ACC_STEP;  // step: columns from one to the other
+    static constexpr int B_BOX = BN == 256 ? 64 : BN / 2;  // rows of a TMA box of weights
     static constexpr int COLS = BN / 2;  // columns of an epilogue thread
     static constexpr int C_STAGE_BYTES = EPI_WARPS * 2 * kCStageBytes;
     static constexpr int AHEAD = 8;       // blocks whose scales are loaded together
@@ -56,18 +60,19 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_add
 struct Fp8Item {
     int m_tile, n0, width;
 };
+template <int BN>
 __device__ __forceinline__ Fp8Item fp8_item(int item, const Fp8Args &p) {
     Fp8Item r;
     int tile = item, off = 0, n_tile;
-    r.width = Fp8PairCfg::BN;
+    r.width = BN;
     if (item >= p.tail_start) {
         const int h = item - p.tail_start;
         tile = p.tail_start + (h >> 1);
-        off = (h & 1) * (Fp8PairCfg::BN / 2);
-        r.width = Fp8PairCfg::BN / 2;
+        off = (h & 1) * (BN / 2);
+        r.width = BN / 2;
     }
     tile_coords(tile, p.num_m_tiles, p.num_n_tiles, p.raster_group, r.m_tile, n_tile);
-    r.n0 = n_tile * Fp8PairCfg::BN + off;
+    r.n0 = n_tile * BN + off;
     return r;
 }
 
@@ -101,9 +106,10 @@ __device__ __forceinline__ void fp8_store_chunk(const CUtensorMap *tmC, uint32_t
 }
 
 // acc[j] += scale * column j of COLS columns of tensor memory, 32 at a time, the next ones on their
-// way while these are added; done() as soon as all have been read.
+// way while these are added; done() as soon as all have been read.  From column `in_first` (a
+// multiple of 32) on the scale is scale2.
 template <int COLS, int N, typename Done>
-__device__ __forceinline__ void fp8_scale_add(uint32_t taddr, float scale, float (&acc)[N], Done done) {
+__device__ __forceinline__ void fp8_scale_add(uint32_t taddr, float scale, float scale2, int in_first, float (&acc)[N], Done done) {
     uint32_t v[2][32];
     tmem_ld_32x32b_x32(taddr, v[0]);
 #pragma unroll
@@ -111,9 +117,14 @@ __device__ __forceinline__ void fp8_scale_add(uint32_t taddr, float scale, float
         tmem_ld_wait();
         if (c + 32 < COLS) tmem_ld_32x32b_x32(taddr + c + 32, v[(c / 32 + 1) & 1]);
         else done();
+        const float f = c < in_first ? scale : scale2;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(__uint_as_float(v[(c / 32) & 1][j]), scale, acc[c + j]);
+        for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(__uint_as_float(v[(c / 32) & 1][j]), f, acc[c + j]);
     }
+}
+template <int COLS, int N, typename Done>
+__device__ __forceinline__ void fp8_scale_add(uint32_t taddr, float scale, float (&acc)[N], Done done) {
+    fp8_scale_add<COLS>(taddr, scale, scale, COLS, acc, done);
 }
 
 __device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
@@ -136,10 +147,11 @@ __device__ __forceinline__ void mbar_arrive_copies(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+template <int WIDTH>
 __global__ void __launch_bounds__(384, 1)
     gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                          const __grid_constant__ CUtensorMap tmC, const Fp8Args p) {
-    using Cfg = Fp8PairCfg;
+    using Cfg = Fp8PairCfg<WIDTH>;
     constexpr int S = Cfg::STAGES;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -197,7 +209,7 @@ __global__ void __launch_bounds__(384, 1)
             uint32_t phase = 0;
             bool stop = false, ready = true;  // the ring's slots are free at first
             for (int item = pair; item < p.num_items && !stop; item += num_pairs) {
-                const Fp8Item it = fp8_item(item, p);
+                const Fp8Item it = fp8_item<WIDTH>(item, p);
                 const int m0 = it.m_tile * Cfg::BM + static_cast<int>(rank) * Cfg::CTA_M;
                 const int nb = it.n0 + static_cast<int>(rank) * (it.width / 2);
                 const bool whole = it.width == Cfg::BN;
@@ -219,7 +231,7 @@ __global__ void __launch_bounds__(384, 1)
                         const uint32_t fb = full_leader + 8 * s;
                         tma_load_2d_pair(smA + s * Cfg::A_BYTES, &tmA, fb, i * kFp8Block, m0);
                         tma_load_2d_pair(smB + s * Cfg::B_BYTES, &tmB, fb, i * kFp8Block, nb);
-                        if (whole) tma_load_2d_pair(smB + s * Cfg::B_BYTES + Cfg::B_BYTES / 2, &tmB, fb, i * kFp8Block, nb + Cfg::BN / 4);
+                        if (Cfg::BN == 256 && whole) tma_load_2d_pair(smB + s * Cfg::B_BYTES + Cfg::B_BYTES / 2, &tmB, fb, i * kFp8Block, nb + Cfg::BN / 4);
                     }
                     __syncwarp();
                     ++issued;
@@ -254,7 +266,7 @@ __global__ void __launch_bounds__(384, 1)
                         const uint64_t bd = b0 + static_cast<uint64_t>(s) * (Cfg::B_BYTES >> 4);
 #pragma unroll
                         for (int kk = 0; kk < kFp8Block / 32; ++kk)
-                            umma_fp8_pair(tmem_base + b * Cfg::BN, ad + 2 * kk, bd + 2 * kk, idesc, kk > 0);
+                            umma_fp8_pair(tmem_base + b * Cfg::ACC_STEP, ad + 2 * kk, bd + 2 * kk, idesc, kk > 0);
                         umma_commit_pair(acc_full + 8 * b, 0x3);  // (the epilogue hands the ring's slot back)
                     }
                     __syncwarp();
@@ -279,7 +291,7 @@ __global__ void __launch_bounds__(384, 1)
             uint32_t sc_phase = 0;
             bool stop = false;
             for (int item = pair; item < p.num_items && !stop; item += num_pairs) {
-                const Fp8Item it = fp8_item(item, p);
+                const Fp8Item it = fp8_item<WIDTH>(item, p);
                 const int m0 = it.m_tile * Cfg::BM + static_cast<int>(rank) * Cfg::CTA_M;
                 for (int i0 = 0; i0 < nkb; i0 += Cfg::AHEAD) {
                     if (ctrl[1] || !mbar_wait_soon(sc_empty + 8 * buf, sc_phase ^ 1u, 4 * lim)) {
@@ -301,7 +313,7 @@ __global__ void __launch_bounds__(384, 1)
                     }
                     if (t < 2 * Cfg::AHEAD) {
                         const int h = t / Cfg::AHEAD, kb = t % Cfg::AHEAD;
-                        const int nb = (it.n0 + h * (it.width / 2)) / kFp8Block;
+                        const int nb = (it.n0 + h * (it.width == kFp8Block ? 0 : kFp8Block)) / kFp8Block;  // the tile's two blocks
                         const bool in = nb * kFp8Block < p.N && i0 + kb < nkb;
                         copy_f32_async(dst + (Cfg::AHEAD * Cfg::CTA_M + t) * 4, in ? p.w_scales + nb * p.ws_row + (i0 + kb) * p.ws_block : p.w_scales, in);
                     }
@@ -317,14 +329,16 @@ __global__ void __launch_bounds__(384, 1)
         const uint32_t cbuf = smC + static_cast<uint32_t>(warp - 4) * 2u * kCStageBytes;
         const uint32_t acc_empty_leader = mapa_shared(acc_empty, 0);
         const uint32_t my_scales = smS + (q * 32 + lane) * 4, lanes = static_cast<uint32_t>(q * 32) << 16;
-        const uint32_t w_scales = smS + (Cfg::AHEAD * Cfg::CTA_M + part * Cfg::AHEAD) * 4;
+        // a part's outputs lie in one block of weight scales, but in 192-wide tiles they may pass into the next
+        const uint32_t w_scales = smS + (Cfg::AHEAD * Cfg::CTA_M + (WIDTH == 256 ? part * Cfg::AHEAD : 0)) * 4;
         int nst = 0, s = 0, buf = 0;
         uint32_t n = 0, sc_phase = 0;
         bool good = true, done = false;
         for (int item = pair; item < p.num_items && good; item += num_pairs) {
-            const Fp8Item it = fp8_item(item, p);
+            const Fp8Item it = fp8_item<WIDTH>(item, p);
             const int cols = it.width / 2;
             const uint32_t taddr = tmem_base + lanes + part * cols;
+            const int in_first = kFp8Block - it.n0 % kFp8Block - part * cols;  // columns of this part in the tile's first block
             float acc[Cfg::COLS];
 #pragma unroll
             for (int j = 0; j < Cfg::COLS; ++j) acc[j] = 0.f;
@@ -332,10 +346,10 @@ __global__ void __launch_bounds__(384, 1)
                 const int left = min(Cfg::AHEAD, nkb - i0);
                 good = warp_wait_soon(sc_full + 8 * buf, sc_phase, 4 * lim);
                 uint32_t sc = my_scales + buf * Cfg::SCALE_BYTES, sw = w_scales + buf * Cfg::SCALE_BYTES;
-                float token = ld_shared_f32(sc), weight = ld_shared_f32(sw);
+                float token = ld_shared_f32(sc), weight = ld_shared_f32(sw), weight2 = WIDTH == 256 ? 0.f : ld_shared_f32(sw + Cfg::AHEAD * 4);
                 for (int u = 0; u < left && good; ++u, ++n) {
                     const uint32_t b = n & 1;
-                    const float scale = token * weight;
+                    const float scale = token * weight, scale2 = token * weight2;
                     good = warp_wait_peeked(done, acc_full + 8 * b, (n >> 1) & 1, 4 * lim);
                     if (!good) break;
                     tc_fence_after();
@@ -344,6 +358,7 @@ __global__ void __launch_bounds__(384, 1)
                     if (u + 1 < left) {
                         token = ld_shared_f32(sc += Cfg::CTA_M * 4);
                         weight = ld_shared_f32(sw += 4);
+                        if (WIDTH != 256) weight2 = ld_shared_f32(sw + Cfg::AHEAD * 4);
                     }
                     const auto read = [&] {
                         tc_fence_before();
@@ -351,8 +366,9 @@ __global__ void __launch_bounds__(384, 1)
                         if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty_leader + 8 * b);
                         done = mbar_peek(acc_full + 8 * (b ^ 1), ((n + 1) >> 1) & 1);
                     };
-                    if (cols == Cfg::COLS) fp8_scale_add<Cfg::COLS>(taddr + b * Cfg::BN, scale, acc, read);
-                    else fp8_scale_add<Cfg::COLS / 2>(taddr + b * Cfg::BN, scale, acc, read);
+                    if (WIDTH != 256) fp8_scale_add<Cfg::COLS>(taddr + b * Cfg::ACC_STEP, scale, scale2, in_first, acc, read);
+                    else if (cols == Cfg::COLS) fp8_scale_add<Cfg::COLS>(taddr + b * Cfg::ACC_STEP, scale, acc, read);
+                    else fp8_scale_add<Cfg::COLS / 2>(taddr + b * Cfg::ACC_STEP, scale, acc, read);
                 }
                 if (lane == 0) mbar_arrive(sc_empty + 8 * buf);
                 if (++buf == Cfg::SCALE_BUFS) { buf = 0; sc_phase ^= 1u; }
