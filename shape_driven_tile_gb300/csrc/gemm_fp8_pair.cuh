@@ -10,12 +10,13 @@
 // holds.  Scales arrive eight blocks at a time in three buffers of shared memory, by 4-byte
 // asynchronous copies that pass over tile borders.
 //
-// What bounds it is the way round a pair of accumulators: MMAs, the commit, the reads, the
-// arrivals of both CTAs' warps, 1500 cycles for two blocks where the tensor cores need 1024.
-// 8192^3 takes 377 us (2.92 PFLOP/s); with one accumulator handed over for every four blocks,
-// which the scales forbid, it would be 311.  Four accumulators of 128 columns were slower (556 us:
-// an MMA of 128 columns takes about as long as one of 256), one-CTA tiles too (522 us), and so
-// were 16 epilogue warps (433 us).
+// What bounds it is the epilogue's 700 to 770 cycles a block, most of them the way round a pair of
+// accumulators (MMAs, the commit, the reads, the arrivals of both CTAs' warps), where the tensor
+// cores need 512: 8192^3 takes 380 us (2.89 PFLOP/s), with a quarter of the columns read 321.  Tried
+// and not faster: four accumulators of 128 columns, half a tile each (382 us; 313 with a quarter
+// read), the next block's first columns on their way while the last ones are added (407), all of a
+// warp's results staged at once in place of the fifth ring slot (405), 16 epilogue warps (433),
+// one-CTA tiles (522).
 //
 // The tiles of a last, partly empty round run as two half-width items each.  192-wide tiles are for
 // shapes of few tiles, which 256-wide ones spread over fewer pairs (1021 x 2560 x 7168: 56 tiles on
@@ -39,7 +40,6 @@ struct Fp8PairCfg {
     static constexpr int STAGES = 5;
     static constexpr int THREADS = 384, EPI_WARPS = 8;
     static constexpr int ACC_BUFS = 2, ACC_STEP = 256, TMEM_COLS = ACC_BUFS * ACC_STEP;  // step: columns from one to the other
-    static constexpr int B_BOX = BN == 256 ? 64 : BN / 2;  // rows of a TMA box of weights
     static constexpr int COLS = BN / 2;  // columns of an epilogue thread
     static constexpr int C_STAGE_BYTES = EPI_WARPS * 2 * kCStageBytes;
     static constexpr int AHEAD = 8;       // blocks whose scales are loaded together
