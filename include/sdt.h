@@ -1,8 +1,8 @@
 /*
  * sdt.h -- C ABI of the shape-driven-tile library (libsdt.so) for GB300 (sm_103a).
  *
- * Two products with the tile-selection calls around them, and the attention of a decode
- * step between them:
+ * Two products with the tile-selection calls around them, the attention of a decode step
+ * between them, and a layer's products in 8 bits with what makes their operands:
  *
  *   gemm_f16   C = A . B, fp16 in, fp32 accumulate, fp16 out, with the CTA tile
  *              chosen from the problem shape.
@@ -10,6 +10,8 @@
  *              K-major weight matrix, bf16 or q8 (int8 + one fp16 scale per 32).
  *   paged_attn_m1  attention of one new token per request over a paged key-value
  *              cache (paged_tables, paged_append around it).
+ *   gemm_fp8   C = A . W^T, fp8 values with a scale per 128 of k, fp32 sums
+ *              (rms_norm_fp8, quant_fp8 before it, rope_qk after it).
  *
  * Conventions for every call in this header:
  *  - Pointers named A, B, C, x, W, scales, y are DEVICE pointers owned by the
@@ -660,7 +662,8 @@ int rms_norm_fp8(const sdt_rms_norm_fp8 *call, sdt_stream_t stream);
  * in fp32, rounded once; inverse turns the other way (with it the call takes gradients of the
  * outputs to gradients of the inputs).  Elements from rotary on are copied.
  * q, k, q_out, k_out: [tokens][heads][head_dim] fp16 or bf16 (dtype), head_dim contiguous, any
- * other strides in elements (16-byte aligned heads are fastest); heads may be 0 (no such side).
+ * other strides in elements up to 2^32 (16-byte aligned heads are fastest); heads may be 0 (no
+ * such side).
  * An output is its input itself or lies apart from both inputs and the other output.  positions: int32 or int64
  * (position_bytes 4 or 8); turns: uint64 [rotary / 2].  head_dim even, rotary even, at most
  * head_dim; tokens * heads * head_dim below 2^31.

@@ -140,7 +140,7 @@ static auto kernel_for(int v, bool interleaved) {
                     : kernel_for<T, 1>(interleaved);
 }
 
-constexpr int64_t kRopeMaxHeads = 65535, kRopeMaxDim = 65536, kRopeMaxStride = int64_t(1) << 40;
+constexpr int64_t kRopeMaxHeads = 65535, kRopeMaxDim = 65536, kRopeMaxStride = int64_t(1) << 32;
 
 // An output whose tokens and heads do not overlap one another.
 static bool apart(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t d) {
@@ -155,7 +155,7 @@ static int check_rope_side(const char *what, const void *in, const void *out, in
     if (!in || !out) return fail(SDT_ERR_NULL, "rope_qk: %s or its output is NULL", what);
     if (!aligned(in, 2) || !aligned(out, 2)) return fail(SDT_ERR_ALIGN, "rope_qk: %s and its output must be 2-byte aligned", what);
     for (int64_t s : {it, ih, ot, oh})
-        if (s < 0 || s > kRopeMaxStride) return fail(SDT_ERR_ARG, "rope_qk: strides of %s must be in 0 .. 2^40", what);
+        if (s < 0 || s > kRopeMaxStride) return fail(SDT_ERR_ARG, "rope_qk: strides of %s must be in 0 .. 2^32", what);
     if (!apart(tokens, ot, heads, oh, d)) return fail(SDT_ERR_ARG, "rope_qk: tokens and heads of the output of %s must not overlap", what);
     if (in == out && it == ot && ih == oh) return SDT_OK;
     const auto lo = [](const void *p) { return reinterpret_cast<uintptr_t>(p); };
