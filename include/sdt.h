@@ -636,6 +636,7 @@ int quant_fp8(const sdt_quant_fp8 *call, sdt_stream_t stream);
  * rms_norm_fp8 -- the residual's addition, root-mean-square norm, and fp8 output:
  *   r = x + residual, rounded to their type and written back to residual (without one: r = x);
  *   y[t][i] = r[t][i] * weight[i] / sqrt(mean_j r[t][j]^2 + eps)      (fp32)
+ * (squares are summed in fp32: a row with values past 1e18 may overflow, and is zeros or NaN then)
  * and q, scales of y as quant_fp8 makes them.  out, if not NULL, receives y rounded to x's type.
  * x, residual, out: fp16 or bf16 (dtype), 16-byte aligned, row strides multiples of 8; weight:
  * x's type or fp32 (weight_dtype), 16-byte aligned; width up to 32768; sizes and outputs

@@ -304,8 +304,9 @@ __global__ void __launch_bounds__(384, 1)
                     int rows = p.M - m0 - row0, blocks = nkb - i0 - kb0;  // left from this thread's first value on
 #pragma unroll 2
                     for (int v = 0; v < 8; ++v) {
-                        copy_f32_async(to, src, rows > 0 && blocks > 0);
-                        copy_f32_async(to + near_dst, src + near, rows > near_rows && blocks > 0);
+                        const bool in = rows > 0 && blocks > 0, in_near = rows > near_rows && blocks > 0;
+                        copy_f32_async(to, in ? src : p.a_scales, in);
+                        copy_f32_async(to + near_dst, in_near ? src + near : p.a_scales, in_near);
                         src += far;
                         to += far_dst;
                         rows -= far_rows;
