@@ -617,7 +617,7 @@ int sdt_gemm_fp8_plan_for(int64_t M, int64_t N, int64_t K, int sm_count, int *ti
  * 0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3)))), computed in fp32.  A block's scale is
  * max(max|y|, 2^-100) / 448; its values are rounded to nearest even and at most 448.  A NaN
  * stays a NaN of its own; a block that holds an infinity gets an infinite scale and stands for
- * NaN.  Any number of tokens; width a multiple of 8 up to 65536, tokens * width up to 2^34.
+ * NaN.  Width a multiple of 8 up to 65536; tokens times the width in whole blocks of 128 below 2^34 - 2^12.
  * x and gate: fp16 or bf16 (dtype), 16-byte aligned, row strides multiples of 8 (they may be
  * slices of one row, as a product writes them side by side); q: e4m3, 8-byte aligned, row
  * stride a multiple of 8; scales: fp32 of any strides.  The outputs must not overlap the inputs

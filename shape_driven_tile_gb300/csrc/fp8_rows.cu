@@ -321,6 +321,8 @@ static int check_out(const char *who, void *q, float *scales, int64_t tokens, in
     if (!aligned(q, 8) || !aligned(scales, 4)) return fail(SDT_ERR_ALIGN, "%s: q must be 8-byte aligned, scales 4-byte", who);
     if (tokens > 1 && (q_row < width || q_row % 8)) return fail(SDT_ERR_ARG, "%s: q's row stride must be a multiple of 8, at least the width", who);
     const int64_t blocks = (width + 127) / 128;
+    if (tokens == 1) s_row = q_row = 0;  // (a dimension of one never steps)
+    if (blocks == 1) s_block = 0;
     constexpr int64_t most = int64_t(1) << 32;
     if (s_row < 0 || s_block < 0 || s_row > most || s_block > most || q_row > most) return fail(SDT_ERR_ARG, "%s: strides must be in 0 .. 2^32", who);
     const bool rows_out = tokens == 1 || s_row >= (blocks == 1 ? 1 : (blocks - 1) * s_block + 1);
@@ -341,7 +343,7 @@ static int check_in(const char *who, const char *what, const void *p, int64_t to
 static int check_size(const char *who, int64_t tokens, int64_t width, int64_t widest, int dtype) {
     if (width < 0 || width > widest || width % 8) return fail(SDT_ERR_SHAPE, "%s: width must be a multiple of 8 up to %lld (got %lld)", who, (long long)widest, (long long)width);
     if (tokens < 0 || (width > 0 && tokens > (INT32_MAX - kQuantThreads * kQuantUnroll) / ((width + 127) / 128 * 16)))
-        return fail(SDT_ERR_SHAPE, "%s: tokens * width must be in 0 .. 2^34 (got %lld tokens)", who, (long long)tokens);
+        return fail(SDT_ERR_SHAPE, "%s: tokens times the width in whole blocks of 128 must be below 2^34 - 2^12 (got %lld tokens)", who, (long long)tokens);
     if (dtype != SDT_DTYPE_F16 && dtype != SDT_DTYPE_BF16) return fail(SDT_ERR_ARG, "%s: dtype must be fp16 or bf16 (got %d)", who, dtype);
     return SDT_OK;
 }

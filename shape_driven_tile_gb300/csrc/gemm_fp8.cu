@@ -11,6 +11,7 @@
 namespace sdt {
 
 constexpr int64_t kFp8MaxDim = int64_t(1) << 30;
+constexpr int kFp8MaxSms = 65536;  // of a plan
 constexpr int kFp8MaxSplits = 8;  // CTAs of a portable cluster
 
 struct Fp8Plan {
@@ -106,8 +107,9 @@ static int check_fp8(const sdt_gemm_fp8 &c) {
     if (c.N > 1 && (c.ldw < c.K || c.ldw % 16)) return fail(SDT_ERR_ARG, "gemm_fp8: ldw must be a multiple of 16, at least K (got %lld)", (long long)c.ldw);
     // strides that TMA takes (below 2^40 bytes), and scale offsets within 64 bits
     constexpr int64_t most = int64_t(1) << 32;
-    if (c.lda >= most || c.ldw >= most || c.ldc >= most) return fail(SDT_ERR_ARG, "gemm_fp8: strides must be below 2^32 elements");
-    for (int64_t s : {c.as_row, c.as_block, c.ws_row, c.ws_block})
+    if ((c.M > 1 && (c.lda >= most || c.ldc >= most)) || (c.N > 1 && c.ldw >= most)) return fail(SDT_ERR_ARG, "gemm_fp8: strides must be below 2^32 elements");
+    const bool rows = c.M > 1, blocks = c.K > kFp8Block, panels = c.N > kFp8Block;  // (a dimension of one never steps)
+    for (int64_t s : {rows ? c.as_row : 0, blocks ? c.as_block : 0, panels ? c.ws_row : 0, blocks ? c.ws_block : 0})
         if (s < 0 || s >= most) return fail(SDT_ERR_ARG, "gemm_fp8: scale strides must be in 0 .. 2^32 (got %lld)", (long long)s);
     return SDT_OK;
 }
@@ -170,8 +172,8 @@ extern "C" {
 int sdt_gemm_fp8_plan_for(int64_t M, int64_t N, int64_t K, int sm_count, int *tile, int *splits) {
     clear_error();
     if (!tile || !splits) return fail(SDT_ERR_NULL, "NULL output pointer");
-    if (M < 1 || N < 1 || K < 1 || M > kFp8MaxDim || N > kFp8MaxDim || K > kFp8MaxDim || sm_count < 1)
-        return fail(SDT_ERR_SHAPE, "M, N, K must be in 1 .. 2^30 and sm_count positive");
+    if (M < 1 || N < 1 || K < 1 || M > kFp8MaxDim || N > kFp8MaxDim || K > kFp8MaxDim || sm_count < 1 || sm_count > kFp8MaxSms)
+        return fail(SDT_ERR_SHAPE, "M, N, K must be in 1 .. 2^30, sm_count in 1 .. 65536");
     const Fp8Plan p = fp8_plan(M, N, K, sm_count);
     *tile = p.tile;
     *splits = p.splits;
@@ -204,10 +206,10 @@ int gemm_fp8(const sdt_gemm_fp8 *call, sdt_stream_t stream_h) {
     a.a_scales = c.a_scales;
     a.w_scales = c.w_scales;
     a.C = c.c;
-    a.as_row = c.as_row;
-    a.as_block = c.as_block;
-    a.ws_row = c.ws_row;
-    a.ws_block = c.ws_block;
+    a.as_row = c.M > 1 ? c.as_row : 0;
+    a.as_block = c.K > kFp8Block ? c.as_block : 0;
+    a.ws_row = c.N > kFp8Block ? c.ws_row : 0;
+    a.ws_block = c.K > kFp8Block ? c.ws_block : 0;
     a.ldc = ldc;
     a.M = int(c.M);
     a.N = int(c.N);

@@ -1,5 +1,4 @@
-// gemm_fp8.cuh -- what the kernels of gemm_fp8 share: arguments, the fp8 MMA, packed fp32
-// arithmetic, scales in shared memory, output types.
+// gemm_fp8.cuh -- what the kernels of gemm_fp8 share: arguments, the fp8 MMA, waits that ask ahead.
 //
 //   C[m][n] = sum_b ws[n / 128][b] * as[m][b] * sum_{k in block b} a[m][k] * w[n][k]
 //

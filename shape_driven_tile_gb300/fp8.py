@@ -118,7 +118,7 @@ def gemm_fp8(a, a_scales, w, w_scales, out=None, *, out_dtype=torch.bfloat16, ti
 def gemm_fp8_plan(M: int, N: int, K: int, sm_count: int = 152) -> tuple[int, int]:
     """(tile, splits) that gemm_fp8 picks on a GPU with sm_count SMs; no GPU needed."""
     tile, splits = ctypes.c_int(), ctypes.c_int()
-    check(lib().sdt_gemm_fp8_plan_for(M, N, K, int(sm_count), ctypes.byref(tile), ctypes.byref(splits)))
+    check(lib().sdt_gemm_fp8_plan_for(M, N, K, _integer("sm_count", sm_count), ctypes.byref(tile), ctypes.byref(splits)))
     return tile.value, splits.value
 
 

@@ -91,6 +91,8 @@ class RopeTable:
             frequencies, own = rope_frequencies(rotary, base, scaling=scaling, factor=factor, original_length=original_length,
                                                 low=low, high=high)
         else:
+            if not hasattr(rotary, "__index__"):
+                raise TypeError(f"rotary must be an integer, got {type(rotary).__name__}")
             frequencies, own = [float(f) for f in frequencies], 1.0
             if rotary != 2 * len(frequencies) or not frequencies:
                 raise ValueError(f"frequencies must be rotary // 2 = {rotary // 2} numbers, got {len(frequencies)}")

@@ -114,6 +114,8 @@ def test_tables_refused():
             sdt.RopeTable(4, device="cpu", **kw)
     with pytest.raises(TypeError, match="rotary"):
         sdt.RopeTable(4.0, device="cpu")
+    with pytest.raises(TypeError, match="rotary"):
+        sdt.RopeTable(4.0, frequencies=[1.0, 0.5], device="cpu")
 
 
 def two_pi(bits):
@@ -152,3 +154,9 @@ def test_frequencies_of_the_scalings():
 def test_plans(m, n, k):
     tile, splits = sdt.gemm_fp8_plan(m, n, k)
     assert 1 <= splits <= min(8, -(-k // 128)) and (tile >= min(m, 64) or m > 64)
+
+
+def test_plans_refused():
+    for sms, error in ((0, sdt.SdtError), (65537, sdt.SdtError), (2 ** 31, ValueError), (1.5, TypeError)):
+        with pytest.raises(error):
+            sdt.gemm_fp8_plan(64, 128, 128, sms)

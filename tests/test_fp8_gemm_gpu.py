@@ -77,6 +77,18 @@ def test_strides(cuda_device, m):
     check(a, one.expand(m, 3), w, one.expand(2, 3))
 
 
+def test_strides_of_single_rows_and_blocks_may_be_anything(cuda_device):
+    a, sa, w, sw = operands(1, 72, 112, seed=10)
+    far = 2 ** 33 + 5
+    out = torch.zeros(72, dtype=torch.bfloat16, device=cuda_device).as_strided((1, 72), (far, 1))
+    check(a.as_strided((1, 112), (far, 1)), sa.as_strided((1, 1), (far, far)), w, sw.as_strided((1, 1), (far, far)), out)
+    x = torch.randn(1, 112, device=cuda_device).to(torch.bfloat16)
+    q, s = sdt.quant_fp8(x)
+    q1, s1 = (torch.zeros_like(t).as_strided(t.shape, (far, 1)) for t in (q, s))
+    sdt.quant_fp8(x, q=q1, scales=s1.as_strided((1, 1), (far, far)))
+    assert torch.equal(q1.float(), q.float()) and torch.equal(s1, s)
+
+
 @pytest.mark.parametrize("m,n,k", [(0, 16, 32), (4, 0, 32), (4, 16, 0), (130, 264, 0)])
 def test_empty(cuda_device, m, n, k):
     a, w = (torch.zeros(s, device=cuda_device).to(E4M3) for s in ((m, k), (n, k)))
