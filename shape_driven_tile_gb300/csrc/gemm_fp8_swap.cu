@@ -10,10 +10,11 @@ template <int BT>
 int launch_fp8_swap(const CUtensorMap &tmW, const CUtensorMap &tmX, const Fp8Args &args, cudaStream_t stream) {
     using Cfg = SwapCfg<BT>;
     static std::atomic<int> configured[64];
-    if (int e = ensure_smem(gemm_fp8_swap_kernel<BT>, Cfg::SMEM_BYTES, configured)) return e;
+    if (int e = ensure_smem(gemm_fp8_swap_kernel<BT>, Cfg::SMEM_MOST, configured)) return e;
     const unsigned grid = static_cast<unsigned>(args.num_m_tiles) * static_cast<unsigned>(args.num_n_tiles) *
                           static_cast<unsigned>(args.splits);
-    return launch_kernel(gemm_fp8_swap_kernel<BT>, dim3(grid), dim3(Cfg::THREADS), size_t(Cfg::SMEM_BYTES), stream,
+    return launch_kernel(gemm_fp8_swap_kernel<BT>, dim3(grid), dim3(Cfg::THREADS),
+                         size_t(BT == 128 && args.splits == 1 ? Cfg::SMEM_ALONE : Cfg::SMEM_BYTES), stream,
                          static_cast<unsigned>(args.splits), tmW, tmX, args);
 }
 

@@ -22,7 +22,7 @@
 // it started, and frees it before it waits for the sums), so kernels of several streams cannot
 // block each other over it.
 //
-// Roles: warp 0 lane 0 feeds the ring (TMA), warp 1 issues the MMAs, the rest scale and add.
+// Roles: warp 0 feeds the ring (TMA), warp 1 issues the MMAs, the rest scale and add.
 #pragma once
 
 #include "gemm_fp8.cuh"
@@ -41,7 +41,11 @@ struct SwapCfg {
     static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
     static constexpr int ACC_BUFS = 4;
     static constexpr int TMEM_COLS = ACC_BUFS * BT;  // an SM's CTAs always fit
+    // ring slots: beside a buffer for the sums of a cluster's CTAs, and with 128 tokens and no cluster, where the
+    // sums go where the ring was (128 x 16384 x 4096: 16.6 us, 18.0 with four slots; with 64 tokens a fourth slot
+    // in place of the buffer takes 48 us for 64 x 28672 x 8192 instead of 42)
     static constexpr int STAGES = BT == 16 ? 5 : BT == 64 ? 3 : 4;
+    static constexpr int STAGES_ALONE = 6;
     static constexpr int PER_SM = BT == 128 ? 1 : 2;  // CTAs of an SM
     static constexpr int CHUNK = BT == 128 ? 8 : 512 / BT;  // k-blocks whose scales are in shared memory at a time
     static constexpr int SCALE_BYTES = CHUNK * BT * 4;
@@ -51,9 +55,13 @@ struct SwapCfg {
     static constexpr int SUM_PITCH = SWAP ? ROWS : ROWS + 4;  // floats (16-byte stores of 8 neighbouring lanes reach all banks)
     static constexpr int SUM_BYTES = SUM_ROWS * SUM_PITCH * 4;
     static constexpr int CTRL_BYTES = 512;
-    static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 2 * SCALE_BYTES + SUM_BYTES + CTRL_BYTES;
+    static constexpr int OTHER_BYTES = 1024 + 2 * SCALE_BYTES + CTRL_BYTES;
+    static constexpr int SMEM_BYTES = OTHER_BYTES + STAGES * STAGE_BYTES + SUM_BYTES;
+    static constexpr int SMEM_ALONE = OTHER_BYTES + STAGES_ALONE * STAGE_BYTES;
+    static constexpr int SMEM_MOST = BT == 128 && SMEM_ALONE > SMEM_BYTES ? SMEM_ALONE : SMEM_BYTES;
     static_assert(BT == 16 || BT == 32 || BT == 64 || BT == 128, "tokens per tile");
-    static_assert(TMEM_COLS * PER_SM <= 512 && SMEM_BYTES <= (PER_SM == 2 ? 115712 : 232448), "an SM holds PER_SM CTAs");
+    static_assert(TMEM_COLS * PER_SM <= 512 && SMEM_MOST <= (PER_SM == 2 ? 115712 : 232448), "an SM holds PER_SM CTAs");
+    static_assert(BT < 128 || BT * SUM_PITCH * 4 <= STAGES_ALONE * STAGE_BYTES, "the sums fit where the ring was");
 };
 
 __device__ __forceinline__ void st_cluster_f4(uint32_t addr, float x, float y, float z, float w) {
@@ -80,13 +88,17 @@ __global__ void __launch_bounds__(SwapCfg<BT>::THREADS, SwapCfg<BT>::PER_SM)
     gemm_fp8_swap_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                          const Fp8Args p) {
     using Cfg = SwapCfg<BT>;
-    constexpr int S = Cfg::STAGES, NB = Cfg::ACC_BUFS, E = Cfg::EPI_WARPS * 32;
+    constexpr int NB = Cfg::ACC_BUFS, E = Cfg::EPI_WARPS * 32;
+    const bool alone = BT == 128 && p.splits == 1;
+    const int S = alone ? Cfg::STAGES_ALONE : Cfg::STAGES;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t smW = base, smX = base + S * Cfg::W_BYTES;
     const uint32_t smS = base + S * Cfg::STAGE_BYTES;  // two chunks of scales
-    const uint32_t smR = smS + 2 * Cfg::SCALE_BYTES;   // sums from the cluster's CTAs: [CTA][token of this one's share][row]
-    const uint32_t bars = smR + Cfg::SUM_BYTES;
+    // sums from the cluster's CTAs: [CTA][token of this one's share][row]; a CTA alone takes the ring,
+    // which nothing reads or fills once the last block's MMAs are done
+    const uint32_t smR = alone ? base : smS + 2 * Cfg::SCALE_BYTES;
+    const uint32_t bars = smS + 2 * Cfg::SCALE_BYTES + (alone ? 0 : Cfg::SUM_BYTES);
     const uint32_t full = bars, empty = bars + 8 * S, acc_full = bars + 16 * S, acc_empty = acc_full + 8 * NB;
     volatile uint32_t *ctrl = reinterpret_cast<volatile uint32_t *>(smem_raw + (acc_empty + 8 * NB - smem_u32(smem_raw)));
     // ctrl[0]: TMEM base   ctrl[1]: a role gave up   ctrl[2]: blocks the producer asked for
