@@ -119,7 +119,7 @@ __device__ __forceinline__ void fp8_scale_add(uint32_t taddr, float scale, float
         else done();
         const float f = c < in_first ? scale : scale2;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(__uint_as_float(v[(c / 32) & 1][j]), f, acc[c + j]);
+        for (int j = 0; j < 32; j += 2) fma2(acc + c + j, v[(c / 32) & 1] + j, make_float2(f, f));
     }
 }
 template <int COLS, int N, typename Done>

@@ -290,11 +290,8 @@ __global__ void __launch_bounds__(SwapCfg<BT>::THREADS, SwapCfg<BT>::PER_SM)
                         }
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            float *to = acc + 16 * g + 4 * j;
-                            to[0] = fmaf(__uint_as_float(v[g][4 * j]), f[j].x, to[0]);
-                            to[1] = fmaf(__uint_as_float(v[g][4 * j + 1]), f[j].y, to[1]);
-                            to[2] = fmaf(__uint_as_float(v[g][4 * j + 2]), f[j].z, to[2]);
-                            to[3] = fmaf(__uint_as_float(v[g][4 * j + 3]), f[j].w, to[3]);
+                            fma2(acc + 16 * g + 4 * j, v[g] + 4 * j, make_float2(f[j].x, f[j].y));
+                            fma2(acc + 16 * g + 4 * j + 2, v[g] + 4 * j + 2, make_float2(f[j].z, f[j].w));
                         }
                     }
                 } else {
@@ -305,7 +302,7 @@ __global__ void __launch_bounds__(SwapCfg<BT>::THREADS, SwapCfg<BT>::PER_SM)
                     tmem_ld_wait();
                     have_read();
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) acc[j % Cfg::COLS] = fmaf(__uint_as_float(v[j / 32][j % 32]), scale, acc[j % Cfg::COLS]);
+                    for (int j = 0; j < 64; j += 2) fma2(acc + j % Cfg::COLS, v[j / 32] + j % 32, make_float2(scale, scale));
                 }
             }
             if (++b == NB) { b = 0; acc_phase ^= 1u; }
