@@ -47,14 +47,14 @@ static int fp8_splits(int tile, int64_t tiles, int64_t kb, int sm_count) {
 
 // The tile: up to 64 tokens the smallest that holds them (larger ones are mostly empty rows), above
 // that the smallest of four estimates in microseconds, fitted to measured shapes: a block takes a
-// CTA of 64 tokens 0.55 beside another one, a CTA of 128 alone 0.33, a two-CTA tile 0.44 (0.36 if it
-// is 192 wide, 0.30 as half-width items).  Rows that are not whole 32-byte sectors cost the first two,
+// CTA of 64 tokens 0.50 beside another one, a CTA of 128 alone 0.29, a two-CTA tile 0.40 (0.33 if it
+// is 192 wide, 0.29 as half-width items).  Rows that are not whole 32-byte sectors cost the first two,
 // which load most per product, 22 % more (333 x 5000 with k of 4224: 20.7, 14.5, 15.9, 18.4; with 4208:
-// 25.3, 17.5, 16.4, 18.7).  Measured with 64, 128, 192 and 256: 96 x 4096 x 4096 8.7, 8.4, 13.7, 12.7;
-// 256 x 4096 x 4096 12.7, 10.8, 13.9, 13.0; 96 x 4096 x 14336 18.8, 17.1, 40.8, 36.8; 512 x 4096 x 4096
-// 19.8, 14.1, 14.6, 13.8; 1021 x 2560 x 7168 49, 41, 23.2, 26.9; 2048 x 5120 x 4096 84, 67, 39.6, 43.1;
-// 4096^3 128, 94, 62.9, 57.6.  Over 48 shapes of 96 to 1021 tokens the choice is 0.2 % slower than the
-// best on average, 4 % at worst.
+// 25.3, 17.5, 16.4, 18.7).  Measured with 64, 128, 192 and 256: 96 x 4096 x 4096 8.5, 8.2, 13.4, 12.5;
+// 256 x 4096 x 4096 12.4, 10.5, 13.7, 12.7; 96 x 4096 x 14336 18.0, 16.9, 38.3, 35.7; 512 x 4096 x 4096
+// 19.0, 13.4, 14.3, 13.5; 700 x 4096 x 14336 87, 68, 39.6, 46.9; 1021 x 2560 x 7168 47, 38, 22.1, 26.1;
+// 1021 x 12288 x 4096 96, 78, 48.6, 45.1.  Over 48 shapes of 96 to 1021 tokens the choice is 0.1 % slower
+// than the best on average, 4 % at worst.
 // `tile`: 0, or the tile that the caller asks for.
 static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int sm_count, int tile = 0) {
     const int64_t kb = (K + kFp8Block - 1) / kFp8Block;
@@ -66,9 +66,9 @@ static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int sm_count, int tile 
     if (M <= 64) return best;
     const auto blocks = [&](int splits) { return double((kb + splits - 1) / splits); };
     const double sectors = K % 32 ? 1.22 : 1.0;
-    double least = 3.5 + 0.55 * sectors * blocks(best.splits) * std::max(1.0, double(tiles(64)) * best.splits / (2 * sm_count));
+    double least = 3.5 + 0.50 * sectors * blocks(best.splits) * std::max(1.0, double(tiles(64)) * best.splits / (2 * sm_count));
     const int splits = fp8_splits(128, tiles(128), kb, sm_count);
-    const double alone = 3.5 + 0.33 * sectors * blocks(splits) * double((tiles(128) * splits + sm_count - 1) / sm_count);
+    const double alone = 3.5 + 0.29 * sectors * blocks(splits) * double((tiles(128) * splits + sm_count - 1) / sm_count);
     if (alone < least) {
         least = alone;
         best = {128, splits};
@@ -76,7 +76,7 @@ static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int sm_count, int tile 
     for (int width : {256, 192}) {
         const Fp8PairItems items = fp8_pair_items(M, N, sm_count, width);
         const double rounds = double((items.tail_start + items.pairs - 1) / items.pairs);
-        const double paired = 4.0 + double(kb) * ((width == 256 ? 0.44 : 0.36) * rounds + (items.num_items > items.tail_start ? 0.30 : 0.0));
+        const double paired = 4.0 + double(kb) * ((width == 256 ? 0.40 : 0.33) * rounds + (items.num_items > items.tail_start ? 0.29 : 0.0));
         if (paired < least) {
             least = paired;
             best = {width, 1};

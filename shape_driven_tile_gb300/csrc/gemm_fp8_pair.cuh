@@ -4,27 +4,26 @@
 // A pair of CTAs runs M = 256 MMAs (cta_group::2) as gemm_pair.cuh does: each CTA stages its own
 // 128 token rows and half of the tile's weight rows per 128-deep block, 32 KB that feed 512
 // cycles of MMAs.  Two accumulators of 256 columns fill tensor memory and hold one block's sums
-// each: while the tensor cores fill one, eight epilogue warps per CTA read the other, scale it
-// and add it to registers (128 columns a thread: 256 cycles of multiply-adds).  A thread's lane
-// is a token row, so its scale is one register: the token's times that of the 128 outputs it
-// holds.  Scales arrive eight blocks at a time in three buffers of shared memory, by 4-byte
+// each: while the tensor cores fill one, eight epilogue warps per CTA (twelve for 192 outputs) read
+// the other, scale it and add it to registers (128 columns a thread, or 64).  A thread's lane is a
+// token row and its columns lie in one block of 128 outputs, so its scale is one register.  Scales arrive eight blocks at a time in three buffers of shared memory, by 4-byte
 // asynchronous copies that pass over tile borders.
 //
-// What bounds it is the epilogue's 700 to 770 cycles a block, most of them the way round a pair of
+// What bounds it is the epilogue's 680 to 750 cycles a block, most of them the way round a pair of
 // accumulators (MMAs, the commit, the reads, the arrivals of both CTAs' warps), where the tensor
-// cores need 512: 8192^3 takes 380 us (2.89 PFLOP/s), with a quarter of the columns read 321.  Tried
-// and not faster: four accumulators of 128 columns, half a tile each (382 us; 313 with a quarter
-// read), the next block's first columns on their way while the last ones are added (407), all of a
-// warp's results staged at once in place of the fifth ring slot (405), 16 epilogue warps (433),
-// one-CTA tiles (522).
+// cores need 512: 8192^3 takes 369 us (2.98 PFLOP/s).  When it took 380, with one multiply-add a value,
+// it was 321 with a quarter of the columns read; tried then and not faster: four accumulators of 128
+// columns, half a tile each (382 us; 313 with a quarter read), the next block's first columns on
+// their way while the last ones are added (407), all of a warp's results staged at once in place of
+// the fifth ring slot (405), 16 epilogue warps (433), one-CTA tiles (522).
 //
 // The tiles of a last, partly empty round run as two half-width items each.  192-wide tiles are for
 // shapes of few tiles, which 256-wide ones spread over fewer pairs (1021 x 2560 x 7168: 56 tiles on
-// 76 pairs instead of 40, 23.3 us against 27.4).
+// 76 pairs instead of 40, 21.8 us against 26.4); with eight epilogue warps of 96 columns they take 22.1.
 //
-// Roles (384 threads): warp 0 feeds the ring (TMA), warp 1 of the leader issues the MMAs, warps 2
-// and 3 copy scales, warps 4..11 are the epilogue, which takes over registers of the first four
-// (setmaxnreg: 56 a thread there, 224 in the epilogue, of 3 x 168 at launch).
+// Roles: warp 0 feeds the ring (TMA), warp 1 of the leader issues the MMAs, warps 2 and 3 copy
+// scales, the others are the epilogue, which takes over registers of the first four (setmaxnreg:
+// 56 a thread there, 224 in eight epilogue warps, of 168 at launch; 152 in twelve, of 128).
 #pragma once
 
 #include "gemm_fp8.cuh"
@@ -38,9 +37,13 @@ struct Fp8PairCfg {
     static constexpr int A_BYTES = CTA_M * kFp8Block, B_BYTES = BN / 2 * kFp8Block;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int STAGES = 5;
-    static constexpr int THREADS = 384, EPI_WARPS = 8;
+    static constexpr int PARTS = WIDTH == 256 ? 2 : 3;  // epilogue warps side by side, each with a part of the columns
+    static constexpr int EPI_WARPS = 4 * PARTS, THREADS = 128 + 32 * EPI_WARPS;
+    // registers of a thread: what the launch gives all, and after the roles have parted
+    static constexpr int ROLE_REGS = 56, EPI_REGS = PARTS == 2 ? 224 : 152;
+    static_assert(128 * ROLE_REGS + 32 * EPI_WARPS * EPI_REGS <= THREADS * (65536 / THREADS / 8 * 8), "within the launch's registers");
     static constexpr int ACC_BUFS = 2, ACC_STEP = 256, TMEM_COLS = ACC_BUFS * ACC_STEP;  // step: columns from one to the other
-    static constexpr int COLS = BN / 2;  // columns of an epilogue thread
+    static constexpr int COLS = BN / PARTS;  // columns of an epilogue thread
     static constexpr int C_STAGE_BYTES = EPI_WARPS * 2 * kCStageBytes;
     static constexpr int AHEAD = 8;       // blocks whose scales are loaded together
     static constexpr int SCALE_BUFS = 3;
@@ -106,10 +109,9 @@ __device__ __forceinline__ void fp8_store_chunk(const CUtensorMap *tmC, uint32_t
 }
 
 // acc[j] += scale * column j of COLS columns of tensor memory, 32 at a time, the next ones on their
-// way while these are added; done() as soon as all have been read.  From column `in_first` (a
-// multiple of 32) on the scale is scale2.
+// way while these are added; done() as soon as all have been read.
 template <int COLS, int N, typename Done>
-__device__ __forceinline__ void fp8_scale_add(uint32_t taddr, float scale, float scale2, int in_first, float (&acc)[N], Done done) {
+__device__ __forceinline__ void fp8_scale_add(uint32_t taddr, float scale, float (&acc)[N], Done done) {
     uint32_t v[2][32];
     tmem_ld_32x32b_x32(taddr, v[0]);
 #pragma unroll
@@ -117,14 +119,9 @@ __device__ __forceinline__ void fp8_scale_add(uint32_t taddr, float scale, float
         tmem_ld_wait();
         if (c + 32 < COLS) tmem_ld_32x32b_x32(taddr + c + 32, v[(c / 32 + 1) & 1]);
         else done();
-        const float f = c < in_first ? scale : scale2;
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) fma2(acc + c + j, v[(c / 32) & 1] + j, make_float2(f, f));
+        for (int j = 0; j < 32; j += 2) fma2(acc + c + j, v[(c / 32) & 1] + j, make_float2(scale, scale));
     }
-}
-template <int COLS, int N, typename Done>
-__device__ __forceinline__ void fp8_scale_add(uint32_t taddr, float scale, float (&acc)[N], Done done) {
-    fp8_scale_add<COLS>(taddr, scale, scale, COLS, acc, done);
 }
 
 __device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
@@ -148,7 +145,7 @@ __device__ __forceinline__ void mbar_arrive_copies(uint32_t bar) {
 }
 
 template <int WIDTH>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(Fp8PairCfg<WIDTH>::THREADS, 1)
     gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                          const __grid_constant__ CUtensorMap tmC, const Fp8Args p) {
     using Cfg = Fp8PairCfg<WIDTH>;
@@ -198,7 +195,7 @@ __global__ void __launch_bounds__(384, 1)
     griddep_wait();
 
     if (warp < 4) {
-        regs_dec<56>();
+        regs_dec<Cfg::ROLE_REGS>();
         if (warp == 0) {
             if (elect_one()) {
                 tma_prefetch_desc(&tmA);
@@ -325,21 +322,21 @@ __global__ void __launch_bounds__(384, 1)
             asm volatile("cp.async.wait_all;" ::: "memory");
         }
     } else {
-        regs_inc<224>();
+        regs_inc<Cfg::EPI_REGS>();
         const int q = warp & 3, part = (warp - 4) >> 2;
         const uint32_t cbuf = smC + static_cast<uint32_t>(warp - 4) * 2u * kCStageBytes;
         const uint32_t acc_empty_leader = mapa_shared(acc_empty, 0);
         const uint32_t my_scales = smS + (q * 32 + lane) * 4, lanes = static_cast<uint32_t>(q * 32) << 16;
-        // a part's outputs lie in one block of weight scales, but in 192-wide tiles they may pass into the next
-        const uint32_t w_scales = smS + (Cfg::AHEAD * Cfg::CTA_M + (WIDTH == 256 ? part * Cfg::AHEAD : 0)) * 4;
         int nst = 0, s = 0, buf = 0;
         uint32_t n = 0, sc_phase = 0;
         bool good = true, done = false;
         for (int item = pair; item < p.num_items && good; item += num_pairs) {
             const Fp8Item it = fp8_item<WIDTH>(item, p);
-            const int cols = it.width / 2;
+            const int cols = it.width / Cfg::PARTS;
             const uint32_t taddr = tmem_base + lanes + part * cols;
-            const int in_first = kFp8Block - it.n0 % kFp8Block - part * cols;  // columns of this part in the tile's first block
+            // a part's outputs lie in one block of weight scales, the tile's first or second
+            const int second = WIDTH == 256 ? part : it.n0 % kFp8Block + part * cols >= kFp8Block;
+            const uint32_t w_scales = smS + (Cfg::AHEAD * Cfg::CTA_M + second * Cfg::AHEAD) * 4;
             float acc[Cfg::COLS];
 #pragma unroll
             for (int j = 0; j < Cfg::COLS; ++j) acc[j] = 0.f;
@@ -347,10 +344,10 @@ __global__ void __launch_bounds__(384, 1)
                 const int left = min(Cfg::AHEAD, nkb - i0);
                 good = warp_wait_soon(sc_full + 8 * buf, sc_phase, 4 * lim);
                 uint32_t sc = my_scales + buf * Cfg::SCALE_BYTES, sw = w_scales + buf * Cfg::SCALE_BYTES;
-                float token = ld_shared_f32(sc), weight = ld_shared_f32(sw), weight2 = WIDTH == 256 ? 0.f : ld_shared_f32(sw + Cfg::AHEAD * 4);
+                float token = ld_shared_f32(sc), weight = ld_shared_f32(sw);
                 for (int u = 0; u < left && good; ++u, ++n) {
                     const uint32_t b = n & 1;
-                    const float scale = token * weight, scale2 = token * weight2;
+                    const float scale = token * weight;
                     good = warp_wait_peeked(done, acc_full + 8 * b, (n >> 1) & 1, 4 * lim);
                     if (!good) break;
                     tc_fence_after();
@@ -359,7 +356,6 @@ __global__ void __launch_bounds__(384, 1)
                     if (u + 1 < left) {
                         token = ld_shared_f32(sc += Cfg::CTA_M * 4);
                         weight = ld_shared_f32(sw += 4);
-                        if (WIDTH != 256) weight2 = ld_shared_f32(sw + Cfg::AHEAD * 4);
                     }
                     const auto read = [&] {
                         tc_fence_before();
@@ -367,8 +363,7 @@ __global__ void __launch_bounds__(384, 1)
                         if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty_leader + 8 * b);
                         done = mbar_peek(acc_full + 8 * (b ^ 1), ((n + 1) >> 1) & 1);
                     };
-                    if (WIDTH != 256) fp8_scale_add<Cfg::COLS>(taddr + b * Cfg::ACC_STEP, scale, scale2, in_first, acc, read);
-                    else if (cols == Cfg::COLS) fp8_scale_add<Cfg::COLS>(taddr + b * Cfg::ACC_STEP, scale, acc, read);
+                    if (WIDTH != 256 || cols == Cfg::COLS) fp8_scale_add<Cfg::COLS>(taddr + b * Cfg::ACC_STEP, scale, acc, read);
                     else fp8_scale_add<Cfg::COLS / 2>(taddr + b * Cfg::ACC_STEP, scale, acc, read);
                 }
                 if (lane == 0) mbar_arrive(sc_empty + 8 * buf);
