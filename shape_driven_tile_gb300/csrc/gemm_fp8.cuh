@@ -136,7 +136,8 @@ __device__ __forceinline__ bool elect_one() {
     return ok != 0;
 }
 
-// acc[0..1] += v[0..1] * scale, two values an instruction (8192^3 takes 369 us; with one at a time 378; 4096^3 56.4, 58.3).
+// acc[0..1] += v[0..1] * scale, two values an instruction (on one GPU 8192^3 takes 369 us, with one at a time
+// 378; 4096^3 56.4, 58.3).
 __device__ __forceinline__ void fma2(float *acc, const uint32_t *v, float2 scale) {
     const float2 r = __ffma2_rn(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), scale, make_float2(acc[0], acc[1]));
     acc[0] = r.x;

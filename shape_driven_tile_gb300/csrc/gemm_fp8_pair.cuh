@@ -11,11 +11,12 @@
 //
 // What bounds it is the epilogue's 680 to 750 cycles a block, most of them the way round a pair of
 // accumulators (MMAs, the commit, the reads, the arrivals of both CTAs' warps), where the tensor
-// cores need 512: 8192^3 takes 369 us (2.98 PFLOP/s).  When it took 380, with one multiply-add a value,
-// it was 321 with a quarter of the columns read; tried then and not faster: four accumulators of 128
-// columns, half a tile each (382 us; 313 with a quarter read), the next block's first columns on
-// their way while the last ones are added (407), all of a warp's results staged at once in place of
-// the fifth ring slot (405), 16 epilogue warps (433), one-CTA tiles (522).
+// cores need 512: 8192^3 takes 369 to 378 us, GPU by GPU (2.9 to 3.0 PFLOP/s).  16 epilogue warps of
+// 64 columns take 394 where eight take 378.  With one multiply-add a value it took 380, and 321 with a
+// quarter of the columns read; tried then and not faster: four accumulators of 128 columns, half a
+// tile each (382 us; 313 with a quarter read), the next block's first columns on their way while the
+// last ones are added (407), all of a warp's results staged at once in place of the fifth ring slot
+// (405), one-CTA tiles (522).
 //
 // The tiles of a last, partly empty round run as two half-width items each.  192-wide tiles are for
 // shapes of few tiles, which 256-wide ones spread over fewer pairs (1021 x 2560 x 7168: 56 tiles on
