@@ -2,20 +2,22 @@
 // residual's addition) and quant_fp8 (as they are, or act(gate) * x).
 //
 // Quantisation of one block of 128 values y (the last block of a row may be shorter):
-// top = max(max|y|, 2^-100), scale = top * fl(1/448), q = e4m3(y * (1 / scale)), rounded to
-// nearest even; the product is within 2^-22 of y / scale before that rounding, and at most 448
-// up to roundings that the conversion's saturation takes back.  The floor keeps 1 / scale finite
-// for rows of zeros.  A NaN stays a NaN of its own; an infinity makes the scale infinite,
-// so that its whole block stands for NaN.
+// top = max(max|y|, 2^-100), scale = top * fl(1/448), q = e4m3(y * 448 / top), rounded to nearest
+// even.  With 16-bit values on both sides of the quotient exact ties are common (0.5 % of normally
+// distributed bf16 values), and a factor 448 / top of 24 bits puts a fifth of them on the wrong
+// side: it is held in two parts, so that the quotient is off by 2^-45 before its rounding to fp32 and
+// a tie stays one.  The floor keeps the factor finite for rows of zeros.  A NaN stays a NaN of its
+// own; an infinity makes the scale infinite, so that its whole block stands for NaN.
 //
 // A thread moves 16-byte pieces of 8 values; 16 neighbouring threads hold a block and find its
 // largest value by shuffles.  The norm holds a row in registers between the sum of squares and
 // the scaling, so each value is read once and written once.
 //
-// What bounds it: memory for prompts (quant_fp8 of 8192 x 14336: 53 us, the measured copy rate; gated
-// by silu 91 us, 96 %; by gelu 102 us, 86 %, where instructions count; rms_norm_fp8 of 8191 x 8128 with
-// a residual and 16-bit output 94 us, 95 %; 16384 x 4096 with a residual 79 us, 89 %), the launch for a
-// decode step's rows (1.5 to 2.5 us).
+// What bounds it: memory for prompts (quant_fp8 of 8192 x 14336: 55 us, 97 % of the measured copy rate; gated
+// by silu 91 us, 96 %; by gelu 103 us, 85 %, where instructions count; rms_norm_fp8 of 8191 x 8128 with
+// a residual and 16-bit output 96.5 us, 93 %; 16384 x 4096 with a residual 80.6 us, 87 %; with a factor in one
+// part and the row's factor in every value 53.7, 94.2 and 78.4 us), the launch for a decode step's rows
+// (1.5 to 2.5 us).
 #include <cuda_fp8.h>
 
 #include <cstring>
@@ -71,23 +73,41 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
     asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-__device__ __forceinline__ float top_of(const float2 (&f)[4]) {
+__device__ __forceinline__ float top_of(const float2 (&f)[4], float least) {
     const float t = max3_abs(f[0].x, f[0].y, f[1].x), u = max3_abs(f[1].y, f[2].x, f[2].y);
-    return max3_abs(max3_abs(t, u, f[3].x), f[3].y, kTinyTop);
+    return max3_abs(max3_abs(t, u, f[3].x), f[3].y, least);
 }
 
-__device__ __forceinline__ uint2 to_e4m3(const float2 (&f)[4], float inv) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = __nv_cvt_float2_to_fp8x2(__fmul2_rn(f[i], make_float2(inv, inv)), __NV_SATFINITE, __NV_E4M3);
-    return make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410));
-}
-
-// 1 / x to about half a step more than rounding, for normal x of up to 2^126.
+// 1 / x to a step, for x of 2^-126 to 2^126.
 __device__ __forceinline__ float reciprocal(float x) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return fmaf(fmaf(-x, r, 1.0f), r, r);
+    return r;
+}
+
+// 448 / top as hi + lo, for a top whose scale (top / 448, to some steps) is s.  hi is off by some steps, and
+// what it lacks is known: 448 - hi * top is exact but for one rounding.  (By way of s no top, up to the
+// largest fp32 value, takes the quotient out of the range of normal numbers.)  In one part it is rounded once.
+struct Factor {
+    float hi, lo;
+};
+template <bool TWO>
+__device__ __forceinline__ Factor factor_of(float top, float s) {
+    const float r = reciprocal(s), lacks = fmaf(-r, top, kE4m3Max), unit = r * (1.0f / kE4m3Max);
+    if (TWO) return {r, lacks * unit};
+    return {fmaf(lacks, unit, r), 0.0f};
+}
+
+template <bool TWO>
+__device__ __forceinline__ uint2 to_e4m3(const float2 (&f)[4], Factor k) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 hi = make_float2(k.hi, k.hi), lo = make_float2(k.lo, k.lo);
+        const float2 v = TWO ? __ffma2_rn(f[i], hi, __fmul2_rn(f[i], lo)) : __fmul2_rn(f[i], hi);
+        w[i] = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+    }
+    return make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410));
 }
 
 struct RowsOut {
@@ -97,16 +117,19 @@ struct RowsOut {
 };
 
 // The block's scale and the piece's fp8 values; `group` lanes (16, or a row's 8) hold the block.
-// q and scale: where they go, used only if `write`.
-__device__ __forceinline__ void quantise_piece(uint8_t *q, float *scale, int piece, const float2 (&f)[4], int group, bool write) {
-    float top = top_of(f);
+// least: the smallest top; what f stands for is f * unit (1 but for the norm).
+// TWO: a factor in two parts.  q and scale: where they go, used only if `write`.
+template <bool TWO>
+__device__ __forceinline__ void quantise_piece(uint8_t *q, float *scale, int piece, const float2 (&f)[4], int group, bool write,
+                                               float least = kTinyTop, float unit = 1.0f) {
+    float top = top_of(f, least);
 #pragma unroll
     for (int x = 1; x < 16; x <<= 1)
         if (x < group) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
     const float s = top * (1.0f / kE4m3Max);
     if (!write) return;
-    *reinterpret_cast<uint2 *>(q) = to_e4m3(f, reciprocal(s));
-    if ((piece & 15) == 0) *scale = s;
+    *reinterpret_cast<uint2 *>(q) = to_e4m3<TWO>(f, factor_of<TWO>(top, s));
+    if ((piece & 15) == 0) *scale = s * unit;
 }
 
 // 1 / (1 + exp(-t)) of two values, to some 1.5 steps of fp32: the exponential's argument is taken in
@@ -143,8 +166,12 @@ struct QuantArgs {
     FastDiv padded;   // pieces of a row rounded up to whole blocks of 16
 };
 
+// Registers for full SMs (silu took 38 without a bound: 106 us for 8192 x 14336 instead of 91), but for gelu, which
+// loses more to fewer registers (104.7 us) than to fewer threads (103.0).
+constexpr int quant_resident(int gate) { return gate == kGateGelu ? 6 : 8; }
+
 template <typename T, int GATE>
-__global__ void __launch_bounds__(kQuantThreads) quant_fp8_kernel(const QuantArgs a) {
+__global__ void __launch_bounds__(kQuantThreads, quant_resident(GATE)) quant_fp8_kernel(const QuantArgs a) {
     griddep_launch_dependents();
     griddep_wait();
     const uint32_t base = blockIdx.x * (kQuantThreads * kQuantUnroll) + threadIdx.x;
@@ -182,7 +209,7 @@ __global__ void __launch_bounds__(kQuantThreads) quant_fp8_kernel(const QuantArg
                 f[i] = __fmul2_rn(f[i], __fmul2_rn(h[i], sigmoid(t)));
             }
         }
-        quantise_piece(a.out.q + row[u] * a.out.q_row + piece[u] * 8, a.out.scales + row[u] * a.out.s_row + (piece[u] >> 4) * a.out.s_block, piece[u], f, 16, have[u]);
+        quantise_piece<GATE == kGateNone>(a.out.q + row[u] * a.out.q_row + piece[u] * 8, a.out.scales + row[u] * a.out.s_row + (piece[u] >> 4) * a.out.s_block, piece[u], f, 16, have[u]);
     }
 }
 
@@ -273,7 +300,13 @@ __global__ void __maxnreg__(norm_registers(VPT, RES)) rms_norm_fp8_kernel(const 
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         }
+        // The row's factor as a power of two, which enters the values, and a rest of 1 .. 2, which divides out of the
+        // quotients: values times weights of 16 bits are exact, and so are the ties between them.
         const float k = rsqrtf(fmaf(sum, a.inv_width, a.eps));
+        const bool finite = k < __int_as_float(0x7f800000);  // (a row with a NaN, or zeros with eps = 0, stands for NaN)
+        const float k2 = finite ? __int_as_float(__float_as_int(k) & 0x7f800000) : k;
+        const float rest = finite ? __int_as_float((__float_as_int(k) & 0x007fffff) | 0x3f800000) : 1.0f;
+        const float least = kTinyTop * reciprocal(rest);
         uint8_t *q = a.out.q + row * a.out.q_row + r * 8;
         float *scale = a.out.scales + row * a.out.s_row + (r >> 4) * a.out.s_block;
 #pragma unroll
@@ -295,9 +328,13 @@ __global__ void __maxnreg__(norm_registers(VPT, RES)) rms_norm_fp8_kernel(const 
             }
             // (pieces past the row are zeros throughout)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = __fmul2_rn(__fmul2_rn(f[i], make_float2(k, k)), h[i]);
-            if (a.out16 && have) *reinterpret_cast<uint4 *>(a.out16 + row * a.o_row + piece * 16) = from_f32<T>(f);
-            quantise_piece(q + u * per * 8, scale + (u * per >> 4) * a.out.s_block, piece, f, per < 16 ? per : 16, have);
+            for (int i = 0; i < 4; ++i) f[i] = __fmul2_rn(__fmul2_rn(f[i], make_float2(k2, k2)), h[i]);
+            if (a.out16 && have) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) h[i] = __fmul2_rn(f[i], make_float2(rest, rest));
+                *reinterpret_cast<uint4 *>(a.out16 + row * a.o_row + piece * 16) = from_f32<T>(h);
+            }
+            quantise_piece<true>(q + u * per * 8, scale + (u * per >> 4) * a.out.s_block, piece, f, per < 16 ? per : 16, have, least, rest);
         }
         if (!kAhead) load(row + step);
     }
