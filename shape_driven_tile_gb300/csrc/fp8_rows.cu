@@ -132,17 +132,19 @@ __device__ __forceinline__ void quantise_piece(uint8_t *q, float *scale, int pie
     if ((piece & 15) == 0) *scale = s * unit;
 }
 
-// 1 / (1 + exp(-t)) of two values, to some 1.5 steps of fp32: the exponential's argument is taken in
-// two parts (a rounded one alone is off by |t| steps), the reciprocal gets a Newton step.  (Values
-// next to a border of the fp8 grid fall on its other side as often as such errors reach it; without
-// these two steps twice as many did.)  Past +-87.5 it is 1 or 0; a NaN counts as infinity here.
+// 1 / (1 + exp(-t)) of two values, to some 1.5 steps of fp32 whatever t: with n = -t and x the rounded n / ln 2,
+// exp(n) = 2^x * exp(n - x ln 2), and the rest in brackets (at most 1e-5, so that 1 + rest is its exponential) is
+// taken with ln 2 in two parts; the reciprocal gets a Newton step.  (Values next to a border of the fp8 grid
+// fall on its other side as often as such errors reach it; with a rounded argument alone, which is off by |t|
+// steps, and no Newton step twice as many did.)  Past +-87.5 it is 1 or 0; a NaN counts as infinity here.
 __device__ __forceinline__ float2 sigmoid(float2 t) {
-    const float2 c = make_float2(fminf(fmaxf(t.x, -87.5f), 87.5f), fminf(fmaxf(t.y, -87.5f), 87.5f));
-    const float2 x = __fmul2_rn(c, make_float2(1.44269504f, 1.44269504f));
-    const float2 rest = __fmul2_rn(__ffma2_rn(c, make_float2(-1.44269504f, -1.44269504f), x), make_float2(0.6931472f, 0.6931472f));
+    constexpr float kLn2Hi = 0.693147182f, kLn2Lo = -1.90465421e-9f;  // together ln 2 to 2^-53
+    const float2 n = make_float2(fminf(fmaxf(-t.x, -87.5f), 87.5f), fminf(fmaxf(-t.y, -87.5f), 87.5f));
+    const float2 x = __fmul2_rn(n, make_float2(1.44269504f, 1.44269504f));
+    const float2 rest = __ffma2_rn(x, make_float2(-kLn2Lo, -kLn2Lo), __ffma2_rn(x, make_float2(-kLn2Hi, -kLn2Hi), n));
     float2 e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(-x.x));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(-x.y));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(x.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(x.y));
     e = __ffma2_rn(e, rest, e);
     const float2 minus_one = make_float2(-1.0f, -1.0f), minus_d = __ffma2_rn(e, minus_one, minus_one);
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(-minus_d.x));
