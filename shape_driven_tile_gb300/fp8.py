@@ -21,8 +21,8 @@ FP8_CODES = {torch.float8_e4m3fn: 4, torch.float8_e5m2: 5}
 ROW_CODES = {torch.float16: 0, torch.bfloat16: 1}
 ACTIVATIONS = {"silu": 1, "gelu": 2}
 
-# sdt_gemm_fp8, sdt_quant_fp8 and sdt_rms_norm_fp8 (include/sdt.h)
-_GEMM, _QUANT, _NORM = struct.Struct("5P10q5i"), struct.Struct("4P7q2i"), struct.Struct("6P8qf2i")
+# sdt_gemm_fp8, sdt_quant_fp8 and sdt_rms_norm_fp8 (include/sdt.h; "0q" is C's padding at the end)
+_GEMM, _QUANT, _NORM = struct.Struct("5P10q5i0q"), struct.Struct("4P7q2i0q"), struct.Struct("6P8qf2i0q")
 _current_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 _F32, _E4M3 = torch.float32, torch.float8_e4m3fn

@@ -18,7 +18,7 @@ VALUE_CODES = {torch.float16: 0, torch.bfloat16: 1}
 POSITION_BYTES = {torch.int32: 4, torch.int64: 8}
 SCALINGS = ("none", "linear", "base", "ramp", "smooth")
 # sdt_rope_qk (include/sdt.h)
-_ROPE = struct.Struct("6P13qf4i")
+_ROPE = struct.Struct("6P13qf4i0q")
 
 
 def rope_frequencies(rotary: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
