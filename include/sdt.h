@@ -583,8 +583,8 @@ size_t sdt_paged_attn_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t
  * blocks b of 128 consecutive k (the last one may be shorter).  A: M x K, W: N x K ("K-major",
  * as gemv_m1's), e4m3 or e5m2 each (SDT_DTYPE_E4M3 / _E5M2); scales fp32 of any strides; C:
  * M x N fp16, bf16 or fp32.  Block sums are formed on the tensor cores, scaled and added in
- * fp32, and rounded once to C's type.  Results depend on the shape (which decides the tile and
- * how k is shared out) but not on timing.  A NaN among a row's values or scales makes that row
+ * fp32, and rounded once to C's type.  Results depend on the shape and on whether rows of A and W
+ * start at multiples of 32 bytes (which decide the tile and how k is shared out) but not on timing.  A NaN among a row's values or scales makes that row
  * (of W: that column) of C NaN; memory outside the operands is not read.  C must not overlap them.
  *
  * Any M, K >= 0 (M == 0 or N == 0: no-op; K == 0 writes zeros); N a multiple of 8; dimensions
@@ -608,7 +608,10 @@ typedef struct sdt_gemm_fp8 {
     int a_dtype, w_dtype, c_dtype, tile, splits;
 } sdt_gemm_fp8;
 int gemm_fp8(const sdt_gemm_fp8 *call, sdt_stream_t stream);
-/* The tile and splits that gemm_fp8 picks on a GPU with sm_count SMs; needs no GPU. */
+/* The tile and splits that gemm_fp8 takes for a call on a GPU with sm_count SMs (M, N and K at least 1;
+ * nothing is followed or enqueued, and no GPU is needed). */
+int sdt_gemm_fp8_plan_call(const sdt_gemm_fp8 *call, int sm_count, int *tile, int *splits);
+/* The same for sizes alone: rows of K rounded up to 16, from bases at multiples of 32 bytes. */
 int sdt_gemm_fp8_plan_for(int64_t M, int64_t N, int64_t K, int sm_count, int *tile, int *splits);
 
 /*

@@ -88,6 +88,7 @@ SIGNATURES = {
     "paged_attn_m1": (cint, [vp, vp]),  # a packed sdt_paged_attn
     "sdt_paged_attn_workspace_bytes": (ctypes.c_size_t, [i64, i64, i64]),
     "gemm_fp8": (cint, [vp, vp]),  # a packed sdt_gemm_fp8
+    "sdt_gemm_fp8_plan_call": (cint, [vp, cint, ctypes.POINTER(cint), ctypes.POINTER(cint)]),  # a packed sdt_gemm_fp8
     "sdt_gemm_fp8_plan_for": (cint, [i64, i64, i64, cint, ctypes.POINTER(cint), ctypes.POINTER(cint)]),
     "quant_fp8": (cint, [vp, vp]),  # a packed sdt_quant_fp8
     "rms_norm_fp8": (cint, [vp, vp]),  # a packed sdt_rms_norm_fp8

@@ -48,15 +48,18 @@ static int fp8_splits(int tile, int64_t tiles, int64_t kb, int sm_count) {
 // The tile: up to 64 tokens the smallest that holds them (larger ones are mostly empty rows), above
 // that the smallest of four estimates in microseconds, fitted to measured shapes: a block takes a
 // CTA of 64 tokens 0.50 beside another one, a CTA of 128 alone 0.29, a two-CTA tile 0.40 (0.33 if it
-// is 192 wide, 0.29 as half-width items).  Rows that are not whole 32-byte sectors cost the first two,
-// which load most per product, 22 % more (333 x 5000 with k of 4224: 20.7, 14.5, 15.9, 18.4; with 4208:
-// 25.3, 17.5, 16.4, 18.7).  Measured with 64, 128, 192 and 256: 96 x 4096 x 4096 8.5, 8.2, 13.4, 12.5;
+// is 192 wide, 0.29 as half-width items).  Where rows of both operands start within 32-byte sectors, the
+// first two, which load most per product, cost 22 % more: whether they do follows from the rows' pitch and
+// the bases, not from K (333 x 5000 x 4208 with 64, 128, 192 and 256, rows 4208 apart: 22.7, 16.8, 15.5, 17.9; 4224
+// apart 19.6, 13.7, 14.9, 17.7; A alone 4208 apart 19.6, 14.4, 15.2, 17.7; W alone 19.9, 14.2, 15.1, 17.7; 4224 apart
+// from bases in the middle of a sector 24.8, 18.2, 16.7, 19.1; 512 x 4096 x 4096 with rows 4112 apart 22.0, 16.5, 14.9,
+// 14.0, in whole sectors 18.6, 13.2, 13.9, 13.3).  Measured with 64, 128, 192 and 256: 96 x 4096 x 4096 8.5, 8.2, 13.4, 12.5;
 // 256 x 4096 x 4096 12.4, 10.5, 13.7, 12.7; 96 x 4096 x 14336 18.0, 16.9, 38.3, 35.7; 512 x 4096 x 4096
 // 19.0, 13.4, 14.3, 13.5; 700 x 4096 x 14336 87, 68, 39.6, 46.9; 1021 x 2560 x 7168 47, 38, 22.1, 26.1;
 // 1021 x 12288 x 4096 96, 78, 48.6, 45.1.  Over 48 shapes of 96 to 1021 tokens the choice is 0.1 % slower
 // than the best on average, 4 % at worst.
-// `tile`: 0, or the tile that the caller asks for.
-static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int sm_count, int tile = 0) {
+// broken: whether rows of both operands start within sectors.  `tile`: 0, or the tile that the caller asks for.
+static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int sm_count, bool broken, int tile = 0) {
     const int64_t kb = (K + kFp8Block - 1) / kFp8Block;
     const auto tiles = [&](int t) { return ((M + t - 1) / t) * ((N + 127) / 128); };
     if (tile == 0) tile = M <= 16 ? 16 : M <= 32 ? 32 : 64;
@@ -65,7 +68,7 @@ static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int sm_count, int tile 
     Fp8Plan best{tile, fp8_splits(tile, tiles(tile), kb, sm_count)};
     if (M <= 64) return best;
     const auto blocks = [&](int splits) { return double((kb + splits - 1) / splits); };
-    const double sectors = K % 32 ? 1.22 : 1.0;
+    const double sectors = broken ? 1.22 : 1.0;
     double least = 3.5 + 0.50 * sectors * blocks(best.splits) * std::max(1.0, double(tiles(64)) * best.splits / (2 * sm_count));
     const int splits = fp8_splits(128, tiles(128), kb, sm_count);
     const double alone = 3.5 + 0.29 * sectors * blocks(splits) * double((tiles(128) * splits + sm_count - 1) / sm_count);
@@ -83,6 +86,20 @@ static Fp8Plan fp8_plan(int64_t M, int64_t N, int64_t K, int sm_count, int tile 
         }
     }
     return best;
+}
+
+// The stride of rows of k 8-bit values that lie behind one another.
+static int64_t fp8_packed_row(int64_t k) { return (k + 15) / 16 * 16; }
+
+// The plan of a checked call of at least one row, column and k.
+static Fp8Plan fp8_plan(const sdt_gemm_fp8 &c, int sm_count) {
+    const auto broken = [](const void *p, int64_t rows, int64_t stride) {
+        return reinterpret_cast<uintptr_t>(p) % 32 != 0 || (rows > 1 && stride % 32 != 0);
+    };
+    Fp8Plan plan = fp8_plan(c.M, c.N, c.K, sm_count, broken(c.a, c.M, c.lda) && broken(c.w, c.N, c.ldw), c.tile);
+    if (c.splits && plan.tile <= 128) plan.splits = c.splits;
+    plan.splits = int(std::min<int64_t>(plan.splits, (c.K + kFp8Block - 1) / kFp8Block));
+    return plan;
 }
 
 static bool is_fp8(int t) { return t == SDT_DTYPE_E4M3 || t == SDT_DTYPE_E5M2; }
@@ -178,7 +195,22 @@ int sdt_gemm_fp8_plan_for(int64_t M, int64_t N, int64_t K, int sm_count, int *ti
     if (!tile || !splits) return fail(SDT_ERR_NULL, "NULL output pointer");
     if (M < 1 || N < 1 || K < 1 || M > kFp8MaxDim || N > kFp8MaxDim || K > kFp8MaxDim || sm_count < 1 || sm_count > kFp8MaxSms)
         return fail(SDT_ERR_SHAPE, "M, N, K must be in 1 .. 2^30, sm_count in 1 .. 65536");
-    const Fp8Plan p = fp8_plan(M, N, K, sm_count);
+    const Fp8Plan p = fp8_plan(M, N, K, sm_count, fp8_packed_row(K) % 32 != 0);
+    *tile = p.tile;
+    *splits = p.splits;
+    return SDT_OK;
+}
+
+int sdt_gemm_fp8_plan_call(const sdt_gemm_fp8 *call, int sm_count, int *tile, int *splits) {
+    clear_error();
+    if (!call || !tile || !splits) return fail(SDT_ERR_NULL, "gemm_fp8: NULL call or output pointer");
+    sdt_gemm_fp8 c;
+    memcpy(&c, call, sizeof c);
+    const int rc = check_fp8(c);
+    if (rc) return rc;
+    if (c.M < 1 || c.N < 1 || c.K < 1 || sm_count < 1 || sm_count > kFp8MaxSms)
+        return fail(SDT_ERR_SHAPE, "M, N, K must be at least 1, sm_count in 1 .. 65536");
+    const Fp8Plan p = fp8_plan(c, sm_count);
     *tile = p.tile;
     *splits = p.splits;
     return SDT_OK;
@@ -196,8 +228,7 @@ int gemm_fp8(const sdt_gemm_fp8 *call, sdt_stream_t stream_h) {
     if (rc) return rc;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_h);
     // a dimension of one never steps: its stride may be anything
-    const auto up16 = [](int64_t k) { return (k + 15) / 16 * 16; };
-    const int64_t lda = c.M > 1 ? c.lda : up16(c.K), ldw = c.N > 1 ? c.ldw : up16(c.K), ldc = c.M > 1 ? c.ldc : c.N;
+    const int64_t lda = c.M > 1 ? c.lda : fp8_packed_row(c.K), ldw = c.N > 1 ? c.ldw : fp8_packed_row(c.K), ldc = c.M > 1 ? c.ldc : c.N;
     const size_t size = c.c_dtype == SDT_DTYPE_F32 ? 4 : 2;
     if (c.K == 0) {
         const cudaError_t e = cudaMemset2DAsync(c.c, size_t(ldc) * size, 0, size_t(c.N) * size, size_t(c.M), stream);
@@ -222,9 +253,7 @@ int gemm_fp8(const sdt_gemm_fp8 *call, sdt_stream_t stream_h) {
     a.timeout_ns = wait_timeout_ns();
     rc = status_word(&a.status);
     if (rc) return rc;
-    Fp8Plan plan = fp8_plan(c.M, c.N, c.K, dev.sm_count, c.tile);
-    if (c.splits) plan.splits = c.splits;
-    plan.splits = std::min(plan.splits, a.num_kb);
+    const Fp8Plan plan = fp8_plan(c, dev.sm_count);
     if (plan.tile > 128) return run_pair(c, plan.tile, a, lda, ldw, dev, stream);
     return run_swap(c, plan, a, lda, ldw, stream);
 }

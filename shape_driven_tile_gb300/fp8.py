@@ -115,10 +115,18 @@ def gemm_fp8(a, a_scales, w, w_scales, out=None, *, out_dtype=torch.bfloat16, ti
     return out
 
 
-def gemm_fp8_plan(M: int, N: int, K: int, sm_count: int = 152) -> tuple[int, int]:
-    """(tile, splits) that gemm_fp8 picks on a GPU with sm_count SMs; no GPU needed."""
+def gemm_fp8_plan(M: int, N: int, K: int, sm_count: int = 152, *, lda: int | None = None, ldw: int | None = None) -> tuple[int, int]:
+    """(tile, splits) that gemm_fp8 picks on a GPU with sm_count SMs; no GPU needed.  lda, ldw: elements from row to row of
+    a and w (None: K rounded up to 16); tensors start at multiples of 32 bytes here."""
     tile, splits = ctypes.c_int(), ctypes.c_int()
-    check(lib().sdt_gemm_fp8_plan_for(M, N, K, _integer("sm_count", sm_count), ctypes.byref(tile), ctypes.byref(splits)))
+    at = ctypes.byref(tile), ctypes.byref(splits)
+    if lda is None and ldw is None:
+        check(lib().sdt_gemm_fp8_plan_for(M, N, K, _integer("sm_count", sm_count), *at))
+    else:
+        row, blocks, p = -(-K // 16) * 16, -(-K // BLOCK), 4096  # (an address that nothing follows)
+        call = _GEMM.pack(p, p, p, p, p, M, N, K, row if lda is None else lda, row if ldw is None else ldw, N, blocks, 1, blocks, 1,
+                          FP8_CODES[_E4M3], FP8_CODES[_E4M3], OUT_CODES[torch.bfloat16], 0, 0)
+        check(lib().sdt_gemm_fp8_plan_call(call, _integer("sm_count", sm_count), *at))
     return tile.value, splits.value
 
 
