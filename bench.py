@@ -737,7 +737,7 @@ def step_working_set():
 
 
 SOURCES = {  # the CUDA sources each recorded kernel is built from
-    "gemm": lambda name: name.startswith("gemm") or name in ("ptx.cuh", "launch.cuh"),
+    "gemm": lambda name: (name.startswith("gemm") and not name.startswith("gemm_fp8")) or name in ("ptx.cuh", "launch.cuh", "tensor_map.cuh"),
     "gemv": lambda name: name in ("gemv.cu", "ptx.cuh", "launch.cuh"),
 }
 
