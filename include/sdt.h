@@ -585,7 +585,8 @@ size_t sdt_paged_attn_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t
  * M x N fp16, bf16 or fp32.  Block sums are formed on the tensor cores, scaled and added in
  * fp32, and rounded once to C's type.  Results depend on the shape and on whether rows of A and W
  * start at multiples of 32 bytes (which decide the tile and how k is shared out) but not on timing.  A NaN among a row's values or scales makes that row
- * (of W: that column) of C NaN; memory outside the operands is not read.  C must not overlap them.
+ * (of W: that column) of C NaN; memory outside the operands is not read.  C must not
+ * overlap them or the scales (slices of the same rows do not).
  *
  * Any M, K >= 0 (M == 0 or N == 0: no-op; K == 0 writes zeros); N a multiple of 8; dimensions
  * up to 2^30.  A, W and C 16-byte aligned, lda and ldw (elements) multiples of 16 at least K,
@@ -626,7 +627,7 @@ int sdt_gemm_fp8_plan_for(int64_t M, int64_t N, int64_t K, int sm_count, int *ti
  * x and gate: fp16 or bf16 (dtype), 16-byte aligned, row strides multiples of 8 (they may be
  * slices of one row, as a product writes them side by side); q: e4m3, 8-byte aligned, row
  * stride a multiple of 8; scales: fp32 of any strides.  The outputs must not overlap the inputs
- * or each other.
+ * or each other (SDT_ERR_ARG; slices of the same rows do not).
  */
 typedef struct sdt_quant_fp8 {
     const void *x, *gate; /* gate: NULL with activation 0 */
@@ -647,8 +648,8 @@ int quant_fp8(const sdt_quant_fp8 *call, sdt_stream_t stream);
  * x, residual, out: fp16 or bf16 (dtype), 16-byte aligned, row strides multiples of 8; weight:
  * x's type or fp32 (weight_dtype), 16-byte aligned; width up to 32768; sizes and outputs
  * otherwise as quant_fp8.
- * The outputs must not overlap the inputs or each other (residual is updated in place).  The order
- * of a row's sum follows from width and tokens, not from timing.
+ * The outputs must not overlap the inputs or each other (residual is updated in place and must not
+ * overlap x; SDT_ERR_ARG).  The order of a row's sum follows from width and tokens, not from timing.
  */
 typedef struct sdt_rms_norm_fp8 {
     const void *x, *weight;
@@ -671,7 +672,8 @@ int rms_norm_fp8(const sdt_rms_norm_fp8 *call, sdt_stream_t stream);
  * q, k, q_out, k_out: [tokens][heads][head_dim] fp16 or bf16 (dtype), head_dim contiguous, any
  * other strides in elements up to 2^32 (16-byte aligned heads are fastest); heads may be 0 (no
  * such side).
- * An output is its input itself or lies apart from both inputs and the other output.  positions: int32 or int64
+ * An output is its input itself or lies apart from both inputs, the other output, positions and turns
+ * (SDT_ERR_ARG; slices of the same rows lie apart).  positions: int32 or int64
  * (position_bytes 4 or 8); turns: uint64 [rotary / 2].  head_dim even, rotary even, at most
  * head_dim; tokens * heads * head_dim below 2^31.
  */

@@ -24,6 +24,7 @@
 #include <type_traits>
 
 #include "launch.cuh"
+#include "overlap.cuh"
 #include "paged.cuh"
 #include "ptx.cuh"
 
@@ -387,6 +388,22 @@ static int check_size(const char *who, int64_t tokens, int64_t width, int64_t wi
     return SDT_OK;
 }
 
+// The tensors of a call, outputs first: no output may share a byte with another of them.
+struct Tensor {
+    const char *name;
+    Stretches at;
+};
+template <int N>
+static int check_apart(const char *who, const Tensor (&all)[N], int outputs) {
+    for (int i = 0; i < outputs; ++i)
+        for (int j = i + 1; j < N; ++j)
+            if (overlap(all[i].at, all[j].at)) return fail(SDT_ERR_ARG, "%s: %s and %s overlap", who, all[i].name, all[j].name);
+    return SDT_OK;
+}
+static Stretches scales_of(const float *p, int64_t tokens, int64_t width, int64_t s_row, int64_t s_block) {
+    return {p, tokens, 4 * s_row, (width + 127) / 128, 4 * s_block, 4};
+}
+
 }  // namespace sdt
 
 using namespace sdt;
@@ -406,6 +423,9 @@ int quant_fp8(const sdt_quant_fp8 *call, sdt_stream_t stream) {
     rc = check_in("quant_fp8", "x", c.x, c.tokens, c.x_row, c.width);
     if (!rc && c.gate) rc = check_in("quant_fp8", "gate", c.gate, c.tokens, c.gate_row, c.width);
     if (!rc) rc = check_out("quant_fp8", c.q, c.scales, c.tokens, c.width, c.q_row, c.s_row, c.s_block);
+    if (rc) return rc;
+    rc = check_apart("quant_fp8", {{"q", rows_of(c.q, c.tokens, c.q_row, c.width)}, {"scales", scales_of(c.scales, c.tokens, c.width, c.s_row, c.s_block)},
+                                   {"x", rows_of(c.x, c.tokens, 2 * c.x_row, 2 * c.width)}, {"gate", rows_of(c.gate, c.tokens, 2 * c.gate_row, 2 * c.width)}}, 2);
     if (rc) return rc;
     rc = current_device(nullptr);
     if (rc) return rc;
@@ -440,6 +460,11 @@ int rms_norm_fp8(const sdt_rms_norm_fp8 *call, sdt_stream_t stream) {
     if (!rc && c.residual) rc = check_in("rms_norm_fp8", "residual", c.residual, c.tokens, c.r_row, c.width, true);
     if (!rc && c.out) rc = check_in("rms_norm_fp8", "out", c.out, c.tokens, c.o_row, c.width, true);
     if (!rc) rc = check_out("rms_norm_fp8", c.q, c.scales, c.tokens, c.width, c.q_row, c.s_row, c.s_block);
+    if (rc) return rc;
+    rc = check_apart("rms_norm_fp8", {{"q", rows_of(c.q, c.tokens, c.q_row, c.width)}, {"scales", scales_of(c.scales, c.tokens, c.width, c.s_row, c.s_block)},
+                                      {"residual", rows_of(c.residual, c.tokens, 2 * c.r_row, 2 * c.width)}, {"out", rows_of(c.out, c.tokens, 2 * c.o_row, 2 * c.width)},
+                                      {"x", rows_of(c.x, c.tokens, 2 * c.x_row, 2 * c.width)},
+                                      {"weight", rows_of(c.weight, 1, 0, (c.weight_dtype == SDT_DTYPE_F32 ? 4 : 2) * c.width)}}, 4);
     if (rc) return rc;
     NormArgs a{static_cast<const char *>(c.x), static_cast<char *>(c.residual), static_cast<const char *>(c.weight),
                static_cast<char *>(c.out), c.x_row * 2, c.r_row * 2, c.o_row * 2,

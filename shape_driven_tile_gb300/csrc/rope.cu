@@ -17,6 +17,7 @@
 #include <type_traits>
 
 #include "launch.cuh"
+#include "overlap.cuh"
 #include "paged.cuh"
 #include "ptx.cuh"
 
@@ -157,10 +158,8 @@ static int check_rope_side(const char *what, const void *in, const void *out, in
     for (int64_t s : {it, ih, ot, oh})
         if (s < 0 || s > kRopeMaxStride) return fail(SDT_ERR_ARG, "rope_qk: strides of %s must be in 0 .. 2^32", what);
     if (!apart(tokens, ot, heads, oh, d)) return fail(SDT_ERR_ARG, "rope_qk: tokens and heads of the output of %s must not overlap", what);
-    if (in == out && it == ot && ih == oh) return SDT_OK;
-    const auto lo = [](const void *p) { return reinterpret_cast<uintptr_t>(p); };
-    const uint64_t in_bytes = uint64_t((tokens - 1) * it + (heads - 1) * ih + d) * 2, out_bytes = uint64_t((tokens - 1) * ot + (heads - 1) * oh + d) * 2;
-    if (lo(in) < lo(out) + out_bytes && lo(out) < lo(in) + in_bytes)
+    const bool itself = in == out && it == ot && ih == oh;
+    if (!itself && overlap({in, tokens, 2 * it, heads, 2 * ih, 2 * d}, {out, tokens, 2 * ot, heads, 2 * oh, 2 * d}))
         return fail(SDT_ERR_ARG, "rope_qk: the output of %s must be %s itself or lie apart from it", what, what);
     return SDT_OK;
 }
@@ -189,12 +188,18 @@ extern "C" int rope_qk(const sdt_rope_qk *call, sdt_stream_t stream) {
         if ((i % 2 ? (i % 4 == 1 ? c.q_heads : c.k_heads) : c.tokens) == 1) step[i] = 0;
     int rc = c.q_heads ? check_rope_side("q", c.q, c.q_out, c.tokens, c.q_heads, c.head_dim, step[0], step[1], step[4], step[5]) : SDT_OK;
     if (!rc && c.k_heads) rc = check_rope_side("k", c.k, c.k_out, c.tokens, c.k_heads, c.head_dim, step[2], step[3], step[6], step[7]);
-    if (!rc && c.q_heads && c.k_heads && (c.q_out == c.k_out || c.q_out == c.k || c.k_out == c.q))
-        rc = fail(SDT_ERR_ARG, "rope_qk: the output of one side must not be the other side's tensor");
+    const auto side = [&](const void *p, int64_t heads, int i) {
+        return Stretches{p, c.tokens, 2 * step[i], heads, 2 * step[i + 1], 2 * c.head_dim};
+    };
+    const Stretches qo = side(c.q_out, c.q_heads, 4), ko = side(c.k_out, c.k_heads, 6);
+    if (!rc && c.q_heads && c.k_heads && (overlap(qo, ko) || overlap(qo, side(c.k, c.k_heads, 2)) || overlap(ko, side(c.q, c.q_heads, 0))))
+        rc = fail(SDT_ERR_ARG, "rope_qk: the output of one side must not overlap the other side's tensors");
     if (rc) return rc;
     if (c.rotary && (!c.positions || !c.turns)) return fail(SDT_ERR_NULL, "rope_qk: positions or turns is NULL");
     if (!aligned(c.positions, static_cast<uintptr_t>(c.position_bytes)) || !aligned(c.turns, 8))
         return fail(SDT_ERR_ALIGN, "rope_qk: positions and turns must be aligned to their elements");
+    for (const Stretches &in : {rows_of(c.positions, 1, 0, c.tokens * c.position_bytes), rows_of(c.turns, 1, 0, c.rotary / 2 * 8)})
+        if ((c.q_heads && overlap(qo, in)) || (c.k_heads && overlap(ko, in))) return fail(SDT_ERR_ARG, "rope_qk: an output overlaps positions or turns");
     rc = current_device(nullptr);
     if (rc) return rc;
     const bool in_place = (!c.q_heads || c.q == c.q_out) && (!c.k_heads || c.k == c.k_out);  // then the rest of a head stays as it is

@@ -71,8 +71,8 @@ def gemm_fp8(a, a_scales, w, w_scales, out=None, *, out_dtype=torch.bfloat16, ti
     a: [M, K] and w: [N, K] (K-major, as gemv_m1's W), float8_e4m3fn or float8_e5m2, rows
     contiguous and 16-byte aligned (padding allowed); N a multiple of 8.  a_scales: float32
     [M, ceil(K / 128)], w_scales: float32 [ceil(N / 128), ceil(K / 128)], any strides.  out:
-    [M, N] float16, bfloat16 or float32 (out_dtype if the call allocates it).  Sums are held in
-    float32.  tile, splits: 0 picks (include/sdt.h has the others).
+    [M, N] float16, bfloat16 or float32 (out_dtype if the call allocates it), apart from the
+    operands and scales.  Sums are held in float32.  tile, splits: 0 picks (include/sdt.h has the others).
     """
     try:
         dev, dtype = _current_device(), out_dtype if out is None else out.dtype
@@ -123,8 +123,8 @@ def gemm_fp8_plan(M: int, N: int, K: int, sm_count: int = 152, *, lda: int | Non
     if lda is None and ldw is None:
         check(lib().sdt_gemm_fp8_plan_for(M, N, K, _integer("sm_count", sm_count), *at))
     else:
-        row, blocks, p = -(-K // 16) * 16, -(-K // BLOCK), 4096  # (an address that nothing follows)
-        call = _GEMM.pack(p, p, p, p, p, M, N, K, row if lda is None else lda, row if ldw is None else ldw, N, blocks, 1, blocks, 1,
+        row, blocks, p = -(-K // 16) * 16, -(-K // BLOCK), 4096  # (addresses that nothing follows)
+        call = _GEMM.pack(p, p, p, p, 1 << 62, M, N, K, row if lda is None else lda, row if ldw is None else ldw, N, blocks, 1, blocks, 1,
                           FP8_CODES[_E4M3], FP8_CODES[_E4M3], OUT_CODES[torch.bfloat16], 0, 0)
         check(lib().sdt_gemm_fp8_plan_call(call, _integer("sm_count", sm_count), *at))
     return tile.value, splits.value
@@ -156,7 +156,8 @@ def quant_fp8(x, gate=None, *, activation: str = "silu", q=None, scales=None, st
     may be given), width a multiple of 8 up to 65536.  activation: "silu", or "gelu" (the tanh
     form); it counts only with a gate.  Returns (q, scales): float8_e4m3fn [tokens, width] and
     float32 [tokens, ceil(width / 128)] with x = q * scales, where a block's scale is its
-    largest absolute value / 448; q and scales may be given (scales with any strides).
+    largest absolute value / 448; q and scales may be given (scales with any strides).  No
+    output may overlap an input or another output.
     """
     try:
         dev, dtype = _current_device(), x.dtype
@@ -196,7 +197,8 @@ def rms_norm_fp8(x, weight, residual=None, *, eps: float = 1e-6, out=None, q=Non
     x, residual: float16 or bfloat16 [tokens, width], rows contiguous, width a multiple of 8 up
     to 32768; weight: [width] of x's type or float32.  With a residual, residual <- x + residual
     (rounded to its type, in place), and the norm is of that; without one it is of x.  out, if
-    given, receives the normalised values in x's type too.  Returns (q, scales) as quant_fp8.
+    given, receives the normalised values in x's type too.  Returns (q, scales) as quant_fp8.  No
+    output (residual among them) may overlap an input or another output.
     """
     try:
         dev, dtype = _current_device(), x.dtype

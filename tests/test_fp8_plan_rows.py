@@ -13,7 +13,7 @@ A = 0x10000
 def plan(m, n, k, lda, ldw, a=A, w=A, tile=0, splits=0, sms=152):
     kb = -(-k // 128)
     out = ctypes.c_int(), ctypes.c_int()
-    call = fp8._GEMM.pack(a, A, w, A, 64 * A, m, n, k, lda, ldw, n, kb, 1, kb, 1, 4, 4, 1, tile, splits)
+    call = fp8._GEMM.pack(a, A, w, A, 1 << 50, m, n, k, lda, ldw, n, kb, 1, kb, 1, 4, 4, 1, tile, splits)
     rc = sdt.lib().sdt_gemm_fp8_plan_call(call, sms, *(ctypes.byref(x) for x in out))
     return rc if rc else tuple(x.value for x in out)
 
