@@ -12,6 +12,15 @@ int launch_fp8_pair(const CUtensorMap &tmA, const CUtensorMap &tmB, const CUtens
     using Cfg = Fp8PairCfg<WIDTH>;
     static std::atomic<int> configured[64];
     if (int e = ensure_smem(gemm_fp8_pair_kernel<WIDTH>, Cfg::SMEM_BYTES, configured)) return e;
+    // The epilogue's warps wait until the launch's registers cover their share: a build whose kernel starts with
+    // fewer (the compiler may give fewer than the block's size allows) is not launched.
+    static std::atomic<bool> covered{false};
+    if (!covered.load(std::memory_order_relaxed)) {
+        cudaFuncAttributes has;
+        if (cudaError_t e = cudaFuncGetAttributes(&has, gemm_fp8_pair_kernel<WIDTH>)) return e;
+        if (has.numRegs * Cfg::THREADS < Cfg::SPLIT_REGS) return cudaErrorLaunchOutOfResources;
+        covered.store(true, std::memory_order_relaxed);
+    }
     return launch_kernel(gemm_fp8_pair_kernel<WIDTH>, dim3(2 * static_cast<unsigned>(pairs)), dim3(Cfg::THREADS), size_t(Cfg::SMEM_BYTES),
                          stream, 2, tmA, tmB, tmC, args);
 }

@@ -42,7 +42,8 @@ struct Fp8PairCfg {
     static constexpr int EPI_WARPS = 4 * PARTS, THREADS = 128 + 32 * EPI_WARPS;
     // registers of a thread: what the launch gives all, and after the roles have parted
     static constexpr int ROLE_REGS = 56, EPI_REGS = PARTS == 2 ? 224 : 152;
-    static_assert(128 * ROLE_REGS + 32 * EPI_WARPS * EPI_REGS <= THREADS * (65536 / THREADS / 8 * 8), "within the launch's registers");
+    static constexpr int SPLIT_REGS = 128 * ROLE_REGS + 32 * EPI_WARPS * EPI_REGS;
+    static_assert(SPLIT_REGS <= THREADS * (65536 / THREADS / 8 * 8), "within what a launch can have");
     static constexpr int ACC_BUFS = 2, ACC_STEP = 256, TMEM_COLS = ACC_BUFS * ACC_STEP;  // step: columns from one to the other
     static constexpr int COLS = BN / PARTS;  // columns of an epilogue thread
     static constexpr int C_STAGE_BYTES = EPI_WARPS * 2 * kCStageBytes;
