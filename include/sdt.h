@@ -582,19 +582,21 @@ size_t sdt_paged_attn_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t
  *   C[m][n] = sum_b a_scales[m][b] * w_scales[n / 128][b] * sum_{k in block b} A[m][k] * W[n][k],
  * blocks b of 128 consecutive k (the last one may be shorter).  A: M x K, W: N x K ("K-major",
  * as gemv_m1's), e4m3 or e5m2 each (SDT_DTYPE_E4M3 / _E5M2); scales fp32 of any strides; C:
- * M x N fp16, bf16 or fp32.  Block sums are formed on the tensor cores, scaled and added in
- * fp32, and rounded once to C's type.  Results depend on the shape and on whether rows of A and W
- * start at multiples of 32 bytes (which decide the tile and how k is shared out) but not on timing.  A NaN among a row's values or scales makes that row
- * (of W: that column) of C NaN; memory outside the operands is not read.  C must not
- * overlap them or the scales (slices of the same rows do not).
+ * M x N fp16, bf16 or fp32.  Block sums are formed on the tensor cores, multiplied by the product
+ * of both scales and added in fp32, and rounded once to C's type.  (That product is an fp32 number
+ * of its own: past fp32's range it is infinite, and below 2^-126 it has fewer bits.)  Results depend
+ * on the shape and on whether rows of A and W start at multiples of 32 bytes (which decide the tile
+ * and how k is shared out) but not on timing.  A NaN among a row's values or scales makes that row
+ * (of W: that column, of W's scales their 128 columns) of C NaN; memory outside the operands is not
+ * read.  C must not overlap them or the scales (slices of the same rows do not).
  *
  * Any M, K >= 0 (M == 0 or N == 0: no-op; K == 0 writes zeros); N a multiple of 8; dimensions
  * up to 2^30.  A, W and C 16-byte aligned, lda and ldw (elements) multiples of 16 at least K,
  * ldc a multiple of 8 at least N; a stride of a single row may be anything.  Scales 4-byte
  * aligned, strides not negative.
  * tile: 0 picks; 16, 32, 64 or 128 tokens per tile of 128 weight rows, whose blocks `splits`
- * (0 picks, 1 .. 8) CTAs share; 192 or 256: two-CTA tiles of 256 tokens by that many
- * outputs, which are not split.
+ * (0 picks, 1 .. 8; no more than blocks) CTAs share; 192 or 256: two-CTA tiles of 256 tokens by
+ * that many outputs, which are never split: `splits` counts for nothing there.
  * Errors: SDT_ERR_NULL, SDT_ERR_ALIGN, SDT_ERR_SHAPE (N, dimensions), SDT_ERR_ARG (types,
  * strides, splits), SDT_ERR_TILE.
  */
