@@ -112,6 +112,8 @@ def main():
     p.add_argument("--inner", type=int, default=14336)
     p.add_argument("--graph", action="store_true", help="capture one step and replay it")
     a = p.parse_args()
+    if min(a.batch, a.prompt, a.steps) < 1:
+        p.error("--batch, --prompt and --steps must be at least 1")
     layer = Layer(a.batch, a.prompt + a.steps, kv_heads=a.kv_heads, inner=a.inner)
     g = torch.Generator(device="cuda").manual_seed(1)
     prompts = [max(1, a.prompt - i * a.prompt // (2 * a.batch)) for i in range(a.batch)]
