@@ -169,9 +169,10 @@ struct QuantArgs {
     FastDiv padded;   // pieces of a row rounded up to whole blocks of 16
 };
 
-// Registers for full SMs (silu took 38 without a bound: 106 us for 8192 x 14336 instead of 91), but for gelu, which
-// loses more to fewer registers (104.7 us) than to fewer threads (103.0).
-constexpr int quant_resident(int gate) { return gate == kGateGelu ? 6 : 8; }
+// CTAs an SM holds, and so the registers of a thread: 8 of 32 registers are full SMs (silu without a bound: 38
+// registers and 106 us for 8192 x 14336, 91 with it); gelu's instructions are better off with 47 and five CTAs
+// (100.7 us; six 110, seven and eight 104.7, unbounded, 52 registers, 102.4).
+constexpr int quant_resident(int gate) { return gate == kGateGelu ? 5 : 8; }
 
 template <typename T, int GATE>
 __global__ void __launch_bounds__(kQuantThreads, quant_resident(GATE)) quant_fp8_kernel(const QuantArgs a) {
