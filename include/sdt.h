@@ -622,8 +622,9 @@ int sdt_gemm_fp8_plan_for(int64_t M, int64_t N, int64_t K, int sm_count, int *ti
  * top / 448 (fp32), top = max(max|y|, 2^-100) of the block of 128, with y = x, or act(gate) * x
  * (activation 1: silu, g / (1 + exp(-g)); 2: gelu's tanh form,
  * 0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3)))), computed in fp32.  q is the nearest e4m3
- * number and the even one of a tie, at most 448; a value within 2^-23 of a border between two
- * (with a gate: of y's own fp32 steps) may fall on its other side, but no exact tie of x does.  A NaN
+ * number and the even one of a tie, at most 448: without a gate exact ties of x are ties here.
+ * With one, y is known to some fp32 steps, and a value as near to a border between two e4m3 numbers
+ * may fall on its other side.  A NaN
  * stays a NaN of its own; a block that holds an infinity gets an infinite scale and stands for
  * NaN.  Width a multiple of 8 up to 65536; tokens times the width in whole blocks of 128 below 2^34 - 2^12.
  * x and gate: fp16 or bf16 (dtype), 16-byte aligned, row strides multiples of 8 (they may be
@@ -645,8 +646,8 @@ int quant_fp8(const sdt_quant_fp8 *call, sdt_stream_t stream);
  *   r = x + residual, rounded to their type and written back to residual (without one: r = x);
  *   y[t][i] = r[t][i] * weight[i] / sqrt(mean_j r[t][j]^2 + eps)      (fp32)
  * (squares are summed in fp32: a row with values past 1e18 may overflow, and is zeros or NaN then)
- * and q, scales of y as quant_fp8 makes them (in the quotients r * weight counts alone, exactly if
- * weight has 16 bits).  out, if not NULL, receives y rounded to x's type.
+ * and q, scales of y as quant_fp8 makes them with a gate.  out, if not NULL, receives y rounded to
+ * x's type.
  * x, residual, out: fp16 or bf16 (dtype), 16-byte aligned, row strides multiples of 8; weight:
  * x's type or fp32 (weight_dtype), 16-byte aligned; width up to 32768; sizes and outputs
  * otherwise as quant_fp8.

@@ -5,19 +5,21 @@
 // top = max(max|y|, 2^-100), scale = top * fl(1/448), q = e4m3(y * 448 / top), rounded to nearest
 // even.  With 16-bit values on both sides of the quotient exact ties are common (0.5 % of normally
 // distributed bf16 values), and a factor 448 / top of 24 bits puts a fifth of them on the wrong
-// side: it is held in two parts, so that the quotient is off by 2^-45 before its rounding to fp32 and
-// a tie stays one.  The floor keeps the factor finite for rows of zeros.  A NaN stays a NaN of its
+// side: without a gate it is held in two parts, so that the quotient is off by 2^-45 before its
+// rounding to fp32 and a tie stays one.  What a gate or the norm makes is itself off by some steps
+// of fp32 and takes one factor, rounded once.  (The norm's ties can be kept too: a row's factor divides
+// out of the quotients, and value times weight is exact.  It took 96.5 us for 94.5 and 48.8 for 45.9.)
+// The floor keeps the factor finite for rows of zeros.  A NaN stays a NaN of its
 // own; an infinity makes the scale infinite, so that its whole block stands for NaN.
 //
 // A thread moves 16-byte pieces of 8 values; 16 neighbouring threads hold a block and find its
 // largest value by shuffles.  The norm holds a row in registers between the sum of squares and
 // the scaling, so each value is read once and written once.
 //
-// What bounds it: memory for prompts (quant_fp8 of 8192 x 14336: 55 us, 97 % of the measured copy rate; gated
-// by silu 91 us, 96 %; by gelu 103 us, 85 %, where instructions count; rms_norm_fp8 of 8191 x 8128 with
-// a residual and 16-bit output 96.5 us, 93 %; 16384 x 4096 with a residual 80.6 us, 87 %; with a factor in one
-// part and the row's factor in every value 53.7, 94.2 and 78.4 us), the launch for a decode step's rows
-// (1.5 to 2.5 us).
+// What bounds it: memory for prompts (quant_fp8 of 8192 x 14336: 55 us, 97 % of the measured copy rate, 53.7 with
+// a factor in one part; gated by silu 91 us, 96 %; by gelu 101 us, 87 %, where instructions count; rms_norm_fp8 of
+// 8191 x 8128 with a residual and 16-bit output 94.5 us, 95 %; 16384 x 4096 with a residual 79 us, 89 %), the
+// launch for a decode step's rows (1.5 to 2.5 us).
 #include <cuda_fp8.h>
 
 #include <cstring>
@@ -74,9 +76,9 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
     asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-__device__ __forceinline__ float top_of(const float2 (&f)[4], float least) {
+__device__ __forceinline__ float top_of(const float2 (&f)[4]) {
     const float t = max3_abs(f[0].x, f[0].y, f[1].x), u = max3_abs(f[1].y, f[2].x, f[2].y);
-    return max3_abs(max3_abs(t, u, f[3].x), f[3].y, least);
+    return max3_abs(max3_abs(t, u, f[3].x), f[3].y, kTinyTop);
 }
 
 // 1 / x to a step, for x of 2^-126 to 2^126.
@@ -118,19 +120,17 @@ struct RowsOut {
 };
 
 // The block's scale and the piece's fp8 values; `group` lanes (16, or a row's 8) hold the block.
-// least: the smallest top; what f stands for is f * unit (1 but for the norm).
 // TWO: a factor in two parts.  q and scale: where they go, used only if `write`.
 template <bool TWO>
-__device__ __forceinline__ void quantise_piece(uint8_t *q, float *scale, int piece, const float2 (&f)[4], int group, bool write,
-                                               float least = kTinyTop, float unit = 1.0f) {
-    float top = top_of(f, least);
+__device__ __forceinline__ void quantise_piece(uint8_t *q, float *scale, int piece, const float2 (&f)[4], int group, bool write) {
+    float top = top_of(f);
 #pragma unroll
     for (int x = 1; x < 16; x <<= 1)
         if (x < group) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
     const float s = top * (1.0f / kE4m3Max);
     if (!write) return;
     *reinterpret_cast<uint2 *>(q) = to_e4m3<TWO>(f, factor_of<TWO>(top, s));
-    if ((piece & 15) == 0) *scale = s * unit;
+    if ((piece & 15) == 0) *scale = s;
 }
 
 // 1 / (1 + exp(-t)) of two values, to some 1.5 steps of fp32 whatever t: with n = -t and x the rounded n / ln 2,
@@ -304,13 +304,7 @@ __global__ void __maxnreg__(norm_registers(VPT, RES)) rms_norm_fp8_kernel(const 
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         }
-        // The row's factor as a power of two, which enters the values, and a rest of 1 .. 2, which divides out of the
-        // quotients: values times weights of 16 bits are exact, and so are the ties between them.
         const float k = rsqrtf(fmaf(sum, a.inv_width, a.eps));
-        const bool finite = k < __int_as_float(0x7f800000);  // (a row with a NaN, or zeros with eps = 0, stands for NaN)
-        const float k2 = finite ? __int_as_float(__float_as_int(k) & 0x7f800000) : k;
-        const float rest = finite ? __int_as_float((__float_as_int(k) & 0x007fffff) | 0x3f800000) : 1.0f;
-        const float least = kTinyTop * reciprocal(rest);
         uint8_t *q = a.out.q + row * a.out.q_row + r * 8;
         float *scale = a.out.scales + row * a.out.s_row + (r >> 4) * a.out.s_block;
 #pragma unroll
@@ -332,13 +326,9 @@ __global__ void __maxnreg__(norm_registers(VPT, RES)) rms_norm_fp8_kernel(const 
             }
             // (pieces past the row are zeros throughout)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = __fmul2_rn(__fmul2_rn(f[i], make_float2(k2, k2)), h[i]);
-            if (a.out16 && have) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) h[i] = __fmul2_rn(f[i], make_float2(rest, rest));
-                *reinterpret_cast<uint4 *>(a.out16 + row * a.o_row + piece * 16) = from_f32<T>(h);
-            }
-            quantise_piece<true>(q + u * per * 8, scale + (u * per >> 4) * a.out.s_block, piece, f, per < 16 ? per : 16, have, least, rest);
+            for (int i = 0; i < 4; ++i) f[i] = __fmul2_rn(__fmul2_rn(f[i], make_float2(k, k)), h[i]);
+            if (a.out16 && have) *reinterpret_cast<uint4 *>(a.out16 + row * a.o_row + piece * 16) = from_f32<T>(f);
+            quantise_piece<false>(q + u * per * 8, scale + (u * per >> 4) * a.out.s_block, piece, f, per < 16 ? per : 16, have);
         }
         if (!kAhead) load(row + step);
     }
