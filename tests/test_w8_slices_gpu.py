@@ -15,10 +15,11 @@ def part(rows, lo, hi, dtype):
 
 def test_rows_of_everything(cuda_device):
     """x, residual, 16-bit output, fp8 values and scales side by side."""
-    t, d, g = 700, 512, torch.Generator(device=cuda_device).manual_seed(1)
-    rows = torch.zeros((t, 3 * 1024 + 512 + 16 + 16), dtype=torch.uint8, device=cuda_device)
-    x, r, out = (part(rows, i * 1024, (i + 1) * 1024, torch.bfloat16) for i in range(3))
-    q, s = part(rows, 3072, 3584, E4M3), part(rows, 3584, 3600, torch.float32)
+    t, d, g = 700, 640, torch.Generator(device=cuda_device).manual_seed(1)
+    wide = 2 * d  # bytes of a row in 16 bits
+    rows = torch.zeros((t, 3 * wide + d + 5 * 4 + 12), dtype=torch.uint8, device=cuda_device)
+    x, r, out = (part(rows, i * wide, (i + 1) * wide, torch.bfloat16) for i in range(3))
+    q, s = part(rows, 3 * wide, 3 * wide + d, E4M3), part(rows, 3 * wide + d, 3 * wide + d + 5 * 4, torch.float32)
     x.copy_(torch.randn((t, d), generator=g, device=cuda_device))
     r.copy_(torch.randn((t, d), generator=g, device=cuda_device))
     w, r1, out1 = torch.ones(d, dtype=torch.bfloat16, device=cuda_device), r.clone(), torch.empty((t, d), dtype=torch.bfloat16, device=cuda_device)
@@ -27,7 +28,7 @@ def test_rows_of_everything(cuda_device):
     sdt.rms_norm_fp8(x, w, r, out=out, q=q, scales=s)
     for a, b in ((x, kept), (r, r1), (out, out1), (s, s1), (q.view(torch.uint8), q1.view(torch.uint8))):
         assert torch.equal(a, b)
-    assert (rows[:, 3600:] == 0).all()
+    assert (rows[:, 3 * wide + d + 5 * 4:] == 0).all()
     q1, s1 = sdt.quant_fp8(x.clone(), r.clone())
     sdt.quant_fp8(x, r, q=q, scales=s)
     assert torch.equal(q.view(torch.uint8), q1.view(torch.uint8)) and torch.equal(s, s1)
@@ -36,7 +37,7 @@ def test_rows_of_everything(cuda_device):
     with pytest.raises(sdt.SdtError, match="overlap"):
         sdt.rms_norm_fp8(x, w, x)
     with pytest.raises(sdt.SdtError, match="overlap"):
-        sdt.quant_fp8(x, q=part(rows, 512, 1024, E4M3))
+        sdt.quant_fp8(x, q=part(rows, d, 2 * d, E4M3))
 
 
 @pytest.mark.parametrize("m", [3, 300])
