@@ -393,7 +393,8 @@ static int check_apart(const char *who, const Tensor (&all)[N], int outputs) {
     return SDT_OK;
 }
 static Stretches scales_of(const float *p, int64_t tokens, int64_t width, int64_t s_row, int64_t s_block) {
-    return {p, tokens, 4 * s_row, (width + 127) / 128, 4 * s_block, 4};
+    const int64_t blocks = (width + 127) / 128;
+    return {p, tokens, step_bytes(tokens, s_row, 4), blocks, step_bytes(blocks, s_block, 4), 4};
 }
 
 }  // namespace sdt
@@ -417,12 +418,12 @@ int quant_fp8(const sdt_quant_fp8 *call, sdt_stream_t stream) {
     if (!rc) rc = check_out("quant_fp8", c.q, c.scales, c.tokens, c.width, c.q_row, c.s_row, c.s_block);
     if (rc) return rc;
     rc = check_apart("quant_fp8", {{"q", rows_of(c.q, c.tokens, c.q_row, c.width)}, {"scales", scales_of(c.scales, c.tokens, c.width, c.s_row, c.s_block)},
-                                   {"x", rows_of(c.x, c.tokens, 2 * c.x_row, 2 * c.width)}, {"gate", rows_of(c.gate, c.tokens, 2 * c.gate_row, 2 * c.width)}}, 2);
+                                   {"x", rows_of(c.x, c.tokens, step_bytes(c.tokens, c.x_row, 2), 2 * c.width)}, {"gate", rows_of(c.gate, c.tokens, step_bytes(c.tokens, c.gate_row, 2), 2 * c.width)}}, 2);
     if (rc) return rc;
     rc = current_device(nullptr);
     if (rc) return rc;
     const uint32_t padded = static_cast<uint32_t>((c.width + 127) / 128 * 16);
-    QuantArgs a{static_cast<const char *>(c.x), static_cast<const char *>(c.gate), c.x_row * 2, c.gate_row * 2,
+    QuantArgs a{static_cast<const char *>(c.x), static_cast<const char *>(c.gate), step_bytes(c.tokens, c.x_row, 2), step_bytes(c.tokens, c.gate_row, 2),
                 {static_cast<uint8_t *>(c.q), c.scales, c.q_row, c.s_row, c.s_block},
                 static_cast<uint32_t>(c.tokens) * padded, static_cast<int>(c.width / 8), FastDiv::of(padded)};
     constexpr uint32_t per_cta = kQuantThreads * kQuantUnroll;
@@ -454,12 +455,12 @@ int rms_norm_fp8(const sdt_rms_norm_fp8 *call, sdt_stream_t stream) {
     if (!rc) rc = check_out("rms_norm_fp8", c.q, c.scales, c.tokens, c.width, c.q_row, c.s_row, c.s_block);
     if (rc) return rc;
     rc = check_apart("rms_norm_fp8", {{"q", rows_of(c.q, c.tokens, c.q_row, c.width)}, {"scales", scales_of(c.scales, c.tokens, c.width, c.s_row, c.s_block)},
-                                      {"residual", rows_of(c.residual, c.tokens, 2 * c.r_row, 2 * c.width)}, {"out", rows_of(c.out, c.tokens, 2 * c.o_row, 2 * c.width)},
-                                      {"x", rows_of(c.x, c.tokens, 2 * c.x_row, 2 * c.width)},
+                                      {"residual", rows_of(c.residual, c.tokens, step_bytes(c.tokens, c.r_row, 2), 2 * c.width)}, {"out", rows_of(c.out, c.tokens, step_bytes(c.tokens, c.o_row, 2), 2 * c.width)},
+                                      {"x", rows_of(c.x, c.tokens, step_bytes(c.tokens, c.x_row, 2), 2 * c.width)},
                                       {"weight", rows_of(c.weight, 1, 0, (c.weight_dtype == SDT_DTYPE_F32 ? 4 : 2) * c.width)}}, 4);
     if (rc) return rc;
     NormArgs a{static_cast<const char *>(c.x), static_cast<char *>(c.residual), static_cast<const char *>(c.weight),
-               static_cast<char *>(c.out), c.x_row * 2, c.r_row * 2, c.o_row * 2,
+               static_cast<char *>(c.out), step_bytes(c.tokens, c.x_row, 2), step_bytes(c.tokens, c.r_row, 2), step_bytes(c.tokens, c.o_row, 2),
                {static_cast<uint8_t *>(c.q), c.scales, c.q_row, c.s_row, c.s_block},
                static_cast<int>(c.tokens), static_cast<int>(c.width / 8), 0, 1.0f / static_cast<float>(c.width), c.eps,
                c.weight_dtype == SDT_DTYPE_F32};

@@ -134,10 +134,11 @@ static int check_fp8(const sdt_gemm_fp8 &c) {
     for (int64_t s : {rows ? c.as_row : 0, blocks ? c.as_block : 0, panels ? c.ws_row : 0, blocks ? c.ws_block : 0})
         if (s < 0 || s >= most) return fail(SDT_ERR_ARG, "gemm_fp8: scale strides must be in 0 .. 2^32 (got %lld)", (long long)s);
     const int64_t size = c.c_dtype == SDT_DTYPE_F32 ? 4 : 2, kb = (c.K + kFp8Block - 1) / kFp8Block, nb = (c.N + kFp8Block - 1) / kFp8Block;
-    const Stretches out = rows_of(c.c, c.M, c.ldc * size, c.N * size);
+    const Stretches out = rows_of(c.c, c.M, step_bytes(c.M, c.ldc, size), c.N * size);
     if (overlap(out, rows_of(c.a, c.M, c.lda, c.K)) || overlap(out, rows_of(c.w, c.N, c.ldw, c.K)))
         return fail(SDT_ERR_ARG, "gemm_fp8: C and an operand overlap");
-    if (overlap(out, {c.a_scales, c.M, 4 * c.as_row, kb, 4 * c.as_block, 4}) || overlap(out, {c.w_scales, nb, 4 * c.ws_row, kb, 4 * c.ws_block, 4}))
+    if (overlap(out, {c.a_scales, c.M, step_bytes(c.M, c.as_row, 4), kb, step_bytes(kb, c.as_block, 4), 4}) ||
+        overlap(out, {c.w_scales, nb, step_bytes(nb, c.ws_row, 4), kb, step_bytes(kb, c.ws_block, 4), 4}))
         return fail(SDT_ERR_ARG, "gemm_fp8: C and the scales overlap");
     return SDT_OK;
 }

@@ -90,6 +90,9 @@ inline bool overlap(const Stretches &a, const Stretches &b) {
     return false;
 }
 
+// Bytes from one to the next of n elements `stride` apart (a dimension of one never steps: its stride may be anything).
+inline int64_t step_bytes(int64_t n, int64_t stride, int64_t size) { return n > 1 ? stride * size : 0; }
+
 // Rows of `len` bytes.
 inline Stretches rows_of(const void *p, int64_t rows, int64_t step, int64_t len) { return {p, rows, step, 1, 0, len}; }
 
